@@ -18,8 +18,8 @@ _BINDING_NAMES = frozenset((
 
 
 def __getattr__(name):
-    if name == "cfz":
-        return importlib.import_module(".cfz", __name__)
+    if name in ("cfz", "kv8"):
+        return importlib.import_module("." + name, __name__)
     if name in _BINDING_NAMES:
         return getattr(importlib.import_module(".cfz", __name__), name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

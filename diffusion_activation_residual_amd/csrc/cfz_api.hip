@@ -13,6 +13,7 @@
 
 #include "cfz.h"
 #include "cfz_internal.h"
+#include "kv8_internal.h"
 
 namespace {
 
@@ -101,6 +102,9 @@ cfz_status check_buffers(const cfz_desc &d, const cfz_buffers *b, cfz_buffers *u
 }
 
 }  // namespace
+
+// the same error text, for the other sources' entry points
+cfz_status cfz::report(cfz_status st, const char *text) { return fail(st, "%s", text); }
 
 struct cfz_state {
     uint32_t magic;

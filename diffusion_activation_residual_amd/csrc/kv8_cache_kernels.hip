@@ -1,0 +1,688 @@
+// kv8_cache_kernels.hip -- writing and reading the 8-bit paged K/V cache, and picking pages.
+#include "kv8_internal.h"
+
+#include <math.h>
+
+namespace cfz {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <int DT> struct Src;
+template <> struct Src<CFZ_KV8_BF16> { using T = uint16_t; };
+template <> struct Src<CFZ_KV8_F16> { using T = _Float16; };
+template <> struct Src<CFZ_KV8_F32> { using T = float; };
+
+__device__ inline float widen(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
+__device__ inline float widen(_Float16 h) { return (float)h; }
+__device__ inline float widen(float f) { return f; }
+
+template <class T> struct alignas(4 * sizeof(T)) Four { T v[4]; };
+
+template <class T> __device__ inline void load4(const T *p, float (&o)[4])
+{
+    const Four<T> f = *(const Four<T> *)p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        o[i] = widen(f.v[i]);
+}
+
+__device__ inline void narrow(float f, float &o) { o = f; }
+__device__ inline void narrow(float f, _Float16 &o) { o = (_Float16)f; }
+__device__ inline void narrow(float f, uint16_t &o)
+{
+    // nearest even; a cached value is never NaN
+    const uint32_t u = __float_as_uint(f);
+    o = (uint16_t)((u + 0x7fffu + ((u >> 16) & 1u)) >> 16);
+}
+
+__device__ inline double finite_or_zero(double x)
+{
+    return fabs(x) <= 1.7976931348623157e308 ? fabs(x) : 0.0;
+}
+
+// The 8-bit code nearest to x / s (ties to even), as its byte.  rinv = 1 / s in fp64; one
+// correction by the exact remainder makes y the rounded quotient, so a tie is seen as a tie.
+__device__ inline uint32_t encode(double x, double s, double rinv, int fmt)
+{
+    if (!(s > 0.0) || x != x)
+        return 0;
+    const double lim = (fmt == CFZ_KV8_INT8 ? 128.0 : 464.0) * s;
+    x = x > lim ? lim : (x < -lim ? -lim : x);
+    double y = x * rinv;
+    y = fma(fma(-y, s, x), rinv, y);
+    if (fmt == CFZ_KV8_INT8) {
+        y = rint(y);
+        y = y > 127.0 ? 127.0 : (y < -127.0 ? -127.0 : y);
+        return (uint32_t)(int)y & 0xffu;
+    }
+    // (the correction of -0 is +0, but e4m3 keeps the sign of a zero)
+    y = copysign(y > 448.0 ? 448.0 : (y < -448.0 ? -448.0 : y), x);
+    // round to odd at 20 mantissa bits (the low word's bits are kept as one), which fp32 holds
+    // exactly and which leaves every border between codes on its side
+    const int hi = __double2hiint(y) | (__double2loint(y) != 0 ? 1 : 0);
+    const float f = (float)__hiloint2double(hi, 0);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f, f, 0, false) & 0xffu;
+}
+
+__device__ inline float code_value(uint32_t byte, int fmt)
+{
+    if (fmt == CFZ_KV8_INT8)
+        return (float)(int)(int8_t)(uint8_t)byte;
+    return __builtin_amdgcn_cvt_f32_fp8((int)byte, 0);
+}
+
+// The code times 512: a whole number in both formats (e4m3 steps are 2^-9 and up), so that sums of
+// codes are exact in any order.  A byte that is no code (unwritten memory) counts as 0.
+__device__ inline int code_512(uint32_t byte, int fmt)
+{
+    const float f = code_value(byte, fmt) * 512.0f;
+    return f == f ? (int)f : 0;
+}
+
+__device__ inline double block_max(double x, double *red)
+{
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1)
+        x = fmax(x, __shfl_xor(x, d));
+    if ((threadIdx.x & 63) == 0)
+        red[threadIdx.x >> 6] = x;
+    __syncthreads();
+    x = fmax(fmax(red[0], red[1]), fmax(red[2], red[3]));
+    __syncthreads();
+    return x;
+}
+
+// One work-group appends to one page of one head.  Every new element is read once: keys in units of
+// 8 (two groups of 4 that hold whole rotation pairs) kept rotated in fp64 registers, values in
+// 4 tokens x 4 dimensions, transposed in registers and merged into the page's [dim][token]
+// bytes in LDS, so that the page is written in whole 16-byte vectors.  Older tokens are read only where
+// the page keeps some (their codes enter the mean, and change if the scale grows).
+template <class T, int D, int P>
+__global__ __launch_bounds__(kThreads) void kv8_append_kernel(Kv8Cache c, Kv8Batch b, const T *k,
+                                                              const T *v, int64_t k_stride,
+                                                              int64_t v_stride, Kv8Rotation rot,
+                                                              int span)
+{
+    constexpr int U = D / 8;                // key units per token
+    constexpr int NK = P * U / kThreads;    // key units per thread
+    constexpr int NV = P * D / 16 / kThreads ? P * D / 16 / kThreads : 1;
+    constexpr int ROW = P / 4 + 1;          // LDS words per dimension of the value page (padded)
+    __shared__ uint32_t vpage[D * ROW];
+    __shared__ int sums[D];
+    __shared__ double red[4];
+
+    const int tid = threadIdx.x;
+    int64_t g = blockIdx.x;
+    const int at = (int)(g % span);
+    g /= span;
+    const int head = (int)(g % c.heads);
+    const int seq = (int)(g / c.heads);
+
+    int row0, n;
+    kv8_rows(b, seq, row0, n);
+    const int64_t room = (int64_t)b.width * P;
+    const int old = kv8_length(b, seq, room);
+    const int64_t end = old + (int64_t)n < room ? old + (int64_t)n : room;
+    const int64_t first = ((int64_t)(old / P) + at) * P;  // the page's first token
+    if (first >= end || n == 0)
+        return;
+    const int page = kv8_page(c, b, seq, first / P);
+    if (page < 0)
+        return;
+    const int lo = old > first ? (int)(old - first) : 0;               // first new slot
+    const int hi = end - first < P ? (int)(end - first) : P;           // past the last new slot
+    const int64_t src0 = row0 + (first - old);                         // token row of slot 0
+
+    const int64_t ph = (int64_t)page * c.heads + head;
+    uint8_t *kp = c.k + ph * (P * D);
+    uint8_t *vp = c.v + ph * (P * D);
+
+    // ---- keys: load, rotate
+    const int half = rot.cos ? rot.dim / 2 : 0;
+    double x[NK][8];
+    double kmax = 0.0;
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+        const int unit = tid + i * kThreads, slot = unit / U, u = unit % U;
+        const bool split = half && !rot.interleaved && u < half / 4;
+        const int d0 = split ? 4 * u : 8 * u, d1 = split ? half + 4 * u : 8 * u + 4;
+        if (slot < lo || slot >= hi) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                x[i][j] = 0.0;
+            continue;
+        }
+        const T *p = k + (src0 + slot) * k_stride + (int64_t)head * D;
+        float a[4], e[4];
+        load4(p + d0, a);
+        load4(p + d1, e);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[i][j] = a[j];
+            x[i][4 + j] = e[j];
+        }
+        if (8 * u < 2 * half) {
+            int64_t pos = rot.pos ? (int64_t)rot.pos[src0 + slot] : first + slot;
+            pos = pos < 0 ? 0 : (pos >= rot.rows ? rot.rows - 1 : pos);
+            // angles 4u .. 4u + 3 in either order of the pairs
+            const float4 cs = *(const float4 *)(rot.cos + pos * half + 4 * u);
+            const float4 sn = *(const float4 *)(rot.sin + pos * half + 4 * u);
+            const float cc[4] = {cs.x, cs.y, cs.z, cs.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int p0 = split ? j : 2 * j, p1 = split ? 4 + j : 2 * j + 1;
+                // products of two fp32 values are exact in fp64
+                const double y0 = x[i][p0], y1 = x[i][p1], co = cc[j], si = ss[j];
+                const double r0 = fma(y0, co, -(y1 * si)), r1 = fma(y0, si, y1 * co);
+                if (split) {
+                    x[i][j] = r0;
+                    x[i][4 + j] = r1;
+                } else {
+                    x[i][2 * j] = r0;
+                    x[i][2 * j + 1] = r1;
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            kmax = fmax(kmax, finite_or_zero(x[i][j]));
+    }
+
+    // ---- values: 4 tokens x 4 dimensions per unit
+    float w[NV][4][4];  // [unit][token][dimension]
+    double vmax = 0.0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int unit = tid + i * kThreads, tq = unit / (D / 4), dq = unit % (D / 4);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int slot = tq * 4 + t;
+            if (slot >= lo && slot < hi) {
+                load4(v + (src0 + slot) * v_stride + (int64_t)head * D + dq * 4, w[i][t]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    w[i][t][j] = 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                vmax = fmax(vmax, finite_or_zero(w[i][t][j]));
+        }
+    }
+    const double qmax = c.fmt == CFZ_KV8_INT8 ? 127.0 : 448.0;
+    kmax = block_max(kmax, red);
+    vmax = block_max(vmax, red);
+    const float kprior = lo > 0 ? c.ks[ph] : 0.0f, vprior = lo > 0 ? c.vs[ph] : 0.0f;
+    const float kscale = fmaxf(kprior, (float)(kmax / qmax));
+    const float vscale = fmaxf(vprior, (float)(vmax / qmax));
+    const bool kgrown = lo > 0 && kscale > kprior, vgrown = lo > 0 && vscale > vprior;
+    const double krinv = 1.0 / (double)kscale, vrinv = 1.0 / (double)vscale;
+    __syncthreads();  // every thread has read the old scales
+    if (tid == 0) {
+        c.ks[ph] = kscale;
+        c.vs[ph] = vscale;
+    }
+    if (c.km && tid < D)
+        sums[tid] = 0;
+
+    // ---- the value page as it is, where bytes of it stay
+    if (lo > 0 || hi < P) {
+        for (int i = tid; i < D * P / 16; i += kThreads) {
+            const uint4 q = ((const uint4 *)vp)[i];
+            uint32_t *o = vpage + (i * 4 / (P / 4)) * ROW + i * 4 % (P / 4);
+            o[0] = q.x, o[1] = q.y, o[2] = q.z, o[3] = q.w;
+        }
+    }
+    __syncthreads();
+
+    // ---- key codes (all units of a thread are of the same dimensions, since U divides kThreads)
+    int acc[8] = {};
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+        const int unit = tid + i * kThreads, slot = unit / U, u = unit % U;
+        const bool split = half && !rot.interleaved && u < half / 4;
+        const int d0 = split ? 4 * u : 8 * u, d1 = split ? half + 4 * u : 8 * u + 4;
+        if (slot >= hi || (slot < lo && !kgrown && !c.km))
+            continue;
+        uint32_t *p0 = (uint32_t *)(kp + slot * D + d0), *p1 = (uint32_t *)(kp + slot * D + d1);
+        uint32_t w0, w1;
+        if (slot >= lo) {
+            w0 = w1 = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                w0 |= encode(x[i][j], kscale, krinv, c.fmt) << (8 * j);
+                w1 |= encode(x[i][4 + j], kscale, krinv, c.fmt) << (8 * j);
+            }
+            *p0 = w0;
+            *p1 = w1;
+        } else {
+            w0 = *p0;
+            w1 = *p1;
+            if (kgrown) {
+                uint32_t n0 = 0, n1 = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const double o0 = code_value((w0 >> (8 * j)) & 0xff, c.fmt);
+                    const double o1 = code_value((w1 >> (8 * j)) & 0xff, c.fmt);
+                    n0 |= encode(o0 * kprior, kscale, krinv, c.fmt) << (8 * j);
+                    n1 |= encode(o1 * kprior, kscale, krinv, c.fmt) << (8 * j);
+                }
+                w0 = n0;
+                w1 = n1;
+                *p0 = w0;
+                *p1 = w1;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            acc[j] += code_512((w0 >> (8 * j)) & 0xff, c.fmt);
+            acc[4 + j] += code_512((w1 >> (8 * j)) & 0xff, c.fmt);
+        }
+    }
+    if (c.km) {
+        const int u = tid % U;
+        const bool split = half && !rot.interleaved && u < half / 4;
+        const int d0 = split ? 4 * u : 8 * u, d1 = split ? half + 4 * u : 8 * u + 4;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            atomicAdd(&sums[d0 + j], acc[j]);
+            atomicAdd(&sums[d1 + j], acc[4 + j]);
+        }
+    }
+
+    // ---- value codes into the page in LDS
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int unit = tid + i * kThreads, tq = unit / (D / 4), dq = unit % (D / 4);
+        if (tq >= P / 4 || (tq * 4 >= hi) || (tq * 4 + 4 <= lo && !vgrown))
+            continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t *o = vpage + (dq * 4 + j) * ROW + tq;
+            const uint32_t was = *o;
+            uint32_t now = 0;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int slot = tq * 4 + t;
+                const uint32_t byte = (was >> (8 * t)) & 0xff;
+                uint32_t e = byte;
+                if (slot >= lo && slot < hi)
+                    e = encode(w[i][t][j], vscale, vrinv, c.fmt);
+                else if (slot < lo && vgrown)
+                    e = encode((double)code_value(byte, c.fmt) * vprior, vscale, vrinv, c.fmt);
+                now |= e << (8 * t);
+            }
+            *o = now;
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < D * P / 16; i += kThreads) {
+        const uint32_t *o = vpage + (i * 4 / (P / 4)) * ROW + i * 4 % (P / 4);
+        ((uint4 *)vp)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    if (c.km && tid < D)
+        c.km[ph * D + tid] = (float)((double)sums[tid] / 512.0 * (double)kscale / (double)hi);
+}
+
+// Reads one page of one head back: keys straight, values through LDS (their codes are dimension-major),
+// rows written in vectors of 4 values.
+template <class T, int D, int P>
+__global__ __launch_bounds__(kThreads) void kv8_gather_kernel(Kv8Cache c, Kv8Batch b, T *k, T *v,
+                                                              int span)
+{
+    constexpr int ROW = P / 4 + 1;
+    __shared__ uint32_t vpage[D * ROW];
+    const int tid = threadIdx.x;
+    int64_t g = blockIdx.x;
+    const int at = (int)(g % span);
+    g /= span;
+    const int head = (int)(g % c.heads);
+    const int seq = (int)(g / c.heads);
+    int row0, n;
+    kv8_rows(b, seq, row0, n);
+    const int64_t room = (int64_t)b.width * P;
+    const int64_t old = b.len[seq] < 0 ? 0 : b.len[seq];
+    const int64_t first = (old / P + at) * P;
+    if (first >= old + n || n == 0)
+        return;
+    const int lo = old > first ? (int)(old - first) : 0;
+    const int hi = old + n - first < P ? (int)(old + n - first) : P;
+    const int page = first < room ? kv8_page(c, b, seq, first / P) : -1;
+    const int64_t ph = (int64_t)page * c.heads + head;
+    const int64_t dst0 = row0 + (first - old);
+    if (v && page >= 0) {
+        const uint4 *vp = (const uint4 *)(c.v + ph * (P * D));
+        for (int i = tid; i < D * P / 16; i += kThreads) {
+            const uint4 q = vp[i];
+            uint32_t *o = vpage + (i * 4 / (P / 4)) * ROW + i * 4 % (P / 4);
+            o[0] = q.x, o[1] = q.y, o[2] = q.z, o[3] = q.w;
+        }
+    }
+    const float ks = page >= 0 ? c.ks[ph] : 0.0f, vs = page >= 0 ? c.vs[ph] : 0.0f;
+    if (k) {
+        for (int i = tid; i < P * D / 4; i += kThreads) {
+            const int slot = i / (D / 4), d = i % (D / 4) * 4;
+            if (slot < lo || slot >= hi)
+                continue;
+            const uint32_t w = page >= 0 ? *(const uint32_t *)(c.k + ph * (P * D) + slot * D + d) : 0;
+            Four<T> o;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                narrow(page >= 0 ? code_value((w >> (8 * j)) & 0xff, c.fmt) * ks : 0.0f, o.v[j]);
+            *(Four<T> *)(k + ((dst0 + slot) * c.heads + head) * D + d) = o;
+        }
+    }
+    if (!v)
+        return;
+    __syncthreads();
+    for (int i = tid; i < P * D / 16; i += kThreads) {
+        const int tq = i / (D / 4), d = i % (D / 4) * 4;
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w[j] = page >= 0 ? vpage[(d + j) * ROW + tq] : 0;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int slot = tq * 4 + t;
+            if (slot < lo || slot >= hi)
+                continue;
+            Four<T> o;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                narrow(page >= 0 ? code_value((w[j] >> (8 * t)) & 0xff, c.fmt) * vs : 0.0f, o.v[j]);
+            *(Four<T> *)(v + ((dst0 + slot) * c.heads + head) * D + d) = o;
+        }
+    }
+}
+
+// ---- picking pages
+
+// The order of scores as unsigned numbers; NaN below everything (a page that cannot be picked is 0).
+__device__ inline uint64_t order_key(double s)
+{
+    if (s != s)
+        return 1;
+    s += 0.0;  // -0 counts as 0
+    const uint64_t u = (uint64_t)__double_as_longlong(s);
+    return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+}
+
+// Scores of one query block and KV head against the means of up to kScorePages pages.  The block's
+// queries are summed in fp64 (sums of bf16 or fp16 values; 16 bits more than fp32 where it matters: two
+// pages whose scores differ in the last bit of fp32 keep their order), then each wave takes
+// pages in turn, one lane per D / 64 dimensions.
+constexpr int kScorePages = 64;
+
+template <int D>
+__global__ __launch_bounds__(kThreads) void kv8_score_kernel(Kv8Cache c, Kv8Batch b, Kv8Select a,
+                                                             int units, int stride, int chunks)
+{
+    __shared__ double qs[4][D];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int64_t g = blockIdx.x;
+    const int chunk = (int)(g % chunks);
+    g /= chunks;
+    const int64_t list = g;  // (seq, unit, head)
+    const int head = (int)(g % c.heads);
+    g /= c.heads;
+    const int unit = (int)(g % units);
+    const int seq = (int)(g / units);
+    int row0, n;
+    kv8_rows(b, seq, row0, n);
+    const int len = kv8_length(b, seq, a.max_kv);
+    const int64_t q0 = (int64_t)unit * a.q_block;
+    if (q0 >= n)
+        return;
+    const int64_t q1 = q0 + a.q_block < n ? q0 + a.q_block : n;
+    const int64_t end = a.causal ? (int64_t)len - n + q1 : len;
+    const int seen = end <= 0 ? 0 : (int)((end + c.page - 1) >> c.log2page);
+    if (chunk * kScorePages >= seen)
+        return;
+
+    constexpr int E = D / 64;
+    double sum[E] = {};
+    const int rows = (int)(q1 - q0) * a.group;
+    for (int r = wave; r < rows; r += 4) {
+        const int64_t at = (row0 + q0 + r / a.group) * a.q_stride +
+                           ((int64_t)head * a.group + r % a.group) * D + lane * E;
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+            sum[j] += a.f16 ? (float)((const _Float16 *)a.q)[at + j]
+                            : widen(((const uint16_t *)a.q)[at + j]);
+    }
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+        qs[wave][lane * E + j] = sum[j];
+    __syncthreads();
+    double q[E];
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+        q[j] = (qs[0][lane * E + j] + qs[1][lane * E + j]) +
+               (qs[2][lane * E + j] + qs[3][lane * E + j]);
+    double *out = a.ws + list * stride;
+    for (int i = wave; i < kScorePages; i += 4) {
+        const int p = chunk * kScorePages + i;
+        if (p >= seen)
+            break;
+        const int page = kv8_page(c, b, seq, p);
+        double s = 0.0;
+        if (page >= 0) {
+            const float *m = c.km + ((int64_t)page * c.heads + head) * D + lane * E;
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+                s = fma(q[j], (double)m[j], s);
+        }
+#pragma unroll
+        for (int d = 32; d >= 1; d >>= 1)
+            s += __shfl_xor(s, d);
+        uint64_t key = order_key(s);
+        if (page < 0)
+            key = 0;
+        else if (p < a.first || p >= seen - a.last)
+            key = ~0ull;
+        if (lane == 0)
+            out[p] = __longlong_as_double((long long)key);
+    }
+}
+
+// The `count` largest keys of one list: the threshold is found 8 bits at a time by counting
+// (the same work whatever the keys), then the pages above it and, in index order, as many at it as are left
+// are written in ascending order.
+__global__ __launch_bounds__(kThreads) void kv8_pick_kernel(Kv8Cache c, Kv8Batch b, Kv8Select a,
+                                                            int units, int stride)
+{
+    __shared__ int hist[256];
+    __shared__ int scan[4][2];
+    __shared__ int pick[2];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int64_t g = blockIdx.x;
+    const int64_t list = g;
+    g /= c.heads;
+    const int unit = (int)(g % units);
+    const int seq = (int)(g / units);
+    int row0, n;
+    kv8_rows(b, seq, row0, n);
+    const int len = kv8_length(b, seq, a.max_kv);
+    int32_t *out = a.blocks + list * a.count;
+    const int64_t q0 = (int64_t)unit * a.q_block;
+    int seen = 0;
+    if (q0 < n) {
+        const int64_t q1 = q0 + a.q_block < n ? q0 + a.q_block : n;
+        const int64_t end = a.causal ? (int64_t)len - n + q1 : len;
+        seen = end <= 0 ? 0 : (int)((end + c.page - 1) >> c.log2page);
+    }
+    const uint64_t *keys = (const uint64_t *)(a.ws + list * stride);
+
+    uint64_t prefix = 0;
+    int need = a.count;  // how many of the keys that match the prefix so far are wanted
+    if (seen > a.count) {
+        for (int shift = 56; shift >= 0; shift -= 8) {
+            hist[tid] = 0;
+            __syncthreads();
+            const uint64_t mask = shift == 56 ? 0 : ~0ull << (shift + 8);
+            for (int i = tid; i < seen; i += kThreads) {
+                const uint64_t key = keys[i];
+                if ((key & mask) == prefix)
+                    atomicAdd(&hist[(key >> shift) & 255], 1);
+            }
+            __syncthreads();
+            // how many keys lie in the digits above this thread's
+            const int digit = 255 - tid, mine = hist[digit];
+            int incl = mine;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const int o = __shfl_up(incl, d);
+                incl += lane >= d ? o : 0;
+            }
+            if (lane == 63)
+                scan[wave][0] = incl;
+            __syncthreads();
+            for (int w = 0; w < wave; ++w)
+                incl += scan[w][0];
+            if (incl >= need && incl - mine < need) {
+                pick[0] = digit;
+                pick[1] = need - (incl - mine);
+            }
+            __syncthreads();
+            prefix |= (uint64_t)pick[0] << shift;
+            need = pick[1];
+            __syncthreads();
+        }
+    }
+    // threshold = prefix; pages without a key (0) are never picked
+    int done = 0, ties = 0;  // written so far, ties met so far
+    for (int base = 0; base < seen; base += kThreads) {
+        const int i = base + tid;
+        const uint64_t key = i < seen ? keys[i] : 0;
+        const bool tie = key != 0 && seen > a.count && key == prefix;
+        const bool over = key != 0 && (seen <= a.count || key > prefix);
+        // ranks among the ties first, since only the first `need` of them are taken
+        const uint64_t tb = __ballot(tie);
+        if (lane == 0)
+            scan[wave][0] = __popcll(tb);
+        __syncthreads();
+        int before = ties, all = 0;
+        for (int w = 0; w < 4; ++w) {
+            before += w < wave ? scan[w][0] : 0;
+            all += scan[w][0];
+        }
+        const bool take = over || (tie && before + __popcll(tb & ((1ull << lane) - 1)) < need);
+        ties += all;
+        const uint64_t kb = __ballot(take);
+        if (lane == 0)
+            scan[wave][1] = __popcll(kb);
+        __syncthreads();
+        int at = done;
+        all = 0;
+        for (int w = 0; w < 4; ++w) {
+            at += w < wave ? scan[w][1] : 0;
+            all += scan[w][1];
+        }
+        if (take)
+            out[at + __popcll(kb & ((1ull << lane) - 1))] = i;
+        done += all;
+        __syncthreads();
+    }
+    for (int i = done + tid; i < a.count; i += kThreads)
+        out[i] = -1;
+}
+
+// Work-groups of a page-wise launch over `span` pages per sequence, 0 if there is nothing to do.
+int64_t page_groups(const Kv8Cache &c, const Kv8Batch &b, int &span)
+{
+    // a run of max_rows tokens touches one page more than it fills when it starts inside a page
+    const int64_t pages = (b.max_rows + c.page - 1) / c.page + 1;
+    span = (int)pages;
+    return pages * c.heads * b.batch;
+}
+
+template <class T>
+hipError_t append_as(const Kv8Cache &c, const Kv8Batch &b, const void *k, const void *v,
+                     int64_t ks, int64_t vs, const Kv8Rotation &rot, hipStream_t st)
+{
+    int span;
+    const dim3 grid((unsigned)page_groups(c, b, span));
+#define CFZ_KV8_CASE(D, P)                                                                         \
+    if (c.dim == D && c.page == P)                                                                 \
+        kv8_append_kernel<T, D, P><<<grid, kThreads, 0, st>>>(c, b, (const T *)k, (const T *)v, ks, \
+                                                              vs, rot, span);
+    CFZ_KV8_CASE(64, 32)
+    CFZ_KV8_CASE(64, 64)
+    CFZ_KV8_CASE(64, 128)
+    CFZ_KV8_CASE(128, 32)
+    CFZ_KV8_CASE(128, 64)
+    CFZ_KV8_CASE(128, 128)
+#undef CFZ_KV8_CASE
+    return hipGetLastError();
+}
+
+template <class T>
+hipError_t gather_as(const Kv8Cache &c, const Kv8Batch &b, void *k, void *v, hipStream_t st)
+{
+    int span;
+    const dim3 grid((unsigned)page_groups(c, b, span));
+#define CFZ_KV8_CASE(D, P)                                                                         \
+    if (c.dim == D && c.page == P)                                                                 \
+        kv8_gather_kernel<T, D, P><<<grid, kThreads, 0, st>>>(c, b, (T *)k, (T *)v, span);
+    CFZ_KV8_CASE(64, 32)
+    CFZ_KV8_CASE(64, 64)
+    CFZ_KV8_CASE(64, 128)
+    CFZ_KV8_CASE(128, 32)
+    CFZ_KV8_CASE(128, 64)
+    CFZ_KV8_CASE(128, 128)
+#undef CFZ_KV8_CASE
+    return hipGetLastError();
+}
+
+int64_t select_pages(const Kv8Cache &c, int64_t max_kv) { return (max_kv + c.page - 1) / c.page; }
+
+}  // namespace
+
+hipError_t launch_kv8_append(const Kv8Cache &c, const Kv8Batch &b, int dtype, const void *k,
+                             const void *v, int64_t k_stride, int64_t v_stride,
+                             const Kv8Rotation &rot, hipStream_t st)
+{
+    switch (dtype) {
+    case CFZ_KV8_BF16: return append_as<uint16_t>(c, b, k, v, k_stride, v_stride, rot, st);
+    case CFZ_KV8_F16: return append_as<_Float16>(c, b, k, v, k_stride, v_stride, rot, st);
+    default: return append_as<float>(c, b, k, v, k_stride, v_stride, rot, st);
+    }
+}
+
+hipError_t launch_kv8_gather(const Kv8Cache &c, const Kv8Batch &b, int dtype, void *k, void *v,
+                             hipStream_t st)
+{
+    switch (dtype) {
+    case CFZ_KV8_BF16: return gather_as<uint16_t>(c, b, k, v, st);
+    case CFZ_KV8_F16: return gather_as<_Float16>(c, b, k, v, st);
+    default: return gather_as<float>(c, b, k, v, st);
+    }
+}
+
+size_t kv8_select_workspace_bytes(const Kv8Cache &c, const Kv8Batch &b, int64_t max_kv,
+                                  int64_t q_block)
+{
+    const int64_t units = (b.max_rows + q_block - 1) / q_block;
+    return (size_t)(units * c.heads * b.batch * select_pages(c, max_kv)) * sizeof(double);
+}
+
+hipError_t launch_kv8_select(const Kv8Cache &c, const Kv8Batch &b, const Kv8Select &a,
+                             hipStream_t st)
+{
+    const int units = (int)((b.max_rows + a.q_block - 1) / a.q_block);
+    const int stride = (int)select_pages(c, a.max_kv);
+    const int chunks = (stride + kScorePages - 1) / kScorePages;
+    const int64_t lists = (int64_t)units * c.heads * b.batch;
+    if (chunks > 0) {
+        const dim3 grid((unsigned)(lists * chunks));
+        if (c.dim == 64)
+            kv8_score_kernel<64><<<grid, kThreads, 0, st>>>(c, b, a, units, stride, chunks);
+        else
+            kv8_score_kernel<128><<<grid, kThreads, 0, st>>>(c, b, a, units, stride, chunks);
+    }
+    kv8_pick_kernel<<<dim3((unsigned)lists), kThreads, 0, st>>>(c, b, a, units, stride);
+    return hipGetLastError();
+}
+
+}  // namespace cfz

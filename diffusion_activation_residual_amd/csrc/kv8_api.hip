@@ -129,15 +129,6 @@ cfz_status check_queries(const cfz::Kv8Cache &c, const cfz::Kv8Batch &b, int32_t
     return CFZ_OK;
 }
 
-size_t attend_bytes(const cfz::Kv8Cache &c, const cfz::Kv8Batch &b, int32_t q_heads,
-                    const cfz::Kv8Plan &p)
-{
-    if (p.splits <= 1)
-        return 0;
-    return (size_t)p.splits * (size_t)b.tokens * (size_t)q_heads * (size_t)(c.dim + 4) *
-           sizeof(float);
-}
-
 cfz_status check_workspace(const void *ws, size_t have, size_t need)
 {
     if (need == 0)
@@ -232,7 +223,7 @@ size_t cfz_kv8_attend_workspace_bytes(const cfz_kv8_cache *cache, const cfz_kv8_
         bound_rows(&b);
     const cfz::Kv8Plan p = cfz::kv8_plan(c, b, q_heads, max_kv, blocks != nullptr,
                                          blocks ? blocks->q_block : 1, blocks ? blocks->count : 0);
-    return attend_bytes(c, b, q_heads, p);
+    return (size_t)p.ws_bytes;
 }
 
 cfz_status cfz_kv8_attend(const cfz_kv8_cache *cache, const cfz_kv8_batch *batch,
@@ -263,9 +254,8 @@ cfz_status cfz_kv8_attend(const cfz_kv8_cache *cache, const cfz_kv8_batch *batch
         return fail(CFZ_ERR_ALIGN, "q and out must be 16-byte, lse and lists 4-byte aligned");
     const cfz::Kv8Plan p = cfz::kv8_plan(c, b, q_heads, max_kv, blocks != nullptr,
                                          blocks ? blocks->q_block : 1, blocks ? blocks->count : 0);
-    CFZ_TRY(check_groups((double)p.units * p.tiles * c.heads * b.batch * p.splits));
-    CFZ_TRY(check_groups((double)b.max_rows * q_heads * b.batch + b.batch));
-    CFZ_TRY(check_workspace(workspace, ws_bytes, attend_bytes(c, b, q_heads, p)));
+    CFZ_TRY(check_groups(p.whole));
+    CFZ_TRY(check_workspace(workspace, ws_bytes, (size_t)p.ws_bytes));
     cfz::Kv8Attend a;
     a.q = q;
     a.out = out;

@@ -31,11 +31,18 @@ typedef float f16v __attribute__((ext_vector_type(16)));
 typedef float f2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 
-constexpr float kLift = 10.0f;
+#ifndef KLIFT
+#define KLIFT 6
+#endif
+constexpr float kLift = KLIFT;
 constexpr float kSlack = 5.0f;  // weights reach 2^(kLift + kSlack) = 2^15 < 65504
+constexpr float kLimit = 60000.0f;
 constexpr float kNone = -3.0e38f;
-constexpr float kTinyScale = 0x1p-100f;
+constexpr float kTiny = -100.0f;  // log2 of the value scale up to which codes count as zeros
 constexpr int kBlock = 64;  // keys per step
+constexpr int kMaxItems = 1023;  // tiles per head whose steps a work-group counts
+constexpr int kPrefixWords = kMaxItems + 1;
+constexpr int kCutWords = 4096;  // of the workspace: a Cut for each of at most 1024 work-groups
 
 __device__ inline float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -64,48 +71,19 @@ template <int FMT> __device__ inline h8 to_half8(uint32_t w0, uint32_t w1)
 
 __device__ inline h2 pack(float a, float b) { return __builtin_convertvector((f2){a, b}, h2); }
 
-// Which rows a work-group has: rows r0 .. of the rows (query, shared head) of one query block.
+// A tile: rows r0 .. of the rows (query, shared head) of one query block, and one KV head.
 struct Tile {
-    int seq, head, split;
+    int seq, head;
     int row0;      // token row of the sequence's first query
     int n;         // its queries
     int len;       // its keys
     int q0;        // first query of the block
     int rows;      // rows of the block, (queries in it) * group
     int r0;        // first row of the tile
+    int reach_min, reach_max;  // keys that its first and its last row see
+    int steps;     // of kBlock keys
     const int32_t *list;  // the block's pages or null
 };
-
-template <int BM>
-__device__ inline bool find_tile(const Kv8Cache &c, const Kv8Batch &b, const Kv8Attend &a,
-                                 const Kv8Plan &p, Tile &t)
-{
-    // Consecutive work-groups go round the 8 XCDs; give each XCD consecutive tiles, so that the
-    // tiles that read the same keys share an L2.
-    const unsigned total = (unsigned)p.groups, id = blockIdx.x;
-    const unsigned q = total / 8, r = total % 8, x = id % 8;
-    unsigned g = x * q + (x < r ? x : r) + id / 8;
-    const unsigned tile = g % (unsigned)p.tiles;
-    g /= (unsigned)p.tiles;
-    const unsigned unit = g % (unsigned)p.units;
-    g /= (unsigned)p.units;
-    t.split = g % (unsigned)p.splits;
-    g /= (unsigned)p.splits;
-    t.head = g % (unsigned)c.heads;
-    t.seq = g / (unsigned)c.heads;
-    kv8_rows(b, t.seq, t.row0, t.n);
-    t.len = kv8_length(b, t.seq, a.max_kv);
-    const int64_t q0 = (int64_t)unit * a.q_block;
-    if (q0 >= t.n)
-        return false;
-    t.q0 = (int)q0;
-    const int64_t nq = t.n - q0 < a.q_block ? t.n - q0 : a.q_block;
-    t.rows = (int)(nq * a.group);
-    t.r0 = tile * BM;
-    t.list = a.blocks ? a.blocks + (((int64_t)t.seq * p.units + unit) * c.heads + t.head) * a.count
-                      : nullptr;
-    return t.r0 < t.rows;
-}
 
 // Keys that query qi of the sequence sees: the tokens below this.
 __device__ inline int reach(const Tile &t, int causal, int qi)
@@ -116,10 +94,184 @@ __device__ inline int reach(const Tile &t, int causal, int qi)
     return e < 0 ? 0 : (int)e;
 }
 
+// The tile `item` (query blocks and row tiles of one sequence after the other) of one KV head; false
+// where the sequence has no such rows.
+template <int BM>
+__device__ inline bool find_tile(const Kv8Cache &c, const Kv8Batch &b, const Kv8Attend &a,
+                                 const Kv8Plan &p, int item, int head, Tile &t)
+{
+    const int tile = item % p.tiles;
+    item /= p.tiles;
+    const int unit = item % p.units;
+    t.seq = item / p.units;
+    t.head = head;
+    kv8_rows(b, t.seq, t.row0, t.n);
+    t.len = kv8_length(b, t.seq, a.max_kv);
+    const int64_t q0 = (int64_t)unit * a.q_block;
+    if (q0 >= t.n)
+        return false;
+    t.q0 = (int)q0;
+    const int64_t nq = t.n - q0 < a.q_block ? t.n - q0 : a.q_block;
+    t.rows = (int)(nq * a.group);
+    t.r0 = tile * BM;
+    if (t.r0 >= t.rows)
+        return false;
+    t.list = a.blocks ? a.blocks + (((int64_t)t.seq * p.units + unit) * c.heads + head) * a.count
+                      : nullptr;
+    const int last = t.r0 + BM < t.rows ? t.r0 + BM - 1 : t.rows - 1;
+    t.reach_min = reach(t, a.causal, t.q0 + t.r0 / a.group);
+    t.reach_max = reach(t, a.causal, t.q0 + last / a.group);
+    const int keys = t.list ? a.count << c.log2page : t.reach_max;
+    t.steps = (keys + kBlock - 1) / kBlock;
+    return true;
+}
+
+// Consecutive work-groups go round the 8 XCDs; give each XCD consecutive numbers, so that the
+// tiles that read the same keys share an L2.
+__device__ inline uint32_t by_xcd(uint32_t total)
+{
+    const uint32_t q = total / 8, r = total % 8, x = blockIdx.x % 8;
+    return x * q + (x < r ? x : r) + blockIdx.x / 8;
+}
+
+// The steps of all tiles of all heads, laid end to end, are cut into p.groups equal runs, one per
+// work-group: with tiles of different cost (ragged or causal sequences) or a number of tiles
+// that does not fill the chip evenly, all work-groups end together.  prefix[i] is the number of
+// steps before item i of one head (a tile without keys counts as one step: its rows are
+// written); every work-group computes it from the lengths on the device.
+template <int T, int BM>
+__device__ inline void count_steps(const Kv8Cache &c, const Kv8Batch &b, const Kv8Attend &a,
+                                   const Kv8Plan &p, int *prefix, int *waves)
+{
+    const int tid = threadIdx.x, per = (p.items + T - 1) / T;
+    int sum = 0;
+    for (int i = tid * per; i < (tid + 1) * per && i < p.items; ++i) {
+        Tile t;
+        const int n = !find_tile<BM>(c, b, a, p, i, 0, t) ? 0 : (t.steps > 0 ? t.steps : 1);
+        prefix[i] = sum;
+        sum += n;
+    }
+    int incl = sum;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(incl, d);
+        incl += (tid & 63) >= d ? o : 0;
+    }
+    if ((tid & 63) == 63)
+        waves[tid >> 6] = incl;
+    __syncthreads();
+    int before = incl - sum, all = 0;
+    for (int w = 0; w < T / 64; ++w) {
+        before += w < tid / 64 ? waves[w] : 0;
+        all += waves[w];
+    }
+    for (int i = tid * per; i < (tid + 1) * per && i < p.items; ++i)
+        prefix[i] += before;
+    if (tid == 0)
+        prefix[p.items] = all;
+    __syncthreads();
+}
+
+// The last item that starts at or before step y (items without steps start where the next does).
+__device__ inline int item_at(const int *prefix, int items, int y)
+{
+    int lo = 0, hi = items;  // prefix[lo] <= y < prefix[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (prefix[mid] <= y)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// A run of steps s0 .. s1 of one tile, and where its sums go: to the output if it is the whole tile,
+// else to the work-group's first slot (the tile began in an earlier run) or second.
+struct Run {
+    uint32_t at, end;  // of the work-group, in steps of all tiles
+    uint32_t each;     // steps of a work-group, one more for the first `extra` of them
+    uint32_t extra, groups;
+    int s0, s1;
+    int slot;          // -1: the output
+};
+
+__device__ inline uint32_t run_start(const Run &r, uint32_t w)
+{
+    return r.each * w + (w < r.extra ? w : r.extra);
+}
+
+// The work-group that has step x.
+__device__ inline uint32_t run_of(const Run &r, uint32_t x)
+{
+    const uint32_t head = (r.each + 1) * r.extra;
+    return x < head ? x / (r.each + 1) : r.extra + (x - head) / r.each;
+}
+
+// A tile that a work-group begins and `more` later ones go on with (0: none), for the join.
+struct Cut {
+    int item, head, more, unused;
+};
+
+// The work-group's next run of steps, false when it is done.
+template <int BM>
+__device__ inline bool next_run(const Kv8Cache &c, const Kv8Batch &b, const Kv8Attend &a,
+                                const Kv8Plan &p, const int *prefix, uint32_t w, Run &r, Tile &t)
+{
+    if (r.at >= r.end)
+        return false;
+    if (!p.joined) {  // one work-group, one tile
+        r.at = r.end;
+        r.slot = -1;
+        r.s0 = 0;
+        const uint32_t items = p.items;
+        if (!find_tile<BM>(c, b, a, p, (int)(w % items), (int)(w / items), t))
+            return false;
+        r.s1 = t.steps;
+        return true;
+    }
+    const uint32_t all = __builtin_amdgcn_readfirstlane(prefix[p.items]);
+    const int head = (int)(r.at / all), y = (int)(r.at % all);
+    const int item = __builtin_amdgcn_readfirstlane(item_at(prefix, p.items, y));
+    const int from = __builtin_amdgcn_readfirstlane(prefix[item]);
+    const int cost = __builtin_amdgcn_readfirstlane(prefix[item + 1]) - from;
+    find_tile<BM>(c, b, a, p, item, head, t);
+    r.s0 = y - from;
+    r.s1 = (int)(r.end - r.at) < cost - r.s0 ? r.s0 + (int)(r.end - r.at) : cost;
+    r.slot = r.s0 > 0 ? 2 * (int)w : (r.s1 < cost ? 2 * (int)w + 1 : -1);
+    if (r.slot == 2 * (int)w + 1 && threadIdx.x == 0)
+        ((Cut *)a.ws)[w] = Cut{item, head, (int)(run_of(r, r.at + cost - 1) - w), 0};
+    r.at += r.s1 - r.s0;
+    r.s1 = r.s1 < t.steps ? r.s1 : t.steps;
+    return true;
+}
+
+template <int T, int BM>
+__device__ inline Run first_run(const Kv8Cache &c, const Kv8Batch &b, const Kv8Attend &a,
+                                const Kv8Plan &p, int *prefix, int *waves, uint32_t w)
+{
+    Run r = {0, 1, 1, 0, 1, 0, 0, -1};
+    if (p.joined) {
+        count_steps<T, BM>(c, b, a, p, prefix, waves);
+        const uint32_t total = (uint32_t)prefix[p.items] * (uint32_t)c.heads;  // below 2^31
+        r.groups = total < (uint32_t)p.groups ? total : (uint32_t)p.groups;
+        r.at = r.end = 0;
+        if (w < r.groups) {
+            r.each = total / r.groups;
+            r.extra = total % r.groups;
+            r.at = run_start(r, w);
+            r.end = run_start(r, w + 1);
+        }
+        if (threadIdx.x == 0)
+            ((Cut *)a.ws)[w] = Cut{0, 0, 0, 0};
+    }
+    return r;
+}
+
 // Half a step: 32 tokens, all in one page (or in none: page < 0).
 struct Half {
     int page, tok;
-    float kscale, vscale;
+    float kscale, add;  // K's scale; log2 of V's
 };
 
 // The half that starts at position `vt` of the tile's keys: of the sequence itself, or of its listed
@@ -135,30 +287,36 @@ __device__ inline Half find_half(const Kv8Cache &c, const Kv8Batch &b, const Kv8
         logical = -1;
     h.tok = logical * c.page + (vt & (c.page - 1));
     h.page = logical >= 0 && h.tok < reach_max ? kv8_page(c, b, t.seq, logical) : -1;
-    h.page = __builtin_amdgcn_readfirstlane(h.page);
-    h.kscale = h.vscale = 0.0f;
-    if (h.page >= 0) {
-        const int64_t ph = (int64_t)h.page * c.heads + t.head;
-        h.kscale = c.ks[ph];
-        h.vscale = c.vs[ph];
-    }
+    h.kscale = 0.0f;
+    h.add = kTiny;
     return h;
 }
 
-// What a lane needs of a half: y = acc * mul + add, and the weight's share of the denominator.
+__device__ inline void find_scales(const Kv8Cache &c, const Tile &t, Half &h)
+{
+    if (h.page >= 0) {
+        const int64_t ph = (int64_t)h.page * c.heads + t.head;
+        h.kscale = c.ks[ph];
+        const float z = c.vs[ph];
+        h.add = z > 0x1p-100f ? __builtin_amdgcn_logf(z) : kTiny;  // (no subnormal gets there)
+    }
+}
+
+// The value codes of a half count as zeros: a scale of 2^-100 or less (0 above all).
+__device__ inline bool flushed(const Half &h) { return !(h.add > kTiny); }
+
+// What a lane needs of a half: y = acc * mul + add, and the weight's share of the denominator, 2^-add.
 struct Factor {
     float mul, add, back;
-    bool flush;  // the value codes count as zeros
 };
 
 __device__ inline Factor factor(const Half &h, float qmul)
 {
     Factor f;
-    f.flush = !(h.vscale >= kTinyScale);
-    const float z = f.flush ? kTinyScale : h.vscale;
-    f.mul = h.kscale * qmul;
-    f.add = __builtin_log2f(z);
-    f.back = 1.0f / z;
+    // not 0, so that the masked scores' -infinity stays one (the codes of scale 0 are zeros)
+    f.mul = fmaxf(h.kscale * qmul, 0x1p-120f);
+    f.add = h.add;
+    f.back = exp2_fast(-h.add);
     return f;
 }
 
@@ -175,26 +333,26 @@ __device__ inline u4 keep_live(u4 w, int tok, int len)
     return w;
 }
 
-// N consecutive entries of a query row as fp32.
-template <int N> __device__ inline void load_q(const Kv8Attend &a, int64_t at, float (&x)[N])
+// 8 entries of a query row as fp32.
+__device__ inline void widen_q(const u4 &w, int f16, float *x)
 {
-    static_assert(N % 8 == 0, "16-byte loads");
 #pragma unroll
-    for (int i = 0; i < N; i += 8) {
-        const u4 w = *(const u4 *)((const uint16_t *)a.q + at + i);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t pair = w[j];  // (__builtin_bit_cast of a vector's element takes element 0)
-            if (a.f16) {
-                const h2 h = __builtin_bit_cast(h2, pair);
-                x[i + 2 * j] = (float)h[0];
-                x[i + 2 * j + 1] = (float)h[1];
-            } else {
-                x[i + 2 * j] = __uint_as_float(pair << 16);
-                x[i + 2 * j + 1] = __uint_as_float(pair & 0xffff0000u);
-            }
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t pair = w[j];  // (__builtin_bit_cast of a vector's element takes element 0)
+        if (f16) {
+            const h2 h = __builtin_bit_cast(h2, pair);
+            x[2 * j] = (float)h[0];
+            x[2 * j + 1] = (float)h[1];
+        } else {
+            x[2 * j] = __uint_as_float(pair << 16);
+            x[2 * j + 1] = __uint_as_float(pair & 0xffff0000u);
         }
     }
+}
+
+__device__ inline float first_lane(float x)
+{
+    return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x)));
 }
 
 // The power of two that brings the row's largest entry to [2^14, 2^15): every bf16 or fp16
@@ -205,10 +363,10 @@ __device__ inline float row_scale(float largest, float &inverse)
         inverse = 1.0f;
         return 1.0f;
     }
-    int e = 15 - (ilogbf(largest) + 1);
-    e = e > 120 ? 120 : e;
-    inverse = ldexpf(1.0f, -e);
-    return ldexpf(1.0f, e);
+    int e = (int)(__float_as_uint(largest) >> 23) - 127;  // largest in [2^e, 2^(e + 1))
+    e = e < -106 ? -106 : e;
+    inverse = __uint_as_float((uint32_t)(127 + e - 14) << 23);
+    return __uint_as_float((uint32_t)(127 - e + 14) << 23);
 }
 
 __device__ inline uint32_t out_pair(float a, float b, int f16)
@@ -235,11 +393,12 @@ __device__ inline float lse_of(float m, float l)
                     : (l == l ? -__builtin_inff() : l);
 }
 
-// Partial results of a split: m, l, then D sums, fp32, per (split, token row, query head).
-__device__ inline float *partial(const Kv8Attend &a, const Kv8Batch &b, int D, int split,
-                                 int64_t row, int head)
+// A run's sums of its tile, fp32: 16-byte pieces of the rows' sums in the order in which the kernel's
+// lanes hold them, so that a store instruction covers one span, then m and l of each row.
+template <int BM, int D>
+__device__ inline float *partial(const Kv8Attend &a, int64_t slot)
 {
-    return a.ws + (((int64_t)split * b.tokens + row) * a.q_heads + head) * (D + 4);
+    return a.ws + kCutWords + slot * (BM * (D + 2));
 }
 
 // ------------------------------------------------------------------ few rows
@@ -255,19 +414,19 @@ __global__ __launch_bounds__(256, 2) void kv8_attend_narrow_kernel(Kv8Cache c, K
     constexpr int KS = D / 32;  // MFMA steps over the dimensions
     constexpr int KL = D / 64;  // 16-byte loads per key row and lane
     constexpr int DT = D / 16;  // tiles of output dimensions
-    Tile t;
-    if (!find_tile<BM>(c, b, a, p, t))
-        return;
+    __shared__ int prefix[kPrefixWords], waves[4];
+    __shared__ float om[4][16], ol[4][16], oo[4][16][D + 4];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
-
+    const uint32_t wg = by_xcd((uint32_t)p.groups);
+    Run run = first_run<256, BM>(c, b, a, p, prefix, waves, wg);
+    Tile t;
+    while (next_run<BM>(c, b, a, p, prefix, wg, run, t)) {
     const int r = t.r0 + col;
     const bool have = r < t.rows;
     const int qi = t.q0 + (have ? r : t.rows - 1) / a.group;
     const int qh = t.head * a.group + (have ? r : t.rows - 1) % a.group;
-    const int last_row = t.r0 + BM < t.rows ? t.r0 + BM - 1 : t.rows - 1;
-    const int reach_min = reach(t, a.causal, t.q0 + t.r0 / a.group);
-    const int reach_max = reach(t, a.causal, t.q0 + last_row / a.group);
+    const int reach_min = t.reach_min, reach_max = t.reach_max;
     const int mine = reach(t, a.causal, qi);
 
     // the query row, lane group g holding dimensions g D/4 .. (the order of the dimensions in the
@@ -276,7 +435,11 @@ __global__ __launch_bounds__(256, 2) void kv8_attend_narrow_kernel(Kv8Cache c, K
     float qmul;
     {
         float x[D / 4];
-        load_q<D / 4>(a, (int64_t)(t.row0 + qi) * a.q_stride + (int64_t)qh * D + g * (D / 4), x);
+        const uint16_t *at = (const uint16_t *)a.q + (int64_t)(t.row0 + qi) * a.q_stride +
+                             (int64_t)qh * D + g * (D / 4);
+#pragma unroll
+        for (int i = 0; i < D / 4; i += 8)
+            widen_q(*(const u4 *)(at + i), a.f16, x + i);
         float big = 0.0f;
 #pragma unroll
         for (int i = 0; i < D / 4; ++i)
@@ -292,11 +455,6 @@ __global__ __launch_bounds__(256, 2) void kv8_attend_narrow_kernel(Kv8Cache c, K
             for (int j = 0; j < 8; ++j)
                 q[s][j] = (_Float16)(x[s * 8 + j] * up);
     }
-
-    const int keys = t.list ? a.count << c.log2page : reach_max;
-    const int steps = (keys + kBlock - 1) / kBlock;
-    const int s0 = (int)((int64_t)steps * t.split / p.splits);
-    const int s1 = (int)((int64_t)steps * (t.split + 1) / p.splits);
 
     f4 o[DT];
 #pragma unroll
@@ -319,6 +477,8 @@ __global__ __launch_bounds__(256, 2) void kv8_attend_narrow_kernel(Kv8Cache c, K
             x.h[i] = find_half(c, b, a, t, s * kBlock + 32 * i, reach_max);
     };
     auto load = [&](Step &x) {
+        find_scales(c, t, x.h[0]);
+        find_scales(c, t, x.h[1]);
         const int pk = x.h[kchunk >> 1].page, pv = x.h[g >> 1].page;
         const int sk = x.h[kchunk >> 1].tok & (c.page - 1), sv = x.h[g >> 1].tok & (c.page - 1);
         if (pk >= 0) {
@@ -350,7 +510,8 @@ __global__ __launch_bounds__(256, 2) void kv8_attend_narrow_kernel(Kv8Cache c, K
     };
 
     Step x;
-    int s = s0 + wave;
+    const int s1 = run.s1;
+    int s = run.s0 + wave;
     if (s < s1) {
         meta(s, x);
         load(x);
@@ -381,8 +542,7 @@ __global__ __launch_bounds__(256, 2) void kv8_attend_narrow_kernel(Kv8Cache c, K
         const Factor f = factor(h, qmul);
         const int tok = h.tok + 16 * (g & 1);
         const bool plain = h0.page >= 0 && h1.page >= 0 && h0.tok + 32 <= reach_min &&
-                           h1.tok + 32 <= reach_min && !(h0.vscale < kTinyScale) &&
-                           !(h1.vscale < kTinyScale);
+                           h1.tok + 32 <= reach_min && !flushed(h0) && !flushed(h1);
         float y[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i)
@@ -394,7 +554,7 @@ __global__ __launch_bounds__(256, 2) void kv8_attend_narrow_kernel(Kv8Cache c, K
                 y[i] = none || tok + i >= mine ? -__builtin_inff() : y[i];
 #pragma unroll
             for (int i = 0; i < DT; ++i)
-                v[i] = f.flush ? u4{0, 0, 0, 0} : keep_live(v[i], tok, t.len);
+                v[i] = flushed(h) ? u4{0, 0, 0, 0} : keep_live(v[i], tok, t.len);
         }
         float top = y[0];
 #pragma unroll
@@ -403,7 +563,8 @@ __global__ __launch_bounds__(256, 2) void kv8_attend_narrow_kernel(Kv8Cache c, K
         if (__any(top > m + kSlack)) {
             top = fmaxf(top, __shfl_xor(top, 16));
             top = fmaxf(top, __shfl_xor(top, 32));
-            const float now = fmaxf(m, top), fall = exp2_fast(m - now);
+            // (each row on its own terms: what it gets does not depend on the rows beside it)
+            const float now = top > m + kSlack ? top : m, fall = exp2_fast(m - now);
             m = now;
             l *= fall;
 #pragma unroll
@@ -433,7 +594,6 @@ __global__ __launch_bounds__(256, 2) void kv8_attend_narrow_kernel(Kv8Cache c, K
     l += __shfl_xor(l, 32);
 
     // join the four waves
-    __shared__ float om[4][16], ol[4][16], oo[4][16][D + 4];
     if (g == 0) {
         om[wave][col] = m;
         ol[wave][col] = l;
@@ -456,22 +616,22 @@ __global__ __launch_bounds__(256, 2) void kv8_attend_narrow_kernel(Kv8Cache c, K
             ll += ol[w][row] * e;
             s += *(const f4 *)&oo[w][row][d] * e;
         }
-        const int64_t qrow = t.row0 + t.q0 + rr / a.group;
-        const int head = t.head * a.group + rr % a.group;
-        if (p.splits > 1) {
-            float *out = partial(a, b, D, t.split, qrow, head);
-            if (d == 0) {
-                out[0] = mm;
-                out[1] = ll;
-            }
-            *(f4 *)(out + 4 + d) = s;
+        if (run.slot >= 0) {
+            float *out = partial<BM, D>(a, run.slot);
+            if (d == 0)
+                *(f2 *)(out + BM * D + 2 * row) = f2{mm, ll};
+            *(f4 *)(out + 4 * i) = s;
         } else {
+            const int64_t qrow = t.row0 + t.q0 + rr / a.group;
+            const int head = t.head * a.group + rr % a.group;
             const float inv = ll > 0.0f ? 1.0f / ll : (ll == ll ? 0.0f : ll);
             store_out(a, qrow * a.out_stride + (int64_t)head * D + d, s[0] * inv, s[1] * inv,
                       s[2] * inv, s[3] * inv);
             if (a.lse && d == 0)
                 a.lse[qrow * a.q_heads + head] = lse_of(mm, ll);
         }
+    }
+    __syncthreads();  // om, ol and oo are read
     }
 }
 
@@ -481,267 +641,497 @@ __global__ __launch_bounds__(256, 2) void kv8_attend_narrow_kernel(Kv8Cache c, K
 // once per work-group, one step ahead, converted to fp16 on the way into LDS (each code once instead of once
 // per wave) and read from there by all four waves.  16-byte chunks of a row are exchanged by an XOR of
 // row bits, so that the eight lanes that LDS serves together read eight different bank groups.
-template <int FMT, int D>
-__global__ __launch_bounds__(256, 2) void kv8_attend_wide_kernel(Kv8Cache c, Kv8Batch b,
-                                                                 Kv8Attend a, Kv8Plan p)
+// The XOR of a key row's chunk number: 16 lanes that read one chunk of 16 key rows (in the order
+// that the tile's rows have) must meet 16 different positions of the 256 bytes that LDS serves at
+// once; a row is 256 bytes at head_dim 128, and half of that at 64, where the row's lowest bit counts.
+template <int D> __device__ inline int key_swizzle(int tok)
 {
-    constexpr int BM = 128;
-    constexpr int KS = D / 16;       // MFMA steps over the dimensions
-    constexpr int DT = D / 32;       // tiles of output dimensions
-    constexpr int TPR = D / 16;      // threads per key row of codes
-    constexpr int NL = D * kBlock / 16 / 256;  // 16-byte loads per thread, keys and values alike
-    __shared__ h8 ks[2][kBlock][D / 8];
-    __shared__ h8 vs[2][D][kBlock / 8];
-    Tile t;
-    if (!find_tile<BM>(c, b, a, p, t))
-        return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    if constexpr (D == 128)
+        return (tok & 3) | ((tok >> 4 & 1) << 2) | ((tok >> 2 & 1) << 3);
+    else
+        return (tok >> 1 & 3) | ((tok >> 4 & 1) << 2);
+}
+
+// The same for value rows of VC chunks, read by 16 lanes of consecutive rows.
+template <int VC> __device__ inline int value_swizzle(int row) { return row / (16 / VC) & (VC - 1); }
+
+constexpr int kFront = 4;  // products between an operand's read and its use
+
+template <int FMT, int D, int NW, int R, int H>
+__global__ __launch_bounds__(NW * 64, 2) void kv8_attend_wide_kernel(Kv8Cache c, Kv8Batch b,
+                                                                     Kv8Attend a, Kv8Plan p)
+{
+    constexpr bool PAIRED = NW == 8;  // two waves of the work-group on each SIMD
+    constexpr int BM = 32 * R * NW;
+    constexpr int T = 64 * NW;        // threads
+    constexpr int KS = D / 16;        // MFMA steps over the dimensions
+    constexpr int DT = D / 32;        // tiles of output dimensions
+    constexpr int BK = 32 * H;        // keys of a step
+    constexpr int NK = BK * D / 16;   // 16-byte loads of a step's keys, and of its values
+    constexpr int NL = 2 * NK > T ? 2 * NK / T : 1;  // loads per thread (of the first 2 NK threads)
+    constexpr int VC = BK / 8;        // chunks of a value row in LDS
+    constexpr int AHEAD = (PAIRED ? 1024 : 256) / H;  // steps whose pages are looked up together
+    __shared__ h8 ks[2][BK][D / 8];
+    __shared__ h8 vs[2][D][VC];
+    __shared__ Half halves[H * AHEAD];
+    __shared__ int prefix[kPrefixWords], waves[NW];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int late = PAIRED ? wave / 4 : 0;
     const int col = lane & 31, g = lane >> 5;
-
-    const int r = t.r0 + wave * 32 + col;
-    const bool have = r < t.rows;
-    const int qi = t.q0 + (have ? r : t.rows - 1) / a.group;
-    const int qh = t.head * a.group + (have ? r : t.rows - 1) % a.group;
-    const int last_row = t.r0 + BM < t.rows ? t.r0 + BM - 1 : t.rows - 1;
-    const int reach_min = reach(t, a.causal, t.q0 + t.r0 / a.group);
-    const int reach_max = reach(t, a.causal, t.q0 + last_row / a.group);
-    const int mine = reach(t, a.causal, qi);
-    const int64_t row = t.row0 + qi;
-
-    h8 q[KS];
-    float qmul;
-    {
-        float x[KS][8];
-        float big = 0.0f;
+    const uint32_t wg = by_xcd((uint32_t)p.groups);
+    Run run = first_run<T, BM>(c, b, a, p, prefix, waves, wg);
+    Tile t;
+    while (next_run<BM>(c, b, a, p, prefix, wg, run, t)) {
+        const int wave_row = t.r0 + wave * 32 * R;
+        const bool busy = wave_row < t.rows;  // waves without rows only help to stage
+        int qrow[R], qhead[R], mine[R];
+        u4 raw_q[R][KS];
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            load_q<8>(a, row * a.q_stride + (int64_t)qh * D + s * 16 + g * 8, x[s]);
+        for (int y = 0; y < R; ++y) {
+            int r = wave_row + y * 32 + col;
+            r = r < t.rows ? r : t.rows - 1;
+            qrow[y] = t.q0 + r / a.group;
+            qhead[y] = t.head * a.group + r % a.group;
+            mine[y] = reach(t, a.causal, qrow[y]);
+            const int64_t at = (int64_t)(t.row0 + qrow[y]) * a.q_stride + (int64_t)qhead[y] * D;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                big = fmaxf(big, fabsf(x[s][j]));
+            for (int s = 0; s < KS; ++s)
+                raw_q[y][s] = *(const u4 *)((const uint16_t *)a.q + at + s * 16 + g * 8);
         }
-        big = fmaxf(big, __shfl_xor(big, 32));
-        float inv;
-        const float up = row_scale(big, inv);
-        qmul = inv * (a.scale * 1.4426950408889634f);
+        h8 q[R][KS];
+        float qmul[R];
+        auto scale_q = [&]() {
 #pragma unroll
-        for (int s = 0; s < KS; ++s)
+            for (int y = 0; y < R; ++y) {
+                float x[KS][8];
+                float big = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                q[s][j] = (_Float16)(x[s][j] * up);
-    }
-
-    const int keys = t.list ? a.count << c.log2page : reach_max;
-    const int steps = (keys + kBlock - 1) / kBlock;
-    const int s0 = (int)((int64_t)steps * t.split / p.splits);
-    const int s1 = (int)((int64_t)steps * (t.split + 1) / p.splits);
-
-    f16v o[DT];
+                for (int s = 0; s < KS; ++s) {
+                    widen_q(raw_q[y][s], a.f16, x[s]);
 #pragma unroll
-    for (int i = 0; i < DT; ++i)
+                    for (int j = 0; j < 8; ++j)
+                        big = fmaxf(big, fabsf(x[s][j]));
+                }
+                big = fmaxf(big, __shfl_xor(big, 32));
+                float inv;
+                const float up = row_scale(big, inv);
+                qmul[y] = inv * (a.scale * 1.4426950408889634f);
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            o[i][j] = 0.0f;
-    float m = kNone, l = 0.0f;
-
-    const int64_t page_bytes = (int64_t)c.page * D;
-    u4 kr[NL], vr[NL];
-    Half next[2];
-    // the threads' share of a step: key rows of 16 codes, value rows of 16 tokens
-    const int krow = tid / TPR, kcol = tid % TPR, vrow = tid / 4, vcol = tid % 4;
-    auto load = [&](int s) {
+                for (int s = 0; s < KS; ++s)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            next[i] = find_half(c, b, a, t, s * kBlock + 32 * i, reach_max);
-#pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            const int rr = krow + i * (256 / TPR), hk = rr >> 5;
-            const int pk = hk ? next[1].page : next[0].page;
-            const int sk = (hk ? next[1].tok : next[0].tok) & (c.page - 1);
-            kr[i] = u4{0, 0, 0, 0};
-            if (pk >= 0)
-                kr[i] = *(const u4 *)(c.k + ((int64_t)pk * c.heads + t.head) * page_bytes +
-                                      (sk + (rr & 31)) * D + kcol * 16);
-            const int dd = vrow + i * 64, hv = vcol >> 1;
-            const int pv = hv ? next[1].page : next[0].page;
-            const int tv = hv ? next[1].tok : next[0].tok;
-            vr[i] = u4{0, 0, 0, 0};
-            if (pv >= 0)
-                vr[i] = *(const u4 *)(c.v + ((int64_t)pv * c.heads + t.head) * page_bytes +
-                                      dd * c.page + (tv & (c.page - 1)) + 16 * (vcol & 1));
-        }
-    };
-    auto stage = [&](int buf) {
-        const bool whole = next[0].tok + 32 <= t.len && next[1].tok + 32 <= t.len &&
-                           next[0].vscale >= kTinyScale && next[1].vscale >= kTinyScale;
-        if (!whole) {
-            const Half h = vcol >> 1 ? next[1] : next[0];
-#pragma unroll
-            for (int i = 0; i < NL; ++i)
-                vr[i] = h.vscale >= kTinyScale ? keep_live(vr[i], h.tok + 16 * (vcol & 1), t.len)
-                                               : u4{0, 0, 0, 0};
-        }
-#pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            const int rr = krow + i * (256 / TPR);
-            const int sw = (rr & 3) | ((rr >> 4 & 1) << 2) | ((rr >> 2 & 1) << 3);
-            ks[buf][rr][(kcol * 2) ^ (sw & (D / 8 - 1))] = to_half8<FMT>(kr[i][0], kr[i][1]);
-            ks[buf][rr][(kcol * 2 + 1) ^ (sw & (D / 8 - 1))] = to_half8<FMT>(kr[i][2], kr[i][3]);
-            const int dd = vrow + i * 64;
-            vs[buf][dd][(vcol * 2) ^ (dd & 7)] = to_half8<FMT>(vr[i][0], vr[i][1]);
-            vs[buf][dd][(vcol * 2 + 1) ^ (dd & 7)] = to_half8<FMT>(vr[i][2], vr[i][3]);
-        }
-    };
-
-    // key row `col` of a 32-token half is token 16 (col >> 2 & 1) + (col & 3) + 4 (col >> 3):
-    // accumulator i of lane group g is then token 16 g + i
-    const int ktok = 16 * (col >> 2 & 1) + (col & 3) + 4 * (col >> 3);
-    const int ksw = ((ktok & 3) | ((ktok >> 4 & 1) << 2) | ((ktok >> 2 & 1) << 3)) & (D / 8 - 1);
-
-    if (s0 < s1) {
-        load(s0);
-        stage(0);
-    }
-    __syncthreads();
-    for (int s = s0; s < s1; ++s) {
-        const int buf = (s - s0) & 1;
-        const Half h[2] = {next[0], next[1]};
-        if (s + 1 < s1)
-            load(s + 1);
-        f16v acc[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                acc[x][j] = 0.0f;
-#pragma unroll
-            for (int j = 0; j < KS; ++j)
-                acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                    ks[buf][x * 32 + ktok][(2 * j + g) ^ ksw], q[j], acc[x], 0, 0, 0);
-        }
-        const bool plain = h[0].page >= 0 && h[1].page >= 0 && h[0].tok + 32 <= reach_min &&
-                           h[1].tok + 32 <= reach_min;
-        Factor f[2];
-        float top = -__builtin_inff();
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            f[x] = factor(h[x], qmul);
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                acc[x][j] = fmaf(acc[x][j], f[x].mul, f[x].add);
-            if (!plain) {
-                const int tok = h[x].tok + 16 * g;
-                const bool none = h[x].page < 0;
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    acc[x][j] = none || tok + j >= mine ? -__builtin_inff() : acc[x][j];
+                    for (int j = 0; j < 8; ++j)
+                        q[y][s][j] = (_Float16)(x[s][j] * up);
             }
+        };
+
+        f16v o[R][DT];
+        float m[R], l[R];
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                top = fmaxf(top, acc[x][j]);
-        }
-        if (__any(top > m + kSlack)) {
-            top = fmaxf(top, __shfl_xor(top, 32));
-            const float now = fmaxf(m, top), fall = exp2_fast(m - now);
-            m = now;
-            l *= fall;
+        for (int y = 0; y < R; ++y) {
 #pragma unroll
             for (int i = 0; i < DT; ++i)
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                    o[i][j] *= fall;
+                    o[y][i][j] = 0.0f;
+            m[y] = kNone;
+            l[y] = 0.0f;
         }
-        h8 w[4];
+
+        // A thread's share of a step: loads of 16 codes, of a key row or of a value row; all of
+        // a wave's in one half and of one kind, so that pages and addresses are scalar.
+        const uint32_t head_off = (uint32_t)t.head * (uint32_t)(c.page * D);
+        const int64_t page_bytes = (int64_t)c.heads * c.page * D;
+        const int krow = tid * 16 / D, kcol = tid % (D / 16), vrow = tid / 2, vcol = tid & 1;
+        u4 raw[NL];
+        int first = 0, last = 0;  // the steps that `halves` holds
+        // the halves of this step and the next WIN - 1
+        constexpr int WIN = 3;
+        Half win[WIN][H];
+        auto look = [&](int s, Half (&h)[H]) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            float sum = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-                const float e0 = exp2_fast(acc[x][j] + (kLift - m));
-                const float e1 = exp2_fast(acc[x][j + 1] + (kLift - m));
-                sum += e0 + e1;
-                const h2 e = pack(e0, e1);
-                w[2 * x + j / 8][j % 8] = e[0];
-                w[2 * x + j / 8][j % 8 + 1] = e[1];
+            for (int x = 0; x < H; ++x) {
+                const Half n = halves[H * (s < last ? s - first : 0) + x];
+                h[x].page = s < last ? __builtin_amdgcn_readfirstlane(n.page) : -1;
+                h[x].tok = __builtin_amdgcn_readfirstlane(n.tok);
+                h[x].kscale = first_lane(n.kscale);
+                h[x].add = first_lane(n.add);
             }
-            l = fmaf(sum, f[x].back, l);
-        }
+        };
+        // whether load i is of keys, and of which half
+        auto of_keys = [&](int i) { return T <= NK ? i * T < NK : wave * 64 < NK; };
+        const bool loads = wave * 64 < 2 * NK;
+        auto half_of = [&](int i) {
+            const int id = wave * 64 + i * T;
+            return of_keys(i) ? id * 16 / D / 32 : (id - NK) / (2 * D);
+        };
+        // keys of a step (its halves hk) and values of the step before it (hv)
+        auto load = [&](const Half (&hk)[H], const Half (&hv)[H]) {
 #pragma unroll
-        for (int i = 0; i < DT; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                // weights j of lane group g: tokens 32 (j / 2) + 16 g + 8 (j % 2) ..
-                const int chunk = 4 * (j / 2) + 2 * g + j % 2;
-                o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                    vs[buf][i * 32 + col][chunk ^ (col & 7)], w[j], o[i], 0, 0, 0);
+            for (int i = 0; i < NL; ++i) {
+                const int x = half_of(i);
+                raw[i] = u4{0, 0, 0, 0};
+                if (!loads)
+                    continue;
+                if (of_keys(i)) {
+                    const Half h = x ? hk[H - 1] : hk[0];
+                    if (h.page >= 0)
+                        raw[i] = *(const u4 *)(c.k + (h.page * page_bytes + head_off +
+                                                      ((h.tok & (c.page - 1)) +
+                                                       (i * T * 16 / D & 31)) * D) +
+                                               (uint32_t)((krow & 31) * D + kcol * 16));
+                } else {
+                    const Half h = x ? hv[H - 1] : hv[0];
+                    if (h.page >= 0)
+                        raw[i] = *(const u4 *)(c.v + (h.page * page_bytes + head_off +
+                                                      (h.tok & (c.page - 1))) +
+                                               (uint32_t)((vrow + (i * T - NK - x * 2 * D) / 2) *
+                                                              c.page + vcol * 16));
+                }
             }
-        if (s + 1 < s1)
-            stage(buf ^ 1);
-        __syncthreads();
-    }
-    l += __shfl_xor(l, 32);
-    if (!have)
-        return;
-    if (p.splits > 1) {
-        float *out = partial(a, b, D, t.split, row, qh);
-        if (g == 0) {
-            out[0] = m;
-            out[1] = l;
+        };
+        // what the value rows read hold behind the live tokens becomes zeros
+        auto mend = [&](const Half (&hv)[H]) {
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                if (of_keys(i))
+                    continue;
+                const Half h = half_of(i) ? hv[H - 1] : hv[0];
+                if (h.tok + 32 > t.len || flushed(h))
+                    raw[i] = flushed(h) ? u4{0, 0, 0, 0}
+                                        : keep_live(raw[i], h.tok + 16 * vcol, t.len);
+            }
+        };
+        // 8 of the read codes (part 0 .. 2 NL - 1) to fp16 in LDS: keys of step e, values of e - 1
+        auto stage = [&](int e, int part) {
+            if (!loads)
+                return;
+            const int i = part / 2, z = part & 1, x = half_of(i);
+            const h8 v = to_half8<FMT>(raw[i][2 * z], raw[i][2 * z + 1]);
+            if (of_keys(i)) {
+                const int rr = krow + i * T * 16 / D;
+                ks[(e - first) & 1][rr][(kcol * 2 + z) ^ key_swizzle<D>(rr)] = v;
+            } else {
+                const int dd = vrow + (i * T - NK - x * 2 * D) / 2, vc = x * 4 + vcol * 2 + z;
+                vs[(e - 1 - first) & 1][dd][vc ^ value_swizzle<VC>(dd)] = v;
+            }
+        };
+
+        // key row `col` of a half is token 16 (col >> 2 & 1) + (col & 3) + 4 (col >> 3):
+        // accumulator i of lane group g is then token 16 g + i
+        const int ktok = 16 * (col >> 2 & 1) + (col & 3) + 4 * (col >> 3);
+        const int ksw = key_swizzle<D>(ktok);
+        f16v acc[R][H];
+        h2 w[R][8 * H];
+
+        // The matrix products of a phase: the previous step's values, then this step's scores.  The
+        // operands are read from LDS kFront products ahead (a read takes several products' time).
+        constexpr int NV = 2 * H * DT, NS = H * KS;
+        auto value_operand = [&](int s, int i) {
+            // weights j of lane group g: tokens 32 (j / 2) + 16 g + 8 (j % 2) ..
+            const int j = i / DT, chunk = 4 * (j / 2) + 2 * g + j % 2;
+            return vs[(s - first) & 1][i % DT * 32 + col][chunk ^ value_swizzle<VC>(col)];
+        };
+        auto key_operand = [&](int s, int i) {
+            return ks[(s - first) & 1][i / KS * 32 + ktok][(2 * (i % KS) + g) ^ ksw];
+        };
+        auto add_value = [&](const h8 &v, int i) {
+            const int j = i / DT;
+#pragma unroll
+            for (int y = 0; y < R; ++y) {
+                const h8 wj = {w[y][4 * j][0],     w[y][4 * j][1],     w[y][4 * j + 1][0],
+                               w[y][4 * j + 1][1], w[y][4 * j + 2][0], w[y][4 * j + 2][1],
+                               w[y][4 * j + 3][0], w[y][4 * j + 3][1]};
+                o[y][i % DT] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, wj, o[y][i % DT], 0, 0, 0);
+            }
+        };
+        auto score = [&](const h8 &k, int i) {
+            const int x = i / KS;
+#pragma unroll
+            for (int y = 0; y < R; ++y) {
+                if (i % KS == 0)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        acc[y][x][j] = 0.0f;
+                acc[y][x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[y][i % KS], acc[y][x], 0, 0, 0);
+            }
+        };
+        // Between them goes the staging of what the next step needs: the matrix unit works on while the
+        // codes are converted.
+        auto multiply = [&](int s, auto scores) {
+            constexpr bool MORE = decltype(scores)::value;
+            constexpr int A = NV, N = A + (MORE ? NS : 0);
+            __builtin_amdgcn_sched_barrier(0);
+            h8 x[N];
+#pragma unroll
+            for (int i = 0; i < kFront; ++i)
+                x[i] = i < A ? value_operand(s - 1, i) : key_operand(s, i - A);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                if (i + kFront < N) {
+                    const int n = i + kFront;
+                    x[n] = n < A ? value_operand(s - 1, n) : key_operand(s, n - A);
+                }
+                if (i < A)
+                    add_value(x[i], i);
+                else
+                    score(x[i], i - A);
+                if (MORE && i >= N / 2 && (i - N / 2) % (N / 4 / NL) == 0)
+                    stage(s + 1, (i - N / 2) / (N / 4 / NL));
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        // The weights are formed with the maximum as it stands.  Where a lane's sum of them
+        // exceeds kLimit (infinities and NaN too) the row's maximum is moved up to the true one,
+        // its sums are rescaled and its weights are formed again: rare after the first steps, and one
+        // comparison instead of a maximum over the scores of every step.  (Each row on its
+        // own terms: what it gets does not depend on the rows beside it.)
+        auto weights = [&](const Half (&h)[H]) {
+#pragma unroll
+            for (int x = 0; x < H; ++x)
+                if (h[x].page < 0 || h[x].tok + 32 > t.reach_min) {
+#pragma unroll
+                    for (int y = 0; y < R; ++y) {
+                        const int seen = h[x].page < 0 ? 0 : mine[y] - h[x].tok - 16 * g;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            acc[y][x][j] = j < seen ? acc[y][x][j] : -__builtin_inff();
+                    }
+                }
+            Factor f[R][H];
+            float sum[R][H];
+            auto weigh = [&](int y) {
+#pragma unroll
+                for (int x = 0; x < H; ++x) {
+                    const float base = f[y][x].add + (kLift - m[y]);
+                    float part = 0.0f;
+                    sum[y][x] = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        const float e0 = exp2_fast(fmaf(acc[y][x][j], f[y][x].mul, base));
+                        const float e1 = exp2_fast(fmaf(acc[y][x][j + 1], f[y][x].mul, base));
+                        sum[y][x] += e0;
+                        part += e1;
+                        w[y][8 * x + j / 2] = pack(e0, e1);
+                    }
+                    sum[y][x] += part;
+                }
+            };
+            bool any = false;
+#pragma unroll
+            for (int y = 0; y < R; ++y) {
+#pragma unroll
+                for (int x = 0; x < H; ++x)
+                    f[y][x] = factor(h[x], qmul[y]);
+                weigh(y);
+                any |= !(sum[y][0] + sum[y][H - 1] <= kLimit);
+            }
+            if (__any(any)) {
+#pragma unroll
+                for (int y = 0; y < R; ++y) {
+                    const int over = !(sum[y][0] + sum[y][H - 1] <= kLimit);
+                    float top = kNone;
+#pragma unroll
+                    for (int x = 0; x < H; ++x) {
+                        float z = acc[y][x][0];
+#pragma unroll
+                        for (int j = 1; j < 16; ++j)
+                            z = fmaxf(z, acc[y][x][j]);
+                        top = fmaxf(top, fmaf(z, f[y][x].mul, f[y][x].add));
+                    }
+                    top = fmaxf(top, __shfl_xor(top, 32));
+                    const bool move = over | __shfl_xor(over, 32);
+                    const float now = move ? fmaxf(m[y], top) : m[y], fall = exp2_fast(m[y] - now);
+                    m[y] = now;
+                    l[y] *= fall;
+#pragma unroll
+                    for (int i = 0; i < DT; ++i)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            o[y][i][j] *= fall;
+                    weigh(y);
+                }
+            }
+#pragma unroll
+            for (int y = 0; y < R; ++y)
+#pragma unroll
+                for (int x = 0; x < H; ++x)
+                    l[y] = fmaf(sum[y][x], f[y][x].back, l[y]);
+        };
+
+        // Two phases a step, a barrier after each: the matrix products (the previous step's values,
+        // this step's scores) with the staging of the next step's keys and this step's values between
+        // them, then the weights.  Of the two waves on a SIMD the later one runs a phase
+        // behind, so that one multiplies while the other computes weights.  The keys of step s + 1
+        // and the values of step s are written in the phases of scores s (2 s and, a phase
+        // behind, 2 s + 1); what their buffers held, keys s - 1 and values s - 2, was last read in the
+        // late waves' phase 2 s - 1, and they are first read in the early waves' phase 2 s + 2.
+        Half none[H];
+#pragma unroll
+        for (int x = 0; x < H; ++x)
+            none[x] = Half{-1, 0, 0.0f, kTiny};
+        const int begin = run.s0 * (2 / H), end = run.s1 * (2 / H);
+        auto look_up = [&]() {
+            last = first + AHEAD < end ? first + AHEAD : end;
+            __syncthreads();
+            for (int i = tid; i < H * (last - first); i += T) {
+                Half h = find_half(c, b, a, t, first * BK + 32 * i, t.reach_max);
+                find_scales(c, t, h);
+                halves[i] = h;
+            }
+            __syncthreads();
+        };
+        first = begin;
+        look_up();
+        scale_q();
+        while (first < end) {
+#pragma unroll
+            for (int i = 0; i < WIN; ++i)
+                look(first + i, win[i]);
+            load(win[0], none);
+            // the first step's product with "the previous step's values" adds zeros
+#pragma unroll
+            for (int i = tid; i < D * VC; i += T)
+                (&vs[1][0][0])[i] = h8{};
+#pragma unroll
+            for (int y = 0; y < R; ++y)
+#pragma unroll
+                for (int j = 0; j < 8 * H; ++j)
+                    w[y][j] = h2{};
+#pragma unroll
+            for (int i = 0; i < 2 * NL; ++i)
+                if (of_keys(i / 2))
+                    stage(first, i);
+            load(win[1], win[0]);
+            __syncthreads();
+            if (late)
+                __syncthreads();
+            for (int s = first; s < last; ++s) {
+                mend(win[0]);
+                if (busy) {
+                    multiply(s, std::true_type());
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2 * NL; ++i)
+                        stage(s + 1, i);
+                }
+                load(win[2], win[1]);
+                __syncthreads();
+                if (busy)
+                    weights(win[0]);
+#pragma unroll
+                for (int i = 0; i + 1 < WIN; ++i)
+#pragma unroll
+                    for (int x = 0; x < H; ++x)
+                        win[i][x] = win[i + 1][x];
+                look(s + WIN, win[WIN - 1]);
+                __syncthreads();
+            }
+            if (busy)
+                multiply(last, std::false_type());
+            if (PAIRED && !late)
+                __syncthreads();
+            first = last;
+            if (first < end)
+                look_up();
         }
+
 #pragma unroll
-        for (int i = 0; i < DT; ++i)
+        for (int y = 0; y < R; ++y) {
+            const float all = l[y] + __shfl_xor(l[y], 32);
+            if (wave_row + y * 32 + col >= t.rows)
+                continue;
+            const int64_t row = t.row0 + qrow[y];
+            if (run.slot >= 0) {
+                float *out = partial<BM, D>(a, run.slot) + (wave * R + y) * 32 * D;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                *(f4 *)(out + 4 + i * 32 + j * 8 + g * 4) =
-                    f4{o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]};
-    } else {
-        const float inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
+                for (int i = 0; i < DT * 4; ++i)
+                    *(f4 *)(out + (i * 64 + lane) * 4) =
+                        f4{o[y][i / 4][i % 4 * 4], o[y][i / 4][i % 4 * 4 + 1],
+                           o[y][i / 4][i % 4 * 4 + 2], o[y][i / 4][i % 4 * 4 + 3]};
+                if (g == 0)
+                    *(f2 *)(partial<BM, D>(a, run.slot) + BM * D +
+                            2 * ((wave * R + y) * 32 + col)) = f2{m[y], all};
+            } else {
+                const float inv = all > 0.0f ? 1.0f / all : (all == all ? 0.0f : all);
+                const int64_t at = row * a.out_stride + (int64_t)qhead[y] * D + g * 4;
 #pragma unroll
-        for (int i = 0; i < DT; ++i)
+                for (int i = 0; i < DT; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                store_out(a, row * a.out_stride + (int64_t)qh * D + i * 32 + j * 8 + g * 4,
-                          o[i][4 * j] * inv, o[i][4 * j + 1] * inv, o[i][4 * j + 2] * inv,
-                          o[i][4 * j + 3] * inv);
-        if (a.lse && g == 0)
-            a.lse[row * a.q_heads + qh] = lse_of(m, l);
+                    for (int j = 0; j < 4; ++j)
+                        store_out(a, at + i * 32 + j * 8, o[y][i][4 * j] * inv,
+                                  o[y][i][4 * j + 1] * inv, o[y][i][4 * j + 2] * inv,
+                                  o[y][i][4 * j + 3] * inv);
+                if (a.lse && g == 0)
+                    a.lse[row * a.q_heads + qhead[y]] = lse_of(m[y], all);
+            }
+        }
     }
 }
 
-// Joins the splits' partial results: D / 4 threads per row.
-template <int D>
+// Joins the runs of the tile that work-group blockIdx.x began and did not finish, 256 16-byte pieces
+// per work-group.
+template <int BM, int D>
 __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8Cache c, Kv8Batch b, Kv8Attend a,
-                                                       Kv8Plan p, int chunks)
+                                                       Kv8Plan p)
 {
-    constexpr int PER = 256 / (D / 4);
-    const int seq = blockIdx.x / chunks;
-    int row0, n;
-    kv8_rows(b, seq, row0, n);
-    const int64_t i = (int64_t)(blockIdx.x % chunks) * PER + threadIdx.x / (D / 4);
-    if (i >= (int64_t)n * a.q_heads)
+    const uint32_t w = blockIdx.x;
+    const Cut cut = ((const Cut *)a.ws)[w];
+    if (cut.more == 0)
         return;
-    const int64_t row = row0 + i / a.q_heads;
-    const int head = (int)(i % a.q_heads), d = threadIdx.x % (D / 4) * 4;
-    float m = kNone;
-    for (int s = 0; s < p.splits; ++s)
-        m = fmaxf(m, partial(a, b, D, s, row, head)[0]);
-    float l = 0.0f;
-    f4 o = {0, 0, 0, 0};
-    for (int s = 0; s < p.splits; ++s) {
-        const float *x = partial(a, b, D, s, row, head);
-        const float e = exp2_fast(x[0] - m);
-        l += x[1] * e;
-        o += *(const f4 *)(x + 4 + d) * e;
+    Tile t;
+    if (!find_tile<BM>(c, b, a, p, cut.item, cut.head, t))
+        return;
+    const int i = blockIdx.y * 256 + threadIdx.x;  // the piece
+    int row, d;
+    if constexpr (BM == 16) {
+        row = i / (D / 4);
+        d = i % (D / 4) * 4;
+    } else {
+        row = i / (8 * D) * 32 + i % 32;
+        d = i % (8 * D) / 64 * 8 + i % 64 / 32 * 4;
     }
-    const float inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
-    store_out(a, row * a.out_stride + (int64_t)head * D + d, o[0] * inv, o[1] * inv, o[2] * inv,
+    const int r = t.r0 + row;
+    if (r >= t.rows)
+        return;
+    // the first part lies in the beginning work-group's second slot, the others in first ones
+    const float *x = partial<BM, D>(a, 2 * w + 1);
+    f2 ml = *(const f2 *)(x + BM * D + 2 * row);
+    f4 o = *(const f4 *)(x + 4 * i);
+    for (int k = 1; k <= cut.more; ++k) {
+        x = partial<BM, D>(a, 2 * (w + k));
+        const f2 n = *(const f2 *)(x + BM * D + 2 * row);
+        const f4 v = *(const f4 *)(x + 4 * i);
+        const float now = fmaxf(ml[0], n[0]);
+        const float e0 = exp2_fast(ml[0] - now), e1 = exp2_fast(n[0] - now);
+        ml = f2{now, ml[1] * e0 + n[1] * e1};
+        o = o * e0 + v * e1;
+    }
+    const int64_t qrow = t.row0 + t.q0 + r / a.group;
+    const int qhead = t.head * a.group + r % a.group;
+    const float l = ml[1], inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
+    store_out(a, qrow * a.out_stride + (int64_t)qhead * D + d, o[0] * inv, o[1] * inv, o[2] * inv,
               o[3] * inv);
     if (a.lse && d == 0)
-        a.lse[row * a.q_heads + head] = lse_of(m, l);
+        a.lse[qrow * a.q_heads + qhead] = lse_of(ml[0], l);
 }
 
 constexpr int64_t kNarrowRows = 32;  // rows of a query block up to which the narrow kernel is taken
-constexpr int64_t kFill = 512;       // work-groups that fill the chip (two on each of 256 CUs)
+
+// The launch's shapes: rows per tile, threads, and work-groups that are resident at once.
+struct Shape {
+    int rows, threads, slots;
+};
+
+Shape shape_of(bool wide, int dim, int64_t rows)
+{
+    if (!wide)
+        return {16, 256, 512};
+    if (rows <= 128)
+        return {128, 256, 512};
+    return dim == 64 && rows > 256 ? Shape{512, 512, 256} : Shape{256, 512, 256};
+}
 
 }  // namespace
 
@@ -754,46 +1144,84 @@ Kv8Plan kv8_plan(const Kv8Cache &c, const Kv8Batch &b, int q_heads, int64_t max_
         q_block = b.max_rows;
     const int64_t rows = q_block * group;
     p.wide = rows > kNarrowRows;
-    p.units = q_block > 0 ? (b.max_rows + q_block - 1) / q_block : 0;
-    p.tiles = p.wide ? (rows + 127) / 128 : (rows + 15) / 16;
-    const int64_t whole = p.units * p.tiles * c.heads * b.batch;
+    const Shape sh = shape_of(p.wide, c.dim, rows);
+    const double units = (double)((b.max_rows + q_block - 1) / q_block);
+    const double tiles = (double)((rows + sh.rows - 1) / sh.rows);
+    p.whole = units * tiles * c.heads * b.batch;
+    p.units = p.tiles = p.items = 1;
+    p.joined = 0;
+    p.groups = 1;
+    p.ws_bytes = 0;
+    p.rows = sh.rows;
+    p.threads = sh.threads;
+    if (p.whole >= 2147483648.0)
+        return p;  // refused by the caller
+    p.units = (int)units;
+    p.tiles = (int)tiles;
+    p.items = (int)(units * tiles) * b.batch;
+    p.groups = (int64_t)p.items * c.heads;
     const int64_t keys = listed && (int64_t)count * c.page < max_kv ? (int64_t)count * c.page : max_kv;
     const int64_t steps = (keys + kBlock - 1) / kBlock;
-    // a part should have some steps for each wave, or its joining costs more than it saves
-    int64_t splits = whole > 0 ? kFill / whole : 1;
-    const int64_t most = steps / (p.wide ? 4 : 8);
-    splits = splits < most ? splits : most;
-    p.splits = (int)(splits < 1 ? 1 : (splits > 128 ? 128 : splits));
-    p.groups = whole * p.splits;
+    // Runs of equal length instead of whole tiles: only where a run is long enough to be worth
+    // joining (a narrow one has 4 waves, each of which should have some steps).
+    const int64_t least = p.wide ? 4 : 16;
+    if (p.items <= kMaxItems && steps > least && p.whole * steps < 2147483648.0) {
+        int64_t runs = p.groups * steps / least;
+        runs = runs < sh.slots ? runs : sh.slots;
+        p.joined = 1;
+        p.groups = runs;
+        p.ws_bytes = ((int64_t)kCutWords + 2 * runs * sh.rows * (c.dim + 2)) * sizeof(float);
+    }
     return p;
 }
+
+namespace {
+
+template <int F, int D>
+void attend_as(const Kv8Cache &c, const Kv8Batch &b, const Kv8Attend &a, const Kv8Plan &p,
+               hipStream_t st)
+{
+    const dim3 grid((unsigned)p.groups);
+    if (!p.wide)
+        kv8_attend_narrow_kernel<F, D><<<grid, 256, 0, st>>>(c, b, a, p);
+    else if (p.rows == 128)
+        kv8_attend_wide_kernel<F, D, 4, 1, 2><<<grid, 256, 0, st>>>(c, b, a, p);
+    else if (p.rows == 256)
+        kv8_attend_wide_kernel<F, D, 8, 1, 2><<<grid, 512, 0, st>>>(c, b, a, p);
+    else
+        kv8_attend_wide_kernel<F, 64, 8, 2, 1><<<grid, 512, 0, st>>>(c, b, a, p);
+}
+
+template <int D>
+void join_as(const Kv8Cache &c, const Kv8Batch &b, const Kv8Attend &a, const Kv8Plan &p,
+             hipStream_t st)
+{
+    const dim3 grid((unsigned)p.groups, (unsigned)(p.rows * D / 1024));
+    if (p.rows == 512)
+        kv8_join_kernel<512, D><<<grid, 256, 0, st>>>(c, b, a, p);
+    else if (p.rows == 16)
+        kv8_join_kernel<16, D><<<grid, 256, 0, st>>>(c, b, a, p);
+    else if (p.rows == 128)
+        kv8_join_kernel<128, D><<<grid, 256, 0, st>>>(c, b, a, p);
+    else
+        kv8_join_kernel<256, D><<<grid, 256, 0, st>>>(c, b, a, p);
+}
+
+}  // namespace
 
 hipError_t launch_kv8_attend(const Kv8Cache &c, const Kv8Batch &b, const Kv8Attend &a,
                              const Kv8Plan &p, hipStream_t st)
 {
-    const dim3 grid((unsigned)p.groups);
-#define CFZ_KV8_CASE(F, D)                                                                         \
-    if (c.fmt == F && c.dim == D) {                                                                \
-        if (p.wide)                                                                                \
-            kv8_attend_wide_kernel<F, D><<<grid, 256, 0, st>>>(c, b, a, p);                        \
-        else                                                                                       \
-            kv8_attend_narrow_kernel<F, D><<<grid, 256, 0, st>>>(c, b, a, p);                      \
-    }
-    CFZ_KV8_CASE(CFZ_KV8_INT8, 64)
-    CFZ_KV8_CASE(CFZ_KV8_INT8, 128)
-    CFZ_KV8_CASE(CFZ_KV8_E4M3, 64)
-    CFZ_KV8_CASE(CFZ_KV8_E4M3, 128)
-#undef CFZ_KV8_CASE
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.splits == 1)
-        return e;
-    const int per = 256 / (c.dim / 4);
-    const int64_t chunks = (b.max_rows * a.q_heads + per - 1) / per;
-    const dim3 joins((unsigned)(chunks * b.batch));
-    if (c.dim == 64)
-        kv8_join_kernel<64><<<joins, 256, 0, st>>>(c, b, a, p, (int)chunks);
+    if (c.fmt == CFZ_KV8_INT8)
+        c.dim == 64 ? attend_as<CFZ_KV8_INT8, 64>(c, b, a, p, st)
+                    : attend_as<CFZ_KV8_INT8, 128>(c, b, a, p, st);
     else
-        kv8_join_kernel<128><<<joins, 256, 0, st>>>(c, b, a, p, (int)chunks);
+        c.dim == 64 ? attend_as<CFZ_KV8_E4M3, 64>(c, b, a, p, st)
+                    : attend_as<CFZ_KV8_E4M3, 128>(c, b, a, p, st);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !p.joined || p.groups == 1)
+        return e;
+    c.dim == 64 ? join_as<64>(c, b, a, p, st) : join_as<128>(c, b, a, p, st);
     return hipGetLastError();
 }
 

@@ -38,11 +38,15 @@ hipError_t launch_kv8_gather(const Kv8Cache &c, const Kv8Batch &b, int dtype, vo
 
 // How a call's query rows and keys are cut up; the same for the workspace query and the launch.
 struct Kv8Plan {
-    bool wide;       // 128-row tiles with the keys staged in LDS, else 16-row tiles
-    int splits;      // parts of the key axis, joined by a second launch if > 1
-    int64_t units;   // query blocks per sequence (1 without block lists)
-    int64_t tiles;   // row tiles per query block
-    int64_t groups;  // work-groups of the launch
+    bool wide;         // row tiles with the keys staged in LDS, else 16-row tiles
+    int joined;        // equal runs of steps, joined by a second launch; else one tile a work-group
+    int rows, threads; // per work-group
+    int units;         // query blocks per sequence (1 without block lists)
+    int tiles;         // row tiles per query block
+    int items;         // tiles per head
+    int64_t groups;    // work-groups of the launch
+    int64_t ws_bytes;
+    double whole;      // tiles in all; the launch is possible below 2^31
 };
 
 struct Kv8Attend {

@@ -10,8 +10,8 @@ step 2^-11 each, so |error| <= 2^-11 sum w|v| from them; a score is an fp32 sum 
 products and a few roundings of its factors, off by at most e = (D + 8) 2^-24 max_t sum|q k| + 2^-21
 |y| (y, the score as a power of two with the value scale's logarithm, is below 2^8 here), which moves
 numerator and denominator by e sum w|v| each; the sums over n keys add 2 n 2^-24 sum w|v|; weights
-that fp16 holds as subnormal numbers lose at most 2^-35 of the largest each (2^-25 at a lift of
-2^10), n 2^-35 qmax max(scale) in all; the result is rounded once, half a step of |out|.  lse is off by e
+that fp16 holds as subnormal numbers lose at most 2^-31 of the largest each (2^-25 at a lift of
+2^6), n 2^-31 qmax max(scale) in all; the result is rounded once, half a step of |out|.  lse is off by e
 plus the fp32 roundings of the sum and the logarithm, n 2^-24 + 2^-21 max(1, |lse|)."""
 import sys
 
@@ -233,7 +233,7 @@ def bound(x, out, lse, size, reach, n, half, scale):
     d = x.dim
     e = (d + 8) * 2.0 ** -24 * reach + 2.0 ** -21 * 2.0 ** 8
     top = float(np.max(x.model.vs)) * model.QMAX[x.fmt]
-    tol = (2.0 ** -11 + 2 * e[..., None] + 2 * n * 2.0 ** -24) * size + n * 2.0 ** -35 * top
+    tol = (2.0 ** -11 + 2 * e[..., None] + 2 * n * 2.0 ** -24) * size + n * 2.0 ** -31 * top
     return tol * (1 + half) + half * np.abs(out), e + n * 2.0 ** -24 + 2.0 ** -21 * np.maximum(
         1, np.abs(np.where(np.isfinite(lse), lse, 0)))
 

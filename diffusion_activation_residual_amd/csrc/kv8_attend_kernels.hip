@@ -85,6 +85,9 @@ struct Tile {
     const int32_t *list;  // the block's pages or null
 };
 
+// x / d for x >= 0 where d is often 1 (and uniform): a division is some 40 instructions.
+__device__ inline int quotient(int x, int d) { return d == 1 ? x : x / d; }
+
 // Keys that query qi of the sequence sees: the tokens below this.
 __device__ inline int reach(const Tile &t, int causal, int qi)
 {
@@ -100,10 +103,9 @@ template <int BM>
 __device__ inline bool find_tile(const Kv8Cache &c, const Kv8Batch &b, const Kv8Attend &a,
                                  const Kv8Plan &p, int item, int head, Tile &t)
 {
-    const int tile = item % p.tiles;
-    item /= p.tiles;
-    const int unit = item % p.units;
-    t.seq = item / p.units;
+    const int rest = quotient(item, p.tiles), tile = item - rest * p.tiles;
+    t.seq = quotient(rest, p.units);
+    const int unit = rest - t.seq * p.units;
     t.head = head;
     kv8_rows(b, t.seq, t.row0, t.n);
     t.len = kv8_length(b, t.seq, a.max_kv);
@@ -119,8 +121,8 @@ __device__ inline bool find_tile(const Kv8Cache &c, const Kv8Batch &b, const Kv8
     t.list = a.blocks ? a.blocks + (((int64_t)t.seq * p.units + unit) * c.heads + head) * a.count
                       : nullptr;
     const int last = t.r0 + BM < t.rows ? t.r0 + BM - 1 : t.rows - 1;
-    t.reach_min = reach(t, a.causal, t.q0 + t.r0 / a.group);
-    t.reach_max = reach(t, a.causal, t.q0 + last / a.group);
+    t.reach_min = reach(t, a.causal, t.q0 + quotient(t.r0, a.group));
+    t.reach_max = reach(t, a.causal, t.q0 + quotient(last, a.group));
     const int keys = t.list ? a.count << c.log2page : t.reach_max;
     t.steps = (keys + kBlock - 1) / kBlock;
     return true;
@@ -691,8 +693,9 @@ __global__ __launch_bounds__(NW * 64, 2) void kv8_attend_wide_kernel(Kv8Cache c,
         for (int y = 0; y < R; ++y) {
             int r = wave_row + y * 32 + col;
             r = r < t.rows ? r : t.rows - 1;
-            qrow[y] = t.q0 + r / a.group;
-            qhead[y] = t.head * a.group + r % a.group;
+            const int query = quotient(r, a.group);
+            qrow[y] = t.q0 + query;
+            qhead[y] = (t.head - query) * a.group + r;
             mine[y] = reach(t, a.causal, qrow[y]);
             const int64_t at = (int64_t)(t.row0 + qrow[y]) * a.q_stride + (int64_t)qhead[y] * D;
 #pragma unroll
@@ -1070,51 +1073,72 @@ __global__ __launch_bounds__(NW * 64, 2) void kv8_attend_wide_kernel(Kv8Cache c,
     }
 }
 
-// Joins the runs of the tile that work-group blockIdx.x began and did not finish, 256 16-byte pieces
-// per work-group.
+// Joins the runs of the tile that work-group blockIdx.x began and did not finish: kPieces 16-byte
+// pieces per thread, read together.
+constexpr int kPieces = 4;
+
 template <int BM, int D>
 __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8Cache c, Kv8Batch b, Kv8Attend a,
                                                        Kv8Plan p)
 {
+    constexpr int ALL = BM * D / 4, N = ALL < kPieces * 256 ? ALL / 256 : kPieces;
     const uint32_t w = blockIdx.x;
     const Cut cut = ((const Cut *)a.ws)[w];
     if (cut.more == 0)
         return;
+    const int i0 = blockIdx.y * (N * 256) + threadIdx.x;  // the first piece
+    int row[N], d[N];
+    f2 ml[N];
+    f4 o[N];
+    // the first part lies in the beginning work-group's second slot, the others in first ones
+    const float *x = partial<BM, D>(a, 2 * w + 1);
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const int i = i0 + n * 256;
+        if constexpr (BM == 16) {
+            row[n] = i / (D / 4);
+            d[n] = i % (D / 4) * 4;
+        } else {
+            row[n] = i / (8 * D) * 32 + i % 32;
+            d[n] = i % (8 * D) / 64 * 8 + i % 64 / 32 * 4;
+        }
+        ml[n] = *(const f2 *)(x + BM * D + 2 * row[n]);
+        o[n] = *(const f4 *)(x + 4 * i);
+    }
+    for (int k = 1; k <= cut.more; ++k) {
+        x = partial<BM, D>(a, 2 * (w + k));
+        f2 more[N];
+        f4 v[N];
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            more[n] = *(const f2 *)(x + BM * D + 2 * row[n]);
+            v[n] = *(const f4 *)(x + 4 * (i0 + n * 256));
+        }
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const float now = fmaxf(ml[n][0], more[n][0]);
+            const float e0 = exp2_fast(ml[n][0] - now), e1 = exp2_fast(more[n][0] - now);
+            ml[n] = f2{now, ml[n][1] * e0 + more[n][1] * e1};
+            o[n] = o[n] * e0 + v[n] * e1;
+        }
+    }
     Tile t;
     if (!find_tile<BM>(c, b, a, p, cut.item, cut.head, t))
         return;
-    const int i = blockIdx.y * 256 + threadIdx.x;  // the piece
-    int row, d;
-    if constexpr (BM == 16) {
-        row = i / (D / 4);
-        d = i % (D / 4) * 4;
-    } else {
-        row = i / (8 * D) * 32 + i % 32;
-        d = i % (8 * D) / 64 * 8 + i % 64 / 32 * 4;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const int r = t.r0 + row[n];
+        if (r >= t.rows)
+            continue;
+        const int query = quotient(r, a.group);
+        const int64_t qrow = t.row0 + t.q0 + query;
+        const int qhead = (t.head - query) * a.group + r;
+        const float l = ml[n][1], inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
+        store_out(a, qrow * a.out_stride + (int64_t)qhead * D + d[n], o[n][0] * inv, o[n][1] * inv,
+                  o[n][2] * inv, o[n][3] * inv);
+        if (a.lse && d[n] == 0)
+            a.lse[qrow * a.q_heads + qhead] = lse_of(ml[n][0], l);
     }
-    const int r = t.r0 + row;
-    if (r >= t.rows)
-        return;
-    // the first part lies in the beginning work-group's second slot, the others in first ones
-    const float *x = partial<BM, D>(a, 2 * w + 1);
-    f2 ml = *(const f2 *)(x + BM * D + 2 * row);
-    f4 o = *(const f4 *)(x + 4 * i);
-    for (int k = 1; k <= cut.more; ++k) {
-        x = partial<BM, D>(a, 2 * (w + k));
-        const f2 n = *(const f2 *)(x + BM * D + 2 * row);
-        const f4 v = *(const f4 *)(x + 4 * i);
-        const float now = fmaxf(ml[0], n[0]);
-        const float e0 = exp2_fast(ml[0] - now), e1 = exp2_fast(n[0] - now);
-        ml = f2{now, ml[1] * e0 + n[1] * e1};
-        o = o * e0 + v * e1;
-    }
-    const int64_t qrow = t.row0 + t.q0 + r / a.group;
-    const int qhead = t.head * a.group + r % a.group;
-    const float l = ml[1], inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
-    store_out(a, qrow * a.out_stride + (int64_t)qhead * D + d, o[0] * inv, o[1] * inv, o[2] * inv,
-              o[3] * inv);
-    if (a.lse && d == 0)
-        a.lse[qrow * a.q_heads + qhead] = lse_of(ml[0], l);
 }
 
 constexpr int64_t kNarrowRows = 32;  // rows of a query block up to which the narrow kernel is taken
@@ -1129,7 +1153,7 @@ Shape shape_of(bool wide, int dim, int64_t rows)
     if (!wide)
         return {16, 256, 512};
     if (rows <= 128)
-        return {128, 256, 512};
+        return dim == 64 ? Shape{128, 128, 1024} : Shape{128, 256, 512};
     return dim == 64 && rows > 256 ? Shape{512, 512, 256} : Shape{256, 512, 256};
 }
 
@@ -1184,8 +1208,10 @@ void attend_as(const Kv8Cache &c, const Kv8Batch &b, const Kv8Attend &a, const K
     const dim3 grid((unsigned)p.groups);
     if (!p.wide)
         kv8_attend_narrow_kernel<F, D><<<grid, 256, 0, st>>>(c, b, a, p);
+    else if (p.rows == 128 && D == 64)
+        kv8_attend_wide_kernel<F, 64, 2, 2, 1><<<grid, 128, 0, st>>>(c, b, a, p);
     else if (p.rows == 128)
-        kv8_attend_wide_kernel<F, D, 4, 1, 2><<<grid, 256, 0, st>>>(c, b, a, p);
+        kv8_attend_wide_kernel<F, 128, 4, 1, 2><<<grid, 256, 0, st>>>(c, b, a, p);
     else if (p.rows == 256)
         kv8_attend_wide_kernel<F, D, 8, 1, 2><<<grid, 512, 0, st>>>(c, b, a, p);
     else
@@ -1196,7 +1222,8 @@ template <int D>
 void join_as(const Kv8Cache &c, const Kv8Batch &b, const Kv8Attend &a, const Kv8Plan &p,
              hipStream_t st)
 {
-    const dim3 grid((unsigned)p.groups, (unsigned)(p.rows * D / 1024));
+    const int pieces = p.rows * D / 1024;  // per thread, over all
+    const dim3 grid((unsigned)p.groups, (unsigned)(pieces < kPieces ? 1 : pieces / kPieces));
     if (p.rows == 512)
         kv8_join_kernel<512, D><<<grid, 256, 0, st>>>(c, b, a, p);
     else if (p.rows == 16)

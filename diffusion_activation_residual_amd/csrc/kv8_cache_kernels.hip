@@ -409,17 +409,21 @@ __device__ inline uint64_t order_key(double s)
 }
 
 // Scores of one query block and KV head against the means of up to kScorePages pages.  The block's
-// queries are summed in fp64 (sums of bf16 or fp16 values; 16 bits more than fp32 where it matters: two
-// pages whose scores differ in the last bit of fp32 keep their order), then each wave takes
-// pages in turn, one lane per D / 64 dimensions.
+// queries are summed in fp64 and the products are too: 64 bits where two pages' scores may differ in
+// the last bit of fp32.  A query row is read by D / 8 lanes (16 bytes each) and a page's mean by 8
+// lanes, so that loads are wide and the sums across lanes short.  Bound by latency (a few dozen KB
+// per work-group).
 constexpr int kScorePages = 64;
 
 template <int D>
 __global__ __launch_bounds__(kThreads) void kv8_score_kernel(Kv8Cache c, Kv8Batch b, Kv8Select a,
                                                              int units, int stride, int chunks)
 {
-    __shared__ double qs[4][D];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    constexpr int LANES = D / 8, ROWS = kThreads / LANES;  // lanes per row, rows at once
+    constexpr int E = D / 8;                               // a lane's dimensions of a mean
+    __shared__ double part[ROWS][D + 2];
+    __shared__ double qs[D];
+    const int tid = threadIdx.x;
     int64_t g = blockIdx.x;
     const int chunk = (int)(g % chunks);
     g /= chunks;
@@ -440,48 +444,73 @@ __global__ __launch_bounds__(kThreads) void kv8_score_kernel(Kv8Cache c, Kv8Batc
     if (chunk * kScorePages >= seen)
         return;
 
-    constexpr int E = D / 64;
-    double sum[E] = {};
-    const int rows = (int)(q1 - q0) * a.group;
-    for (int r = wave; r < rows; r += 4) {
-        const int64_t at = (row0 + q0 + r / a.group) * a.q_stride +
-                           ((int64_t)head * a.group + r % a.group) * D + lane * E;
+    // the means first: they do not wait for the queries
+    constexpr int TURNS = kScorePages * 8 / kThreads;
+    float4 mean[TURNS][E / 4];
+    int page[TURNS];
+    const int sub = tid % 8;
 #pragma unroll
-        for (int j = 0; j < E; ++j)
-            sum[j] += a.f16 ? (float)((const _Float16 *)a.q)[at + j]
-                            : widen(((const uint16_t *)a.q)[at + j]);
+    for (int i = 0; i < TURNS; ++i) {
+        const int p = chunk * kScorePages + i * (kThreads / 8) + tid / 8;
+        page[i] = p < seen ? kv8_page(c, b, seq, p) : -1;
+#pragma unroll
+        for (int j = 0; j < E / 4; ++j)
+            mean[i][j] = page[i] >= 0
+                             ? *(const float4 *)(c.km + ((int64_t)page[i] * c.heads + head) * D +
+                                                 j * 32 + sub * 4)
+                             : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+
+    double sum[8] = {};
+    const int rows = (int)(q1 - q0) * a.group, d0 = tid % LANES * 8;
+#pragma unroll 4
+    for (int r = tid / LANES; r < rows; r += ROWS) {
+        const int query = a.group == 1 ? r : r / a.group;
+        const int64_t at = (row0 + q0 + query) * a.q_stride +
+                           ((int64_t)(head - query) * a.group + r) * D + d0;
+        const uint4 w = *(const uint4 *)((const uint16_t *)a.q + at);
+        const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint16_t lo = (uint16_t)words[j], hi = (uint16_t)(words[j] >> 16);
+            sum[2 * j] += a.f16 ? (float)__builtin_bit_cast(_Float16, lo) : widen(lo);
+            sum[2 * j + 1] += a.f16 ? (float)__builtin_bit_cast(_Float16, hi) : widen(hi);
+        }
     }
 #pragma unroll
-    for (int j = 0; j < E; ++j)
-        qs[wave][lane * E + j] = sum[j];
+    for (int j = 0; j < 8; ++j)
+        part[tid / LANES][d0 + j] = sum[j];
     __syncthreads();
-    double q[E];
-#pragma unroll
-    for (int j = 0; j < E; ++j)
-        q[j] = (qs[0][lane * E + j] + qs[1][lane * E + j]) +
-               (qs[2][lane * E + j] + qs[3][lane * E + j]);
-    double *out = a.ws + list * stride;
-    for (int i = wave; i < kScorePages; i += 4) {
-        const int p = chunk * kScorePages + i;
-        if (p >= seen)
-            break;
-        const int page = kv8_page(c, b, seq, p);
+    if (tid < D) {
         double s = 0.0;
-        if (page >= 0) {
-            const float *m = c.km + ((int64_t)page * c.heads + head) * D + lane * E;
 #pragma unroll
-            for (int j = 0; j < E; ++j)
-                s = fma(q[j], (double)m[j], s);
+        for (int r = 0; r < ROWS; ++r)
+            s += part[r][tid];
+        qs[tid] = s;
+    }
+    __syncthreads();
+    double *out = a.ws + list * stride;
+#pragma unroll
+    for (int i = 0; i < TURNS; ++i) {
+        const int p = chunk * kScorePages + i * (kThreads / 8) + tid / 8;
+        double s = 0.0;
+#pragma unroll
+        for (int j = 0; j < E / 4; ++j) {
+            const double *q = qs + j * 32 + sub * 4;
+            s = fma(q[0], (double)mean[i][j].x, s);
+            s = fma(q[1], (double)mean[i][j].y, s);
+            s = fma(q[2], (double)mean[i][j].z, s);
+            s = fma(q[3], (double)mean[i][j].w, s);
         }
 #pragma unroll
-        for (int d = 32; d >= 1; d >>= 1)
+        for (int d = 4; d >= 1; d >>= 1)
             s += __shfl_xor(s, d);
         uint64_t key = order_key(s);
-        if (page < 0)
+        if (page[i] < 0)
             key = 0;
         else if (p < a.first || p >= seen - a.last)
             key = ~0ull;
-        if (lane == 0)
+        if (sub == 0 && p < seen)
             out[p] = __longlong_as_double((long long)key);
     }
 }

@@ -124,7 +124,7 @@ __device__ inline bool find_tile(const Kv8Cache &c, const Kv8Batch &b, const Kv8
     t.reach_min = reach(t, a.causal, t.q0 + quotient(t.r0, a.group));
     t.reach_max = reach(t, a.causal, t.q0 + quotient(last, a.group));
     const int keys = t.list ? a.count << c.log2page : t.reach_max;
-    t.steps = (keys + kBlock - 1) / kBlock;
+    t.steps = c.pages > 0 ? (keys + kBlock - 1) / kBlock : 0;
     return true;
 }
 
@@ -417,6 +417,8 @@ __global__ __launch_bounds__(256, 2) void kv8_attend_narrow_kernel(Kv8Cache c, K
     constexpr int KL = D / 64;  // 16-byte loads per key row and lane
     constexpr int DT = D / 16;  // tiles of output dimensions
     __shared__ int prefix[kPrefixWords], waves[4];
+    constexpr int AHEAD = 128;  // steps whose pages are looked up together
+    __shared__ Half halves[2 * AHEAD];
     __shared__ float om[4][16], ol[4][16], oo[4][16][D + 4];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
@@ -469,56 +471,43 @@ __global__ __launch_bounds__(256, 2) void kv8_attend_narrow_kernel(Kv8Cache c, K
     const int64_t page_bytes = (int64_t)c.page * D;
     const int kchunk = col >> 2, krow = (col & 3) + 16 * (kchunk & 1);
 
-    struct Step {
-        Half h[2];
-        u4 k[4][KL], v[DT];
-    };
-    auto meta = [&](int s, Step &x) {
+    // A lane's share of a step: 16-byte pieces of 4 key rows and of D / 16 value rows, and the half
+    // that its scores and values belong to.  (Of a half without a page, page 0 is read and nothing of
+    // it used.)
+    u4 kr[4][KL], vr[DT];
+    Half next;
+    const uint32_t koff = krow * D + g * (D / 4), voff = col * c.page + 16 * (g & 1);
+    auto load = [&](int i) {
+        const Half hk = halves[2 * i + (kchunk >> 1)];
+        next = halves[2 * i + (g >> 1)];
+        const uint8_t *kp = c.k + ((int64_t)(hk.page < 0 ? 0 : hk.page) * c.heads + t.head) * page_bytes +
+                            ((hk.tok & (c.page - 1)) * D + koff);
+        const uint8_t *vp = c.v +
+                            ((int64_t)(next.page < 0 ? 0 : next.page) * c.heads + t.head) * page_bytes +
+                            ((next.tok & (c.page - 1)) + voff);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            x.h[i] = find_half(c, b, a, t, s * kBlock + 32 * i, reach_max);
-    };
-    auto load = [&](Step &x) {
-        find_scales(c, t, x.h[0]);
-        find_scales(c, t, x.h[1]);
-        const int pk = x.h[kchunk >> 1].page, pv = x.h[g >> 1].page;
-        const int sk = x.h[kchunk >> 1].tok & (c.page - 1), sv = x.h[g >> 1].tok & (c.page - 1);
-        if (pk >= 0) {
-            const uint8_t *kp = c.k + ((int64_t)pk * c.heads + t.head) * page_bytes +
-                                (sk + krow) * D + g * (D / 4);
+        for (int u = 0; u < 4; ++u)
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+            for (int j = 0; j < KL; ++j)
+                kr[u][j] = *(const u4 *)(kp + u * 4 * D + j * 16);
 #pragma unroll
-                for (int j = 0; j < KL; ++j)
-                    x.k[u][j] = *(const u4 *)(kp + u * 4 * D + j * 16);
-        } else {
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-#pragma unroll
-                for (int j = 0; j < KL; ++j)
-                    x.k[u][j] = u4{0, 0, 0, 0};
-        }
-        if (pv >= 0) {
-            const uint8_t *vp = c.v + ((int64_t)pv * c.heads + t.head) * page_bytes +
-                                col * c.page + sv + 16 * (g & 1);
-#pragma unroll
-            for (int i = 0; i < DT; ++i)
-                x.v[i] = *(const u4 *)(vp + i * 16 * c.page);
-        } else {
-#pragma unroll
-            for (int i = 0; i < DT; ++i)
-                x.v[i] = u4{0, 0, 0, 0};
-        }
+        for (int i = 0; i < DT; ++i)
+            vr[i] = *(const u4 *)(vp + i * 16 * c.page);
     };
 
-    Step x;
-    const int s1 = run.s1;
-    int s = run.s0 + wave;
-    if (s < s1) {
-        meta(s, x);
-        load(x);
+    for (int first = run.s0; first < run.s1; first += AHEAD) {
+    const int last = first + AHEAD < run.s1 ? first + AHEAD : run.s1;
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * (last - first); i += 256) {
+        Half h = find_half(c, b, a, t, first * kBlock + 32 * i, reach_max);
+        find_scales(c, t, h);
+        halves[i] = h;
     }
-    for (; s < s1; s += 4) {
+    __syncthreads();
+    int s = first + wave;
+    if (s < last)
+        load(s - first);
+    for (; s < last; s += 4) {
         // scores
         f4 acc[4];
 #pragma unroll
@@ -526,30 +515,24 @@ __global__ __launch_bounds__(256, 2) void kv8_attend_narrow_kernel(Kv8Cache c, K
             acc[u] = f4{0, 0, 0, 0};
 #pragma unroll
             for (int j = 0; j < KS; ++j) {
-                const u4 w = x.k[u][j / 2];
+                const u4 w = kr[u][j / 2];
                 acc[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
                     to_half8<FMT>(w[j % 2 * 2], w[j % 2 * 2 + 1]), q[j], acc[u], 0, 0, 0);
             }
         }
-        const Half h0 = x.h[0], h1 = x.h[1];
+        const Half h = next;
         u4 v[DT];
 #pragma unroll
         for (int i = 0; i < DT; ++i)
-            v[i] = x.v[i];
-        if (s + 4 < s1) {
-            meta(s + 4, x);
-            load(x);
-        }
-        const Half h = g < 2 ? h0 : h1;
+            v[i] = vr[i];
+        load((s + 4 < last ? s + 4 : s) - first);
         const Factor f = factor(h, qmul);
         const int tok = h.tok + 16 * (g & 1);
-        const bool plain = h0.page >= 0 && h1.page >= 0 && h0.tok + 32 <= reach_min &&
-                           h1.tok + 32 <= reach_min && !flushed(h0) && !flushed(h1);
         float y[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             y[i] = fmaf(acc[i / 4][i % 4], f.mul, f.add);
-        if (!plain) {
+        if (__any(h.page < 0 || h.tok + 32 > reach_min || flushed(h))) {
             const bool none = h.page < 0;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
@@ -591,6 +574,7 @@ __global__ __launch_bounds__(256, 2) void kv8_attend_narrow_kernel(Kv8Cache c, K
             o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(to_half8<FMT>(v[i][2], v[i][3]), w[1],
                                                           o[i], 0, 0, 0);
         }
+    }
     }
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);

@@ -108,7 +108,8 @@ cfz_status check_groups(double groups)
 
 cfz_status check_pages(const cfz::Kv8Cache &c, const cfz::Kv8Batch &b)
 {
-    return check_groups(((double)((b.max_rows + c.page - 1) / c.page) + 1) * c.heads * b.batch);
+    // (append: keys and values each on their own)
+    return check_groups(2 * ((double)((b.max_rows + c.page - 1) / c.page) + 1) * c.heads * b.batch);
 }
 
 // What attend and select share.

@@ -80,193 +80,327 @@ __device__ inline int code_512(uint32_t byte, int fmt)
     return f == f ? (int)f : 0;
 }
 
-__device__ inline double block_max(double x, double *red)
+// Largest of a wave's values, which are not negative (their bits are then ordered as they are), in
+// every lane: neighbours, rows of 16, then across the rows, all by DPP.
+__device__ inline float wave_max(float x)
 {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1)
-        x = fmax(x, __shfl_xor(x, d));
-    if ((threadIdx.x & 63) == 0)
-        red[threadIdx.x >> 6] = x;
-    __syncthreads();
-    x = fmax(fmax(red[0], red[1]), fmax(red[2], red[3]));
-    __syncthreads();
-    return x;
+    uint32_t u = __float_as_uint(x);
+#define CFZ_MAX_STEP(ctrl)                                                                          \
+    {                                                                                              \
+        const uint32_t o = __builtin_amdgcn_update_dpp(0, (int)u, ctrl, 0xf, 0xf, false);          \
+        u = o > u ? o : u;                                                                         \
+    }
+    CFZ_MAX_STEP(0x111)  // row_shr:1
+    CFZ_MAX_STEP(0x112)
+    CFZ_MAX_STEP(0x114)
+    CFZ_MAX_STEP(0x118)
+    CFZ_MAX_STEP(0x142)  // row_bcast:15
+    CFZ_MAX_STEP(0x143)  // row_bcast:31
+#undef CFZ_MAX_STEP
+    return __uint_as_float(__builtin_amdgcn_readlane(u, 63));
 }
 
-// One work-group appends to one page of one head.  Every new element is read once: keys in units of
-// 8 (two groups of 4 that hold whole rotation pairs) kept rotated in fp64 registers, values in
-// 4 tokens x 4 dimensions, transposed in registers and merged into the page's [dim][token]
-// bytes in LDS, so that the page is written in whole 16-byte vectors.  Older tokens are read only where
-// the page keeps some (their codes enter the mean, and change if the scale grows).
-template <class T, int D, int P>
-__global__ __launch_bounds__(kThreads) void kv8_append_kernel(Kv8Cache c, Kv8Batch b, const T *k,
-                                                              const T *v, int64_t k_stride,
-                                                              int64_t v_stride, Kv8Rotation rot,
-                                                              int span)
+// Largest of a work-group's values, N of them at once.
+template <int N> __device__ inline void block_max(float (&x)[N], float *red)
 {
-    constexpr int U = D / 8;                // key units per token
-    constexpr int NK = P * U / kThreads;    // key units per thread
-    constexpr int NV = P * D / 16 / kThreads ? P * D / 16 / kThreads : 1;
-    constexpr int ROW = P / 4 + 1;          // LDS words per dimension of the value page (padded)
-    __shared__ uint32_t vpage[D * ROW];
-    __shared__ int sums[D];
-    __shared__ double red[4];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        x[n] = wave_max(x[n]);
+        if ((threadIdx.x & 63) == 0)
+            red[(threadIdx.x >> 6) * N + n] = x[n];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        x[n] = fmaxf(fmaxf(red[n], red[N + n]), fmaxf(red[2 * N + n], red[3 * N + n]));
+}
 
-    const int tid = threadIdx.x;
-    int64_t g = blockIdx.x;
+// Four codes from approximate quotients y, each within e of the true one: false if one of them lies so
+// near a border between codes that the true code may be another.
+__device__ inline bool quick_codes(const float (&y)[4], float e, int fmt, uint32_t &word,
+                                   float (&value)[4])
+{
+    if (fmt == CFZ_KV8_INT8) {
+        // adding 1.5 2^23 rounds to a whole number (ties to even) and leaves it in the low byte
+        uint32_t b[4];
+        float far = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float t = y[j] + 12582912.0f;
+            b[j] = __float_as_uint(t);
+            value[j] = t - 12582912.0f;
+            far = fmaxf(far, fabsf(y[j] - value[j]));
+        }
+        const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u);
+        const uint32_t hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000c0cu);
+        word = lo | hi;
+        return far < 0.5f - e;
+    }
+    uint32_t below = 0, above = 0;
+    below = __builtin_amdgcn_cvt_pk_fp8_f32(y[0] - e, y[1] - e, below, false);
+    below = __builtin_amdgcn_cvt_pk_fp8_f32(y[2] - e, y[3] - e, below, true);
+    above = __builtin_amdgcn_cvt_pk_fp8_f32(y[0] + e, y[1] + e, above, false);
+    above = __builtin_amdgcn_cvt_pk_fp8_f32(y[2] + e, y[3] + e, above, true);
+    word = above;
+    value[0] = __builtin_amdgcn_cvt_f32_fp8(word, 0);
+    value[1] = __builtin_amdgcn_cvt_f32_fp8(word, 1);
+    value[2] = __builtin_amdgcn_cvt_f32_fp8(word, 2);
+    value[3] = __builtin_amdgcn_cvt_f32_fp8(word, 3);
+    // (a value that rounds to zero from both sides of it is ambiguous too: the zero has a sign)
+    return below == above;
+}
+
+// A page of one head that gets tokens.
+struct Place {
+    int page, lo, hi;  // its new slots, lo .. hi - 1
+    int64_t first;     // its first token in the sequence
+    int64_t src0;      // token row of slot 0
+    int64_t ph;
+};
+
+template <int P>
+__device__ inline bool find_place(const Kv8Cache &c, const Kv8Batch &b, int span, int64_t g,
+                                  Place &p)
+{
     const int at = (int)(g % span);
     g /= span;
     const int head = (int)(g % c.heads);
     const int seq = (int)(g / c.heads);
-
     int row0, n;
     kv8_rows(b, seq, row0, n);
     const int64_t room = (int64_t)b.width * P;
     const int old = kv8_length(b, seq, room);
     const int64_t end = old + (int64_t)n < room ? old + (int64_t)n : room;
-    const int64_t first = ((int64_t)(old / P) + at) * P;  // the page's first token
-    if (first >= end || n == 0)
-        return;
-    const int page = kv8_page(c, b, seq, first / P);
-    if (page < 0)
-        return;
-    const int lo = old > first ? (int)(old - first) : 0;               // first new slot
-    const int hi = end - first < P ? (int)(end - first) : P;           // past the last new slot
-    const int64_t src0 = row0 + (first - old);                         // token row of slot 0
+    p.first = ((int64_t)(old / P) + at) * P;
+    if (p.first >= end || n == 0)
+        return false;
+    p.page = kv8_page(c, b, seq, p.first / P);
+    p.lo = old > p.first ? (int)(old - p.first) : 0;
+    p.hi = end - p.first < P ? (int)(end - p.first) : P;
+    p.src0 = row0 + (p.first - old);
+    p.ph = (int64_t)p.page * c.heads + head;
+    return true;
+}
 
-    const int64_t ph = (int64_t)page * c.heads + head;
-    uint8_t *kp = c.k + ph * (P * D);
-    uint8_t *vp = c.v + ph * (P * D);
+// Appending: one work-group for the keys of a page of one head, another for its values.  Every new
+// element is read once.  Older tokens are read only where the page keeps some (their codes enter the
+// mean, and change if the scale grows).
+//
+// The codes are those of 64-bit quotients, but fp64 is spent only where fp32 cannot decide: fp32
+// quotients come with a bound of their error, and the few units with a quotient that near a
+// border between codes, or with a value that is not finite, are done again in fp64.  Likewise
+// the largest rotated key: only units whose fp32 maximum comes near the work-group's are looked at
+// again.  Bound by the latency of a page's chain of reads and reductions, hence small work-groups
+// with few registers, many on a CU.
+//
+// Keys: units of 8 dimensions (two groups of 4 that hold whole rotation pairs).
+template <class T, int D, int P>
+__device__ inline void append_keys(const Kv8Cache &c, const T *k, int64_t k_stride,
+                                   const Kv8Rotation &rot, const Place &pl, int head)
+{
+    constexpr int U = D / 8;                // key units per token
+    constexpr int NK = P * U / kThreads;    // key units per thread
+    __shared__ int sums[D];
+    __shared__ float red[8];
+    __shared__ unsigned long long top64;
+    const int tid = threadIdx.x, lo = pl.lo, hi = pl.hi;
+    uint8_t *kp = c.k + pl.ph * (P * D);
 
-    // ---- keys: load, rotate
+    // (all units of a thread are of the same dimensions: U divides kThreads)
     const int half = rot.cos ? rot.dim / 2 : 0;
-    double x[NK][8];
-    double kmax = 0.0;
+    const int u = tid % U;
+    const bool turn = 8 * u < 2 * half, split = turn && !rot.interleaved;
+    const int d0 = split ? 4 * u : 8 * u, d1 = split ? half + 4 * u : 8 * u + 4;
+    auto angles = [&](int slot, float4 &cs, float4 &sn) {
+        int64_t pos = rot.pos ? (int64_t)rot.pos[pl.src0 + slot] : pl.first + slot;
+        pos = pos < 0 ? 0 : (pos >= rot.rows ? rot.rows - 1 : pos);
+        // angles 4u .. 4u + 3 in either order of the pairs
+        cs = *(const float4 *)(rot.cos + pos * half + 4 * u);
+        sn = *(const float4 *)(rot.sin + pos * half + 4 * u);
+    };
+    const T *src = k + pl.src0 * k_stride + (int64_t)head * D;
+    float x[NK][8];
+    // largest key, largest product within a rotation; 0 * (NaN or infinity) shows in bad
+    float big[2] = {0.0f, 0.0f}, bad = 0.0f;
 #pragma unroll
     for (int i = 0; i < NK; ++i) {
-        const int unit = tid + i * kThreads, slot = unit / U, u = unit % U;
-        const bool split = half && !rot.interleaved && u < half / 4;
-        const int d0 = split ? 4 * u : 8 * u, d1 = split ? half + 4 * u : 8 * u + 4;
-        if (slot < lo || slot >= hi) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                x[i][j] = 0.0;
-            continue;
+        const int slot = (tid + i * kThreads) / U;
+        float a[4] = {}, e[4] = {};
+        if (slot >= lo && slot < hi) {
+            load4(src + slot * k_stride + d0, a);
+            load4(src + slot * k_stride + d1, e);
         }
-        const T *p = k + (src0 + slot) * k_stride + (int64_t)head * D;
-        float a[4], e[4];
-        load4(p + d0, a);
-        load4(p + d1, e);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             x[i][j] = a[j];
             x[i][4 + j] = e[j];
         }
-        if (8 * u < 2 * half) {
-            int64_t pos = rot.pos ? (int64_t)rot.pos[src0 + slot] : first + slot;
-            pos = pos < 0 ? 0 : (pos >= rot.rows ? rot.rows - 1 : pos);
-            // angles 4u .. 4u + 3 in either order of the pairs
-            const float4 cs = *(const float4 *)(rot.cos + pos * half + 4 * u);
-            const float4 sn = *(const float4 *)(rot.sin + pos * half + 4 * u);
+    }
+    if (turn) {
+#pragma unroll
+        for (int i = 0; i < NK; ++i) {
+            const int slot = (tid + i * kThreads) / U;
+            if (slot < lo || slot >= hi)
+                continue;
+            float4 cs, sn;
+            angles(slot, cs, sn);
             const float cc[4] = {cs.x, cs.y, cs.z, cs.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
+            float r[8];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int p0 = split ? j : 2 * j, p1 = split ? 4 + j : 2 * j + 1;
-                // products of two fp32 values are exact in fp64
-                const double y0 = x[i][p0], y1 = x[i][p1], co = cc[j], si = ss[j];
-                const double r0 = fma(y0, co, -(y1 * si)), r1 = fma(y0, si, y1 * co);
-                if (split) {
-                    x[i][j] = r0;
-                    x[i][4 + j] = r1;
-                } else {
-                    x[i][2 * j] = r0;
-                    x[i][2 * j + 1] = r1;
-                }
+                const float y0 = split ? x[i][j] : x[i][2 * j];
+                const float y1 = split ? x[i][4 + j] : x[i][2 * j + 1];
+                const float t0 = y1 * ss[j], t1 = y1 * cc[j];
+                const float r0 = fmaf(y0, cc[j], -t0), r1 = fmaf(y0, ss[j], t1);
+                big[1] = fmaxf(fmaxf(fabsf(t0), fabsf(t1)), big[1]);
+                r[2 * j] = r0;
+                r[2 * j + 1] = r1;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[i][j] = split ? r[2 * j] : r[j];
+                x[i][4 + j] = split ? r[2 * j + 1] : r[4 + j];
             }
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            kmax = fmax(kmax, finite_or_zero(x[i][j]));
     }
+#pragma unroll
+    for (int i = 0; i < NK; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            big[0] = fmaxf(fmaxf(fabsf(x[i][j]), fabsf(x[i][j + 1])), big[0]);
+            bad = fmaf(x[i][j], 0.0f, fmaf(x[i][j + 1], 0.0f, bad));
+        }
+    // one unit in fp64; products of two fp32 values are exact there
+    auto exact_unit = [&](int slot, double (&y)[8]) {
+        float a[4], e[4];
+        load4(src + slot * k_stride + d0, a);
+        load4(src + slot * k_stride + d1, e);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            y[j] = a[j];
+            y[4 + j] = e[j];
+        }
+        if (turn) {
+            float4 cs, sn;
+            angles(slot, cs, sn);
+            const float cc[4] = {cs.x, cs.y, cs.z, cs.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
+            double r[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const double y0 = split ? y[j] : y[2 * j], y1 = split ? y[4 + j] : y[2 * j + 1];
+                const double co = cc[j], si = ss[j];
+                r[2 * j] = fma(y0, co, -(y1 * si));
+                r[2 * j + 1] = fma(y0, si, y1 * co);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                y[j] = split ? r[2 * j] : r[j];
+                y[4 + j] = split ? r[2 * j + 1] : r[4 + j];
+            }
+        }
+    };
 
-    // ---- values: 4 tokens x 4 dimensions per unit
-    float w[NV][4][4];  // [unit][token][dimension]
-    double vmax = 0.0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int unit = tid + i * kThreads, tq = unit / (D / 4), dq = unit % (D / 4);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const int slot = tq * 4 + t;
-            if (slot >= lo && slot < hi) {
-                load4(v + (src0 + slot) * v_stride + (int64_t)head * D + dq * 4, w[i][t]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    w[i][t][j] = 0.0f;
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                vmax = fmax(vmax, finite_or_zero(w[i][t][j]));
-        }
-    }
-    const double qmax = c.fmt == CFZ_KV8_INT8 ? 127.0 : 448.0;
-    kmax = block_max(kmax, red);
-    vmax = block_max(vmax, red);
-    const float kprior = lo > 0 ? c.ks[ph] : 0.0f, vprior = lo > 0 ? c.vs[ph] : 0.0f;
-    const float kscale = fmaxf(kprior, (float)(kmax / qmax));
-    const float vscale = fmaxf(vprior, (float)(vmax / qmax));
-    const bool kgrown = lo > 0 && kscale > kprior, vgrown = lo > 0 && vscale > vprior;
-    const double krinv = 1.0 / (double)kscale, vrinv = 1.0 / (double)vscale;
-    __syncthreads();  // every thread has read the old scales
-    if (tid == 0) {
-        c.ks[ph] = kscale;
-        c.vs[ph] = vscale;
-    }
-    if (c.km && tid < D)
+    const bool odd = !(bad == 0.0f);
+    if (odd)
+        big[0] = big[1] = 0.0f;
+    if (tid == 0)
+        top64 = 0;
+    if (tid < D)
         sums[tid] = 0;
-
-    // ---- the value page as it is, where bytes of it stay
-    if (lo > 0 || hi < P) {
-        for (int i = tid; i < D * P / 16; i += kThreads) {
-            const uint4 q = ((const uint4 *)vp)[i];
-            uint32_t *o = vpage + (i * 4 / (P / 4)) * ROW + i * 4 % (P / 4);
-            o[0] = q.x, o[1] = q.y, o[2] = q.z, o[3] = q.w;
+    block_max(big, red);
+    {
+        // a rotated value is rounded by half a step of it and of its second product
+        const float near = big[0] - 0x1p-22f * (big[0] + big[1]);
+        uint32_t look = 0;
+#pragma unroll
+        for (int i = 0; i < NK; ++i) {
+            float m = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                m = fmaxf(m, fabsf(x[i][j]));
+            const int slot = (tid + i * kThreads) / U;
+            if ((odd || m >= near) && slot >= lo && slot < hi)
+                look |= 1u << i;
+        }
+        while (look) {
+            const int slot = (tid + __builtin_ctz(look) * kThreads) / U;
+            look &= look - 1;
+            double y[8], m = 0.0;
+            exact_unit(slot, y);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                m = fmax(m, finite_or_zero(y[j]));
+            atomicMax(&top64, (unsigned long long)__double_as_longlong(m));
         }
     }
+    const float prior = lo > 0 ? c.ks[pl.ph] : 0.0f;
     __syncthreads();
+    const double qmax = c.fmt == CFZ_KV8_INT8 ? 127.0 : 448.0;
+    const float scale = fmaxf(prior, (float)(__longlong_as_double((long long)top64) / qmax));
+    const bool grown = lo > 0 && scale > prior;
+    const double rinv = 1.0 / (double)scale;
+    // fp32 quotients: their factor and the bound of their error; outside the middle of fp32's range
+    // (and for scale 0) everything is done in fp64
+    const float quick = (float)rinv;
+    const bool mid = scale > 0x1p-100f && scale < 0x1p100f && !odd;
+    const float err = 0x1p-23f * (big[1] * quick + 2.0f * (float)qmax);
+    if (tid == 0)
+        c.ks[pl.ph] = scale;
 
-    // ---- key codes (all units of a thread are of the same dimensions, since U divides kThreads)
-    int acc[8] = {};
+    float fast[8] = {};  // sums of codes (exact: at most 8 of up to 448 in steps of 2^-9)
+    int acc[8] = {};     // the same times 512, of the units that are done below
+    uint32_t again = 0;  // units for fp64, older tokens among them
 #pragma unroll
     for (int i = 0; i < NK; ++i) {
-        const int unit = tid + i * kThreads, slot = unit / U, u = unit % U;
-        const bool split = half && !rot.interleaved && u < half / 4;
-        const int d0 = split ? 4 * u : 8 * u, d1 = split ? half + 4 * u : 8 * u + 4;
-        if (slot >= hi || (slot < lo && !kgrown && !c.km))
+        const int slot = (tid + i * kThreads) / U;
+        if (slot >= hi || (slot < lo && !grown && !c.km))
             continue;
-        uint32_t *p0 = (uint32_t *)(kp + slot * D + d0), *p1 = (uint32_t *)(kp + slot * D + d1);
+        float y0[4], y1[4], v0[4], v1[4];
         uint32_t w0, w1;
-        if (slot >= lo) {
-            w0 = w1 = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            y0[j] = x[i][j] * quick;
+            y1[j] = x[i][4 + j] * quick;
+        }
+        const bool sure = quick_codes(y0, err, c.fmt, w0, v0) & quick_codes(y1, err, c.fmt, w1, v1);
+        if (slot >= lo && mid && sure) {
+            *(uint32_t *)(kp + slot * D + d0) = w0;
+            *(uint32_t *)(kp + slot * D + d1) = w1;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                w0 |= encode(x[i][j], kscale, krinv, c.fmt) << (8 * j);
-                w1 |= encode(x[i][4 + j], kscale, krinv, c.fmt) << (8 * j);
+                fast[j] += v0[j];
+                fast[4 + j] += v1[j];
+            }
+        } else {
+            again |= 1u << i;
+        }
+    }
+    while (again) {
+        const int slot = (tid + __builtin_ctz(again) * kThreads) / U;
+        again &= again - 1;
+        uint32_t *p0 = (uint32_t *)(kp + slot * D + d0), *p1 = (uint32_t *)(kp + slot * D + d1);
+        uint32_t w0 = 0, w1 = 0;
+        if (slot >= lo) {
+            double y[8];
+            exact_unit(slot, y);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                w0 |= encode(y[j], scale, rinv, c.fmt) << (8 * j);
+                w1 |= encode(y[4 + j], scale, rinv, c.fmt) << (8 * j);
             }
             *p0 = w0;
             *p1 = w1;
         } else {
             w0 = *p0;
             w1 = *p1;
-            if (kgrown) {
+            if (grown) {
                 uint32_t n0 = 0, n1 = 0;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const double o0 = code_value((w0 >> (8 * j)) & 0xff, c.fmt);
                     const double o1 = code_value((w1 >> (8 * j)) & 0xff, c.fmt);
-                    n0 |= encode(o0 * kprior, kscale, krinv, c.fmt) << (8 * j);
-                    n1 |= encode(o1 * kprior, kscale, krinv, c.fmt) << (8 * j);
+                    n0 |= encode(o0 * prior, scale, rinv, c.fmt) << (8 * j);
+                    n1 |= encode(o1 * prior, scale, rinv, c.fmt) << (8 * j);
                 }
                 w0 = n0;
                 w1 = n1;
@@ -280,37 +414,122 @@ __global__ __launch_bounds__(kThreads) void kv8_append_kernel(Kv8Cache c, Kv8Bat
             acc[4 + j] += code_512((w1 >> (8 * j)) & 0xff, c.fmt);
         }
     }
-    if (c.km) {
-        const int u = tid % U;
-        const bool split = half && !rot.interleaved && u < half / 4;
-        const int d0 = split ? 4 * u : 8 * u, d1 = split ? half + 4 * u : 8 * u + 4;
+    if (!c.km)
+        return;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            atomicAdd(&sums[d0 + j], acc[j]);
-            atomicAdd(&sums[d1 + j], acc[4 + j]);
-        }
+    for (int j = 0; j < 4; ++j) {
+        atomicAdd(&sums[d0 + j], acc[j] + (int)(fast[j] * 512.0f));
+        atomicAdd(&sums[d1 + j], acc[4 + j] + (int)(fast[4 + j] * 512.0f));
     }
+    __syncthreads();
+    if (tid < D)
+        c.km[pl.ph * D + tid] = (float)((double)sums[tid] / 512.0 * (double)scale / (double)hi);
+}
 
-    // ---- value codes into the page in LDS
+// Values: units of 4 tokens x 4 dimensions, transposed in registers and merged into the page's
+// [dim][token] bytes in LDS, so that the page is written in whole 16-byte vectors.
+template <class T, int D, int P>
+__device__ inline void append_values(const Kv8Cache &c, const T *v, int64_t v_stride,
+                                     const Place &pl, int head)
+{
+    constexpr int NV = P * D / 16 / kThreads ? P * D / 16 / kThreads : 1;
+    constexpr int ROW = P / 4 + 1;          // LDS words per dimension (padded)
+    __shared__ uint32_t vpage[D * ROW];
+    __shared__ float red[4];
+    const int tid = threadIdx.x, lo = pl.lo, hi = pl.hi;
+    uint8_t *vp = c.v + pl.ph * (P * D);
+    const T *src = v + pl.src0 * v_stride + (int64_t)head * D;
+    float w[NV][4][4];  // [unit][token][dimension]
+    float big[1] = {0.0f}, bad = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int unit = tid + i * kThreads, tq = unit / (D / 4), dq = unit % (D / 4);
-        if (tq >= P / 4 || (tq * 4 >= hi) || (tq * 4 + 4 <= lo && !vgrown))
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int slot = tq * 4 + t;
+            if (slot >= lo && slot < hi) {
+                load4(src + slot * v_stride + dq * 4, w[i][t]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    w[i][t][j] = 0.0f;
+            }
+        }
+    }
+    // the page as it is, where bytes of it stay
+    if (lo > 0 || hi < P) {
+        for (int i = tid; i < D * P / 16; i += kThreads) {
+            const uint4 q = ((const uint4 *)vp)[i];
+            uint32_t *o = vpage + (i * 4 / (P / 4)) * ROW + i * 4 % (P / 4);
+            o[0] = q.x, o[1] = q.y, o[2] = q.z, o[3] = q.w;
+        }
+    }
+    const float prior = lo > 0 ? c.vs[pl.ph] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+                big[0] = fmaxf(fmaxf(fabsf(w[i][t][j]), fabsf(w[i][t][j + 1])), big[0]);
+                bad = fmaf(w[i][t][j], 0.0f, fmaf(w[i][t][j + 1], 0.0f, bad));
+            }
+    // a thread that holds something not finite looks through its values again
+    const bool odd = !(bad == 0.0f);
+    if (odd) {
+        big[0] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    big[0] = fmaxf(big[0],
+                                   fabsf(w[i][t][j]) <= 3.4028234e38f ? fabsf(w[i][t][j]) : 0.0f);
+    }
+    block_max(big, red);
+    const double qmax = c.fmt == CFZ_KV8_INT8 ? 127.0 : 448.0;
+    const float scale = fmaxf(prior, (float)((double)big[0] / qmax));
+    const bool grown = lo > 0 && scale > prior;
+    const double rinv = 1.0 / (double)scale;
+    const float quick = (float)rinv;
+    const bool mid = scale > 0x1p-100f && scale < 0x1p100f && !odd;
+    const float err = 0x1p-23f * (2.0f * (float)qmax);
+    if (tid == 0)
+        c.vs[pl.ph] = scale;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int unit = tid + i * kThreads, tq = unit / (D / 4), dq = unit % (D / 4);
+        if (tq >= P / 4 || (tq * 4 >= hi) || (tq * 4 + 4 <= lo && !grown))
             continue;
+        const bool whole = mid && tq * 4 >= lo && tq * 4 + 4 <= hi;
+        uint32_t rest = 0;  // dimensions for fp64
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+            const float y[4] = {w[i][0][j] * quick, w[i][1][j] * quick, w[i][2][j] * quick,
+                                w[i][3][j] * quick};
+            float unused[4];
+            uint32_t word;
+            if (quick_codes(y, err, c.fmt, word, unused) && whole)
+                vpage[(dq * 4 + j) * ROW + tq] = word;
+            else
+                rest |= 1u << j;
+        }
+        while (rest) {
+            const int j = __builtin_ctz(rest);
+            rest &= rest - 1;
             uint32_t *o = vpage + (dq * 4 + j) * ROW + tq;
             const uint32_t was = *o;
             uint32_t now = 0;
-#pragma unroll
+#pragma unroll 1
             for (int t = 0; t < 4; ++t) {
                 const int slot = tq * 4 + t;
                 const uint32_t byte = (was >> (8 * t)) & 0xff;
                 uint32_t e = byte;
                 if (slot >= lo && slot < hi)
-                    e = encode(w[i][t][j], vscale, vrinv, c.fmt);
-                else if (slot < lo && vgrown)
-                    e = encode((double)code_value(byte, c.fmt) * vprior, vscale, vrinv, c.fmt);
+                    e = encode(widen(src[slot * v_stride + dq * 4 + j]), scale, rinv, c.fmt);
+                else if (slot < lo && grown)
+                    e = encode((double)code_value(byte, c.fmt) * prior, scale, rinv, c.fmt);
                 now |= e << (8 * t);
             }
             *o = now;
@@ -321,8 +540,23 @@ __global__ __launch_bounds__(kThreads) void kv8_append_kernel(Kv8Cache c, Kv8Bat
         const uint32_t *o = vpage + (i * 4 / (P / 4)) * ROW + i * 4 % (P / 4);
         ((uint4 *)vp)[i] = make_uint4(o[0], o[1], o[2], o[3]);
     }
-    if (c.km && tid < D)
-        c.km[ph * D + tid] = (float)((double)sums[tid] / 512.0 * (double)kscale / (double)hi);
+}
+
+template <class T, int D, int P>
+__global__ __launch_bounds__(kThreads) void kv8_append_kernel(Kv8Cache c, Kv8Batch b, const T *k,
+                                                              const T *v, int64_t k_stride,
+                                                              int64_t v_stride, Kv8Rotation rot,
+                                                              int span)
+{
+    Place pl;
+    const int64_t g = blockIdx.x / 2;
+    if (!find_place<P>(c, b, span, g, pl) || pl.page < 0)
+        return;
+    const int head = (int)(g / span % c.heads);
+    if (blockIdx.x & 1)
+        append_values<T, D, P>(c, v, v_stride, pl, head);
+    else
+        append_keys<T, D, P>(c, k, k_stride, rot, pl, head);
 }
 
 // Reads one page of one head back: keys straight, values through LDS (their codes are dimension-major),
@@ -631,7 +865,7 @@ hipError_t append_as(const Kv8Cache &c, const Kv8Batch &b, const void *k, const 
                      int64_t ks, int64_t vs, const Kv8Rotation &rot, hipStream_t st)
 {
     int span;
-    const dim3 grid((unsigned)page_groups(c, b, span));
+    const dim3 grid((unsigned)(2 * page_groups(c, b, span)));
 #define CFZ_KV8_CASE(D, P)                                                                         \
     if (c.dim == D && c.page == P)                                                                 \
         kv8_append_kernel<T, D, P><<<grid, kThreads, 0, st>>>(c, b, (const T *)k, (const T *)v, ks, \

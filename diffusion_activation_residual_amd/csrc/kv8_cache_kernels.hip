@@ -3,6 +3,8 @@
 
 #include <math.h>
 
+#include <type_traits>
+
 namespace cfz {
 namespace {
 
@@ -25,6 +27,24 @@ template <class T> __device__ inline void load4(const T *p, float (&o)[4])
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         o[i] = widen(f.v[i]);
+}
+
+// 8 values: two groups of 4, in one 16-byte load where they are 16 bytes side by side.
+template <class T> __device__ inline void load8(const T *p0, const T *p1, bool split, float (&a)[4],
+                                                float (&e)[4])
+{
+    if (sizeof(T) == 2 && !split) {
+        struct alignas(16) Eight { T v[8]; };
+        const Eight f = *(const Eight *)p0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[i] = widen(f.v[i]);
+            e[i] = widen(f.v[4 + i]);
+        }
+    } else {
+        load4(p0, a);
+        load4(p1, e);
+    }
 }
 
 __device__ inline void narrow(float f, float &o) { o = f; }
@@ -72,14 +92,6 @@ __device__ inline float code_value(uint32_t byte, int fmt)
     return __builtin_amdgcn_cvt_f32_fp8((int)byte, 0);
 }
 
-// The code times 512: a whole number in both formats (e4m3 steps are 2^-9 and up), so that sums of
-// codes are exact in any order.  A byte that is no code (unwritten memory) counts as 0.
-__device__ inline int code_512(uint32_t byte, int fmt)
-{
-    const float f = code_value(byte, fmt) * 512.0f;
-    return f == f ? (int)f : 0;
-}
-
 // Largest of a wave's values, which are not negative (their bits are then ordered as they are), in
 // every lane: neighbours, rows of 16, then across the rows, all by DPP.
 __device__ inline float wave_max(float x)
@@ -100,54 +112,77 @@ __device__ inline float wave_max(float x)
     return __uint_as_float(__builtin_amdgcn_readlane(u, 63));
 }
 
-// Largest of a work-group's values, N of them at once.
-template <int N> __device__ inline void block_max(float (&x)[N], float *red)
+__device__ inline double wave_max(double x)
 {
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-        x[n] = wave_max(x[n]);
-        if ((threadIdx.x & 63) == 0)
-            red[(threadIdx.x >> 6) * N + n] = x[n];
+#define CFZ_MAX_STEP(ctrl)                                                                          \
+    {                                                                                              \
+        const int lo = __builtin_amdgcn_update_dpp(0, __double2loint(x), ctrl, 0xf, 0xf, false);   \
+        const int hi = __builtin_amdgcn_update_dpp(0, __double2hiint(x), ctrl, 0xf, 0xf, false);   \
+        x = fmax(x, __hiloint2double(hi, lo));                                                     \
     }
-    __syncthreads();
-#pragma unroll
-    for (int n = 0; n < N; ++n)
-        x[n] = fmaxf(fmaxf(red[n], red[N + n]), fmaxf(red[2 * N + n], red[3 * N + n]));
+    CFZ_MAX_STEP(0x111)
+    CFZ_MAX_STEP(0x112)
+    CFZ_MAX_STEP(0x114)
+    CFZ_MAX_STEP(0x118)
+    CFZ_MAX_STEP(0x142)
+    CFZ_MAX_STEP(0x143)
+#undef CFZ_MAX_STEP
+    return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(x), 63),
+                            __builtin_amdgcn_readlane(__double2loint(x), 63));
 }
 
-// Four codes from approximate quotients y, each within e of the true one: false if one of them lies so
-// near a border between codes that the true code may be another.
-__device__ inline bool quick_codes(const float (&y)[4], float e, int fmt, uint32_t &word,
-                                   float (&value)[4])
+// Largest of a work-group's values (not negative).
+template <class T> __device__ inline T block_max(T x, T *red)
+{
+    x = wave_max(x);
+    if ((threadIdx.x & 63) == 0)
+        red[threadIdx.x >> 6] = x;
+    __syncthreads();
+    return fmax(fmax(red[0], red[1]), fmax(red[2], red[3]));
+}
+
+// The same for four finite x whose magnitudes are at most a step of fp32 above the largest code
+// times s, and s within 2^-100 .. 2^100: nothing to cut off, no remainder lost.
+__device__ inline uint32_t encode4(const double (&x)[4], double s, double rinv, int fmt)
+{
+    double y[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        y[j] = x[j] * rinv;
+        y[j] = fma(fma(-y[j], s, x[j]), rinv, y[j]);
+    }
+    if (fmt == CFZ_KV8_INT8) {
+        // adding 1.5 2^52 rounds to a whole number (ties to even) and leaves it in the low byte
+        uint32_t b[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            b[j] = (uint32_t)__double2loint(y[j] + 6755399441055744.0);
+        return __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u) |
+               __builtin_amdgcn_perm(b[3], b[2], 0x04000c0cu);
+    }
+    float f[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        y[j] = copysign(y[j], x[j]);
+        f[j] = (float)__hiloint2double(__double2hiint(y[j]) | (__double2loint(y[j]) != 0 ? 1 : 0), 0);
+    }
+    uint32_t w = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
+    return __builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], w, true);
+}
+
+// Adds the four codes' values to four sums.
+__device__ inline void add_values(uint32_t w, int fmt, float *sum)
 {
     if (fmt == CFZ_KV8_INT8) {
-        // adding 1.5 2^23 rounds to a whole number (ties to even) and leaves it in the low byte
-        uint32_t b[4];
-        float far = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float t = y[j] + 12582912.0f;
-            b[j] = __float_as_uint(t);
-            value[j] = t - 12582912.0f;
-            far = fmaxf(far, fabsf(y[j] - value[j]));
-        }
-        const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u);
-        const uint32_t hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000c0cu);
-        word = lo | hi;
-        return far < 0.5f - e;
+        for (int j = 0; j < 4; ++j)
+            sum[j] += (float)(int)(int8_t)(uint8_t)(w >> (8 * j));
+    } else {
+        sum[0] += __builtin_amdgcn_cvt_f32_fp8(w, 0);
+        sum[1] += __builtin_amdgcn_cvt_f32_fp8(w, 1);
+        sum[2] += __builtin_amdgcn_cvt_f32_fp8(w, 2);
+        sum[3] += __builtin_amdgcn_cvt_f32_fp8(w, 3);
     }
-    uint32_t below = 0, above = 0;
-    below = __builtin_amdgcn_cvt_pk_fp8_f32(y[0] - e, y[1] - e, below, false);
-    below = __builtin_amdgcn_cvt_pk_fp8_f32(y[2] - e, y[3] - e, below, true);
-    above = __builtin_amdgcn_cvt_pk_fp8_f32(y[0] + e, y[1] + e, above, false);
-    above = __builtin_amdgcn_cvt_pk_fp8_f32(y[2] + e, y[3] + e, above, true);
-    word = above;
-    value[0] = __builtin_amdgcn_cvt_f32_fp8(word, 0);
-    value[1] = __builtin_amdgcn_cvt_f32_fp8(word, 1);
-    value[2] = __builtin_amdgcn_cvt_f32_fp8(word, 2);
-    value[3] = __builtin_amdgcn_cvt_f32_fp8(word, 3);
-    // (a value that rounds to zero from both sides of it is ambiguous too: the zero has a sign)
-    return below == above;
 }
 
 // A page of one head that gets tokens.
@@ -162,10 +197,11 @@ template <int P>
 __device__ inline bool find_place(const Kv8Cache &c, const Kv8Batch &b, int span, int64_t g,
                                   Place &p)
 {
-    const int at = (int)(g % span);
-    g /= span;
+    // heads first: work-groups that run together then read whole token rows
     const int head = (int)(g % c.heads);
-    const int seq = (int)(g / c.heads);
+    g /= c.heads;
+    const int at = (int)(g % span);
+    const int seq = (int)(g / span);
     int row0, n;
     kv8_rows(b, seq, row0, n);
     const int64_t room = (int64_t)b.width * P;
@@ -184,215 +220,132 @@ __device__ inline bool find_place(const Kv8Cache &c, const Kv8Batch &b, int span
 
 // Appending: one work-group for the keys of a page of one head, another for its values.  Every new
 // element is read once.  Older tokens are read only where the page keeps some (their codes enter the
-// mean, and change if the scale grows).
-//
-// The codes are those of 64-bit quotients, but fp64 is spent only where fp32 cannot decide: fp32
-// quotients come with a bound of their error, and the few units with a quotient that near a
-// border between codes, or with a value that is not finite, are done again in fp64.  Likewise
-// the largest rotated key: only units whose fp32 maximum comes near the work-group's are looked at
-// again.  Bound by the latency of a page's chain of reads and reductions, hence small work-groups
-// with few registers, many on a CU.
+// mean, and change if the scale grows).  Rotation and quotients are in fp64: a product by 1 / s alone
+// loses ties (49 (1 / 49) < 1), with the remainder put right it is the rounded quotient.  What is not
+// finite, and scales far from 1, take a slower way.  fp32 with a test for quotients near a border,
+// and fp64 for those alone, was slower (130 against 105 us on 4 x 4388 tokens x 30 heads of 64, bf16):
+// values of 8 bits lie near one time and again.
 //
 // Keys: units of 8 dimensions (two groups of 4 that hold whole rotation pairs).
-template <class T, int D, int P>
+template <class T, int D, int P, bool ROT>
 __device__ inline void append_keys(const Kv8Cache &c, const T *k, int64_t k_stride,
                                    const Kv8Rotation &rot, const Place &pl, int head)
 {
     constexpr int U = D / 8;                // key units per token
     constexpr int NK = P * U / kThreads;    // key units per thread
+    using Held = std::conditional_t<ROT, double, float>;  // what holds a key exactly
     __shared__ int sums[D];
-    __shared__ float red[8];
-    __shared__ unsigned long long top64;
+    __shared__ Held red[4];
     const int tid = threadIdx.x, lo = pl.lo, hi = pl.hi;
     uint8_t *kp = c.k + pl.ph * (P * D);
 
     // (all units of a thread are of the same dimensions: U divides kThreads)
-    const int half = rot.cos ? rot.dim / 2 : 0;
+    const int half = ROT ? rot.dim / 2 : 0;
     const int u = tid % U;
     const bool turn = 8 * u < 2 * half, split = turn && !rot.interleaved;
     const int d0 = split ? 4 * u : 8 * u, d1 = split ? half + 4 * u : 8 * u + 4;
-    auto angles = [&](int slot, float4 &cs, float4 &sn) {
-        int64_t pos = rot.pos ? (int64_t)rot.pos[pl.src0 + slot] : pl.first + slot;
-        pos = pos < 0 ? 0 : (pos >= rot.rows ? rot.rows - 1 : pos);
-        // angles 4u .. 4u + 3 in either order of the pairs
-        cs = *(const float4 *)(rot.cos + pos * half + 4 * u);
-        sn = *(const float4 *)(rot.sin + pos * half + 4 * u);
-    };
     const T *src = k + pl.src0 * k_stride + (int64_t)head * D;
-    float x[NK][8];
-    // largest key, largest product within a rotation; 0 * (NaN or infinity) shows in bad
-    float big[2] = {0.0f, 0.0f}, bad = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NK; ++i) {
-        const int slot = (tid + i * kThreads) / U;
-        float a[4] = {}, e[4] = {};
-        if (slot >= lo && slot < hi) {
-            load4(src + slot * k_stride + d0, a);
-            load4(src + slot * k_stride + d1, e);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[i][j] = a[j];
-            x[i][4 + j] = e[j];
-        }
-    }
-    if (turn) {
+    if (tid < D)
+        sums[tid] = 0;
+    const float prior = lo > 0 ? c.ks[pl.ph] : 0.0f;
+    Held x[NK][8];
+    Held big = 0;
+    float bad = 0.0f;  // 0 * (NaN or infinity) shows here
+    {
+        float a[NK][8];
+        float4 cs[ROT ? NK : 1], sn[ROT ? NK : 1];
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
             const int slot = (tid + i * kThreads) / U;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                a[i][j] = 0.0f;
+            if constexpr (ROT)
+                cs[i] = sn[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             if (slot < lo || slot >= hi)
                 continue;
-            float4 cs, sn;
-            angles(slot, cs, sn);
-            const float cc[4] = {cs.x, cs.y, cs.z, cs.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
-            float r[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float y0 = split ? x[i][j] : x[i][2 * j];
-                const float y1 = split ? x[i][4 + j] : x[i][2 * j + 1];
-                const float t0 = y1 * ss[j], t1 = y1 * cc[j];
-                const float r0 = fmaf(y0, cc[j], -t0), r1 = fmaf(y0, ss[j], t1);
-                big[1] = fmaxf(fmaxf(fabsf(t0), fabsf(t1)), big[1]);
-                r[2 * j] = r0;
-                r[2 * j + 1] = r1;
+            load8(src + slot * k_stride + d0, src + slot * k_stride + d1, split,
+                  *(float(*)[4]) & a[i][0], *(float(*)[4]) & a[i][4]);
+            if constexpr (ROT) {
+                if (turn) {
+                    int64_t pos = rot.pos ? (int64_t)rot.pos[pl.src0 + slot] : pl.first + slot;
+                    pos = pos < 0 ? 0 : (pos >= rot.rows ? rot.rows - 1 : pos);
+                    // angles 4u .. 4u + 3 in either order of the pairs
+                    cs[i] = *(const float4 *)(rot.cos + pos * half + 4 * u);
+                    sn[i] = *(const float4 *)(rot.sin + pos * half + 4 * u);
+                }
             }
+        }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[i][j] = split ? r[2 * j] : r[j];
-                x[i][4 + j] = split ? r[2 * j + 1] : r[4 + j];
+        for (int i = 0; i < NK; ++i) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                x[i][j] = a[i][j];
+                bad = fmaf(a[i][j], 0.0f, bad);
+            }
+            if constexpr (ROT) {
+                if (turn) {
+                    const float cc[4] = {cs[i].x, cs[i].y, cs[i].z, cs[i].w};
+                    const float ss[4] = {sn[i].x, sn[i].y, sn[i].z, sn[i].w};
+                    double r[8];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        // products of two fp32 values are exact in fp64
+                        const double y0 = split ? a[i][j] : a[i][2 * j];
+                        const double y1 = split ? a[i][4 + j] : a[i][2 * j + 1];
+                        const double co = cc[j], si = ss[j];
+                        bad = fmaf(cc[j], 0.0f, fmaf(ss[j], 0.0f, bad));
+                        r[2 * j] = fma(y0, co, -(y1 * si));
+                        r[2 * j + 1] = fma(y0, si, y1 * co);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        x[i][j] = split ? r[2 * j] : r[j];
+                        x[i][4 + j] = split ? r[2 * j + 1] : r[4 + j];
+                    }
+                }
             }
         }
     }
+    const bool odd = !(bad == 0.0f);
 #pragma unroll
     for (int i = 0; i < NK; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            big[0] = fmaxf(fmaxf(fabsf(x[i][j]), fabsf(x[i][j + 1])), big[0]);
-            bad = fmaf(x[i][j], 0.0f, fmaf(x[i][j + 1], 0.0f, bad));
-        }
-    // one unit in fp64; products of two fp32 values are exact there
-    auto exact_unit = [&](int slot, double (&y)[8]) {
-        float a[4], e[4];
-        load4(src + slot * k_stride + d0, a);
-        load4(src + slot * k_stride + d1, e);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            y[j] = a[j];
-            y[4 + j] = e[j];
-        }
-        if (turn) {
-            float4 cs, sn;
-            angles(slot, cs, sn);
-            const float cc[4] = {cs.x, cs.y, cs.z, cs.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
-            double r[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const double y0 = split ? y[j] : y[2 * j], y1 = split ? y[4 + j] : y[2 * j + 1];
-                const double co = cc[j], si = ss[j];
-                r[2 * j] = fma(y0, co, -(y1 * si));
-                r[2 * j + 1] = fma(y0, si, y1 * co);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                y[j] = split ? r[2 * j] : r[j];
-                y[4 + j] = split ? r[2 * j + 1] : r[4 + j];
-            }
-        }
-    };
-
-    const bool odd = !(bad == 0.0f);
-    if (odd)
-        big[0] = big[1] = 0.0f;
-    if (tid == 0)
-        top64 = 0;
-    if (tid < D)
-        sums[tid] = 0;
-    block_max(big, red);
-    {
-        // a rotated value is rounded by half a step of it and of its second product
-        const float near = big[0] - 0x1p-22f * (big[0] + big[1]);
-        uint32_t look = 0;
-#pragma unroll
-        for (int i = 0; i < NK; ++i) {
-            float m = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                m = fmaxf(m, fabsf(x[i][j]));
-            const int slot = (tid + i * kThreads) / U;
-            if ((odd || m >= near) && slot >= lo && slot < hi)
-                look |= 1u << i;
-        }
-        while (look) {
-            const int slot = (tid + __builtin_ctz(look) * kThreads) / U;
-            look &= look - 1;
-            double y[8], m = 0.0;
-            exact_unit(slot, y);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                m = fmax(m, finite_or_zero(y[j]));
-            atomicMax(&top64, (unsigned long long)__double_as_longlong(m));
-        }
-    }
-    const float prior = lo > 0 ? c.ks[pl.ph] : 0.0f;
-    __syncthreads();
+        for (int j = 0; j < 8; ++j)
+            big = fmax(big, odd ? (Held)finite_or_zero(x[i][j]) : (Held)fabs(x[i][j]));
+    big = block_max(big, red);
     const double qmax = c.fmt == CFZ_KV8_INT8 ? 127.0 : 448.0;
-    const float scale = fmaxf(prior, (float)(__longlong_as_double((long long)top64) / qmax));
+    const float scale = fmaxf(prior, (float)((double)big / qmax));
     const bool grown = lo > 0 && scale > prior;
     const double rinv = 1.0 / (double)scale;
-    // fp32 quotients: their factor and the bound of their error; outside the middle of fp32's range
-    // (and for scale 0) everything is done in fp64
-    const float quick = (float)rinv;
     const bool mid = scale > 0x1p-100f && scale < 0x1p100f && !odd;
-    const float err = 0x1p-23f * (big[1] * quick + 2.0f * (float)qmax);
     if (tid == 0)
         c.ks[pl.ph] = scale;
 
     float fast[8] = {};  // sums of codes (exact: at most 8 of up to 448 in steps of 2^-9)
-    int acc[8] = {};     // the same times 512, of the units that are done below
-    uint32_t again = 0;  // units for fp64, older tokens among them
 #pragma unroll
     for (int i = 0; i < NK; ++i) {
         const int slot = (tid + i * kThreads) / U;
         if (slot >= hi || (slot < lo && !grown && !c.km))
             continue;
-        float y0[4], y1[4], v0[4], v1[4];
         uint32_t w0, w1;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            y0[j] = x[i][j] * quick;
-            y1[j] = x[i][4 + j] * quick;
-        }
-        const bool sure = quick_codes(y0, err, c.fmt, w0, v0) & quick_codes(y1, err, c.fmt, w1, v1);
-        if (slot >= lo && mid && sure) {
-            *(uint32_t *)(kp + slot * D + d0) = w0;
-            *(uint32_t *)(kp + slot * D + d1) = w1;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                fast[j] += v0[j];
-                fast[4 + j] += v1[j];
-            }
-        } else {
-            again |= 1u << i;
-        }
-    }
-    while (again) {
-        const int slot = (tid + __builtin_ctz(again) * kThreads) / U;
-        again &= again - 1;
-        uint32_t *p0 = (uint32_t *)(kp + slot * D + d0), *p1 = (uint32_t *)(kp + slot * D + d1);
-        uint32_t w0 = 0, w1 = 0;
         if (slot >= lo) {
-            double y[8];
-            exact_unit(slot, y);
+            if (mid) {
+                const double x0[4] = {x[i][0], x[i][1], x[i][2], x[i][3]};
+                const double x1[4] = {x[i][4], x[i][5], x[i][6], x[i][7]};
+                w0 = encode4(x0, scale, rinv, c.fmt);
+                w1 = encode4(x1, scale, rinv, c.fmt);
+            } else {
+                w0 = w1 = 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                w0 |= encode(y[j], scale, rinv, c.fmt) << (8 * j);
-                w1 |= encode(y[4 + j], scale, rinv, c.fmt) << (8 * j);
+                for (int j = 0; j < 4; ++j) {
+                    w0 |= encode(x[i][j], scale, rinv, c.fmt) << (8 * j);
+                    w1 |= encode(x[i][4 + j], scale, rinv, c.fmt) << (8 * j);
+                }
             }
-            *p0 = w0;
-            *p1 = w1;
         } else {
-            w0 = *p0;
-            w1 = *p1;
+            w0 = *(const uint32_t *)(kp + slot * D + d0);
+            w1 = *(const uint32_t *)(kp + slot * D + d1);
             if (grown) {
                 uint32_t n0 = 0, n1 = 0;
 #pragma unroll
@@ -404,56 +357,65 @@ __device__ inline void append_keys(const Kv8Cache &c, const T *k, int64_t k_stri
                 }
                 w0 = n0;
                 w1 = n1;
-                *p0 = w0;
-                *p1 = w1;
             }
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            acc[j] += code_512((w0 >> (8 * j)) & 0xff, c.fmt);
-            acc[4 + j] += code_512((w1 >> (8 * j)) & 0xff, c.fmt);
+        if (slot >= lo || grown) {
+            if (split) {
+                *(uint32_t *)(kp + slot * D + d0) = w0;
+                *(uint32_t *)(kp + slot * D + d1) = w1;
+            } else {
+                *(uint2 *)(kp + slot * D + d0) = make_uint2(w0, w1);
+            }
         }
+        add_values(w0, c.fmt, fast);
+        add_values(w1, c.fmt, fast + 4);
     }
     if (!c.km)
         return;
+    // 512 times a sum of codes is a whole number: exact in any order
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        atomicAdd(&sums[d0 + j], acc[j] + (int)(fast[j] * 512.0f));
-        atomicAdd(&sums[d1 + j], acc[4 + j] + (int)(fast[4 + j] * 512.0f));
+        atomicAdd(&sums[d0 + j], (int)(fast[j] * 512.0f));
+        atomicAdd(&sums[d1 + j], (int)(fast[4 + j] * 512.0f));
     }
     __syncthreads();
     if (tid < D)
         c.km[pl.ph * D + tid] = (float)((double)sums[tid] / 512.0 * (double)scale / (double)hi);
 }
 
-// Values: units of 4 tokens x 4 dimensions, transposed in registers and merged into the page's
+// Values: units of 4 tokens x 8 dimensions (4 in the smallest page), transposed in registers and merged into the page's
 // [dim][token] bytes in LDS, so that the page is written in whole 16-byte vectors.
 template <class T, int D, int P>
 __device__ inline void append_values(const Kv8Cache &c, const T *v, int64_t v_stride,
                                      const Place &pl, int head)
 {
-    constexpr int NV = P * D / 16 / kThreads ? P * D / 16 / kThreads : 1;
+    constexpr int W = P * D >= 32 * kThreads ? 8 : 4;  // dimensions of a unit
+    constexpr int NV = P * D / (4 * W) / kThreads ? P * D / (4 * W) / kThreads : 1;
     constexpr int ROW = P / 4 + 1;          // LDS words per dimension (padded)
     __shared__ uint32_t vpage[D * ROW];
     __shared__ float red[4];
     const int tid = threadIdx.x, lo = pl.lo, hi = pl.hi;
     uint8_t *vp = c.v + pl.ph * (P * D);
     const T *src = v + pl.src0 * v_stride + (int64_t)head * D;
-    float w[NV][4][4];  // [unit][token][dimension]
-    float big[1] = {0.0f}, bad = 0.0f;
+    float w[NV][4][W];  // [unit][token][dimension]
+    float big = 0.0f, bad = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int unit = tid + i * kThreads, tq = unit / (D / 4), dq = unit % (D / 4);
+        const int unit = tid + i * kThreads, tq = unit / (D / W), dq = unit % (D / W);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const int slot = tq * 4 + t;
+            float a[4] = {}, e[4] = {};
             if (slot >= lo && slot < hi) {
-                load4(src + slot * v_stride + dq * 4, w[i][t]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    w[i][t][j] = 0.0f;
+                const T *p = src + slot * v_stride + dq * W;
+                if (W == 8)
+                    load8(p, p + 4, false, a, e);
+                else
+                    load4(p, a);
             }
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+                w[i][t][j] = j < 4 ? a[j & 3] : e[j & 3];
         }
     }
     // the page as it is, where bytes of it stay
@@ -470,69 +432,60 @@ __device__ inline void append_values(const Kv8Cache &c, const T *v, int64_t v_st
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int j = 0; j < 4; j += 2) {
-                big[0] = fmaxf(fmaxf(fabsf(w[i][t][j]), fabsf(w[i][t][j + 1])), big[0]);
+            for (int j = 0; j < W; j += 2) {
+                big = fmaxf(fmaxf(fabsf(w[i][t][j]), fabsf(w[i][t][j + 1])), big);
                 bad = fmaf(w[i][t][j], 0.0f, fmaf(w[i][t][j + 1], 0.0f, bad));
             }
     // a thread that holds something not finite looks through its values again
     const bool odd = !(bad == 0.0f);
     if (odd) {
-        big[0] = 0.0f;
+        big = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    big[0] = fmaxf(big[0],
+                for (int j = 0; j < W; ++j)
+                    big = fmaxf(big,
                                    fabsf(w[i][t][j]) <= 3.4028234e38f ? fabsf(w[i][t][j]) : 0.0f);
     }
-    block_max(big, red);
+    big = block_max(big, red);
     const double qmax = c.fmt == CFZ_KV8_INT8 ? 127.0 : 448.0;
-    const float scale = fmaxf(prior, (float)((double)big[0] / qmax));
+    const float scale = fmaxf(prior, (float)((double)big / qmax));
     const bool grown = lo > 0 && scale > prior;
     const double rinv = 1.0 / (double)scale;
-    const float quick = (float)rinv;
     const bool mid = scale > 0x1p-100f && scale < 0x1p100f && !odd;
-    const float err = 0x1p-23f * (2.0f * (float)qmax);
     if (tid == 0)
         c.vs[pl.ph] = scale;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int unit = tid + i * kThreads, tq = unit / (D / 4), dq = unit % (D / 4);
+        const int unit = tid + i * kThreads, tq = unit / (D / W), dq = unit % (D / W);
         if (tq >= P / 4 || (tq * 4 >= hi) || (tq * 4 + 4 <= lo && !grown))
             continue;
-        const bool whole = mid && tq * 4 >= lo && tq * 4 + 4 <= hi;
-        uint32_t rest = 0;  // dimensions for fp64
+        uint32_t *o = vpage + dq * W * ROW + tq;
+        if (mid && tq * 4 >= lo && tq * 4 + 4 <= hi) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float y[4] = {w[i][0][j] * quick, w[i][1][j] * quick, w[i][2][j] * quick,
-                                w[i][3][j] * quick};
-            float unused[4];
-            uint32_t word;
-            if (quick_codes(y, err, c.fmt, word, unused) && whole)
-                vpage[(dq * 4 + j) * ROW + tq] = word;
-            else
-                rest |= 1u << j;
-        }
-        while (rest) {
-            const int j = __builtin_ctz(rest);
-            rest &= rest - 1;
-            uint32_t *o = vpage + (dq * 4 + j) * ROW + tq;
-            const uint32_t was = *o;
-            uint32_t now = 0;
-#pragma unroll 1
-            for (int t = 0; t < 4; ++t) {
-                const int slot = tq * 4 + t;
-                const uint32_t byte = (was >> (8 * t)) & 0xff;
-                uint32_t e = byte;
-                if (slot >= lo && slot < hi)
-                    e = encode(widen(src[slot * v_stride + dq * 4 + j]), scale, rinv, c.fmt);
-                else if (slot < lo && grown)
-                    e = encode((double)code_value(byte, c.fmt) * prior, scale, rinv, c.fmt);
-                now |= e << (8 * t);
+            for (int j = 0; j < W; ++j) {
+                const double x[4] = {w[i][0][j], w[i][1][j], w[i][2][j], w[i][3][j]};
+                o[j * ROW] = encode4(x, scale, rinv, c.fmt);
             }
-            *o = now;
+            continue;
+        }
+#pragma unroll 1
+        for (int t = 0; t < 4; ++t) {
+            const int slot = tq * 4 + t;
+            if (slot >= hi || (slot < lo && !grown))
+                continue;
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                const uint32_t was = o[j * ROW];
+                const double y = slot >= lo ? (double)(t == 0   ? w[i][0][j]
+                                                       : t == 1 ? w[i][1][j]
+                                                       : t == 2 ? w[i][2][j]
+                                                                : w[i][3][j])
+                                            : (double)code_value((was >> (8 * t)) & 0xff, c.fmt) * prior;
+                o[j * ROW] = (was & ~(0xffu << (8 * t))) | encode(y, scale, rinv, c.fmt) << (8 * t);
+            }
         }
     }
     __syncthreads();
@@ -542,7 +495,7 @@ __device__ inline void append_values(const Kv8Cache &c, const T *v, int64_t v_st
     }
 }
 
-template <class T, int D, int P>
+template <class T, int D, int P, bool ROT>
 __global__ __launch_bounds__(kThreads) void kv8_append_kernel(Kv8Cache c, Kv8Batch b, const T *k,
                                                               const T *v, int64_t k_stride,
                                                               int64_t v_stride, Kv8Rotation rot,
@@ -552,11 +505,11 @@ __global__ __launch_bounds__(kThreads) void kv8_append_kernel(Kv8Cache c, Kv8Bat
     const int64_t g = blockIdx.x / 2;
     if (!find_place<P>(c, b, span, g, pl) || pl.page < 0)
         return;
-    const int head = (int)(g / span % c.heads);
+    const int head = (int)(g % c.heads);
     if (blockIdx.x & 1)
         append_values<T, D, P>(c, v, v_stride, pl, head);
     else
-        append_keys<T, D, P>(c, k, k_stride, rot, pl, head);
+        append_keys<T, D, P, ROT>(c, k, k_stride, rot, pl, head);
 }
 
 // Reads one page of one head back: keys straight, values through LDS (their codes are dimension-major),
@@ -569,10 +522,10 @@ __global__ __launch_bounds__(kThreads) void kv8_gather_kernel(Kv8Cache c, Kv8Bat
     __shared__ uint32_t vpage[D * ROW];
     const int tid = threadIdx.x;
     int64_t g = blockIdx.x;
-    const int at = (int)(g % span);
-    g /= span;
     const int head = (int)(g % c.heads);
-    const int seq = (int)(g / c.heads);
+    g /= c.heads;
+    const int at = (int)(g % span);
+    const int seq = (int)(g / span);
     int row0, n;
     kv8_rows(b, seq, row0, n);
     const int64_t room = (int64_t)b.width * P;
@@ -868,8 +821,8 @@ hipError_t append_as(const Kv8Cache &c, const Kv8Batch &b, const void *k, const 
     const dim3 grid((unsigned)(2 * page_groups(c, b, span)));
 #define CFZ_KV8_CASE(D, P)                                                                         \
     if (c.dim == D && c.page == P)                                                                 \
-        kv8_append_kernel<T, D, P><<<grid, kThreads, 0, st>>>(c, b, (const T *)k, (const T *)v, ks, \
-                                                              vs, rot, span);
+        (rot.cos ? kv8_append_kernel<T, D, P, true> : kv8_append_kernel<T, D, P, false>)            \
+            <<<grid, kThreads, 0, st>>>(c, b, (const T *)k, (const T *)v, ks, vs, rot, span);
     CFZ_KV8_CASE(64, 32)
     CFZ_KV8_CASE(64, 64)
     CFZ_KV8_CASE(64, 128)

@@ -189,6 +189,23 @@ def test_append_special_values(fmt):
     x.check()
 
 
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_append_ties_whose_product_by_the_inverse_scale_is_off(fmt):
+    """x = s (k + 1/2) with s = 49, 107 and the like, where x (1 / s) in 64 bits misses the tie."""
+    grid = model.e4m3_values()[:127] if fmt == "e4m3" else np.arange(128.0)
+    mid = (grid[1:] + grid[:-1]) / 2
+    assert any(49.0 * m * (1.0 / 49.0) != m for m in mid)
+    row = np.resize(np.concatenate([[grid[-1]], mid, -mid]), 32 * 64).reshape(32, 64)
+    steps = np.array([49.0, 98.0 * 2 ** -7, 103.0, 107.0 * 2 ** 9, 161.0, 187.0 * 2 ** -20])
+    rows = np.concatenate([row * s for s in steps])[:, None]
+    assert np.array_equal(np.float32(rows), rows)
+    x = Both(1, 6, 1, 64, 32, fmt, seed=9)
+    k = torch.from_numpy(np.float32(rows)).to(DEV)
+    x.append([192], k, -k)
+    assert np.array_equal(x.model.ks[x.table[0], 0], steps)
+    x.check()
+
+
 def test_append_leaves_out_bad_pages_and_tokens_past_the_table():
     x = Both(3, 3, 1, 64, 32, "int8", seed=8)
     x.table[0, 1], x.table[1, 0] = -1, x.cache.pages

@@ -9,6 +9,7 @@ before any device work) tensors that do not fit the call."""
 from __future__ import annotations
 
 import ctypes as C
+from contextlib import ExitStack, nullcontext
 from dataclasses import dataclass
 from typing import Optional
 
@@ -160,6 +161,7 @@ class Cache:
         self.desc = cfz_kv8_cache(pages, heads, dim, tokens, _CODES[k.dtype], k.data_ptr(),
                                   v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                   None if k_mean is None else k_mean.data_ptr())
+        self._ref = C.byref(self.desc)
 
     # ---- marshalling
 
@@ -171,11 +173,23 @@ class Cache:
                              _ints(offsets, (batch + 1,), self.device, "offsets"),
                              _ints(lengths, (batch,), self.device, "lengths"), tokens, max_rows)
 
-    def _call(self, name, stream, *args):
-        with torch.cuda.device(self.device):
-            st = getattr(_lib, name)(*args, cfz._stream(stream))
+    def _on(self, stream):
+        """The cache's device and `stream`, for the allocations of a call."""
+        if stream is None and torch.cuda.current_device() == self.device.index:
+            return nullcontext()
+        with_both = ExitStack()
+        with_both.enter_context(torch.cuda.device(self.device))
+        with_both.enter_context(torch.cuda.stream(stream))
+        return with_both
+
+    def _call(self, call, stream, *args):
+        if torch.cuda.current_device() == self.device.index:
+            st = call(*args, cfz._stream(stream))
+        else:
+            with torch.cuda.device(self.device):
+                st = call(*args, cfz._stream(stream))
         if st != CFZ_OK:
-            raise CfzError(st, name)
+            raise CfzError(st, call.__name__)
 
     def _workspace(self, nbytes, workspace, stream):
         """The caller's workspace, or one from torch's allocator that stays in use until the
@@ -188,7 +202,7 @@ class Cache:
             return None, 0
         if isinstance(stream, int):
             raise ValueError("a raw stream handle needs an explicit workspace")
-        with torch.cuda.device(self.device), torch.cuda.stream(stream):
+        with self._on(stream):
             return torch.empty(nbytes, dtype=torch.uint8, device=self.device), nbytes
 
     # ---- calls
@@ -217,7 +231,7 @@ class Cache:
                 None if pos is None else _ints(pos, (k.shape[0],), self.device, "positions"),
                 cos.shape[0], 2 * cos.shape[1], bool(rotation.interleaved)))
         batch = self._batch(page_table, lengths, offsets, k.shape[0], max_new)
-        self._call("cfz_kv8_append", stream, C.byref(self.desc), C.byref(batch), _REALS[k.dtype],
+        self._call(_lib.cfz_kv8_append, stream, self._ref, C.byref(batch), _REALS[k.dtype],
                    k.data_ptr(), v.data_ptr(), ks, vs, rot)
 
     def gather(self, page_table, start, offsets, tokens, max_count, dtype=torch.bfloat16, k=None,
@@ -229,7 +243,7 @@ class Cache:
         if k is None and v is None:
             if isinstance(stream, int):
                 raise ValueError("a raw stream handle needs explicit outputs")
-            with torch.cuda.device(self.device), torch.cuda.stream(stream):
+            with self._on(stream):
                 k = torch.empty(shape, dtype=dtype, device=self.device)
                 v = torch.empty(shape, dtype=dtype, device=self.device)
         for t, what in ((k, "k"), (v, "v")):
@@ -239,7 +253,7 @@ class Cache:
         if dtype not in _REALS:
             raise TypeError(f"dtype = {dtype}: expected bf16, fp16 or fp32")
         batch = self._batch(page_table, start, offsets, tokens, max_count)
-        self._call("cfz_kv8_gather", stream, C.byref(self.desc), C.byref(batch), _REALS[dtype],
+        self._call(_lib.cfz_kv8_gather, stream, self._ref, C.byref(batch), _REALS[dtype],
                    None if k is None else k.data_ptr(), None if v is None else v.data_ptr())
         return k, v
 
@@ -274,11 +288,11 @@ class Cache:
                 raise ValueError("blocks: expected [batch, query blocks, kv_heads, count] and "
                                  "q_block >= 1")
             lists = C.byref(self._lists(blocks, batch, max_q, q_block))
-        need = _lib.cfz_kv8_attend_workspace_bytes(C.byref(self.desc), C.byref(batch), heads,
+        need = _lib.cfz_kv8_attend_workspace_bytes(self._ref, C.byref(batch), heads,
                                                    max_kv, lists)
         workspace, have = self._workspace(need, workspace, stream)
         if out is None or lse is None:
-            with torch.cuda.device(self.device), torch.cuda.stream(stream):
+            with self._on(stream):
                 if out is None:
                     out = torch.empty((tokens, heads, self.head_dim), dtype=q.dtype,
                                       device=self.device)
@@ -290,7 +304,7 @@ class Cache:
         if (tuple(lse.shape) != (tokens, heads) or lse.dtype != torch.float32 or
                 lse.device != self.device or not lse.is_contiguous()):
             raise ValueError(f"lse: expected a contiguous fp32 tensor {(tokens, heads)}")
-        self._call("cfz_kv8_attend", stream, C.byref(self.desc), C.byref(batch), _REALS[q.dtype],
+        self._call(_lib.cfz_kv8_attend, stream, self._ref, C.byref(batch), _REALS[q.dtype],
                    q.data_ptr(), stride, heads, bool(causal),
                    self.head_dim ** -0.5 if scale is None else scale, max_kv, lists,
                    out.data_ptr(), ostride, lse.data_ptr(),
@@ -312,14 +326,14 @@ class Cache:
         if blocks is None:
             if isinstance(stream, int):
                 raise ValueError("a raw stream handle needs explicit outputs")
-            with torch.cuda.device(self.device), torch.cuda.stream(stream):
+            with self._on(stream):
                 blocks = torch.empty((batch.batch, -(-max_q // q_block), self.kv_heads, count),
                                      dtype=torch.int32, device=self.device)
         lists = self._lists(blocks, batch, max_q, q_block, count)
-        need = _lib.cfz_kv8_select_workspace_bytes(C.byref(self.desc), C.byref(batch), max_kv,
+        need = _lib.cfz_kv8_select_workspace_bytes(self._ref, C.byref(batch), max_kv,
                                                    C.byref(lists))
         workspace, have = self._workspace(need, workspace, stream)
-        self._call("cfz_kv8_select", stream, C.byref(self.desc), C.byref(batch), _REALS[q.dtype],
+        self._call(_lib.cfz_kv8_select, stream, self._ref, C.byref(batch), _REALS[q.dtype],
                    q.data_ptr(), stride, q.shape[1], bool(causal), max_kv, first, last,
                    C.byref(lists), None if workspace is None else workspace.data_ptr(), have)
         return blocks

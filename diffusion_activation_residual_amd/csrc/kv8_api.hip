@@ -101,8 +101,8 @@ cfz_status check_stride(int64_t stride, int64_t row, int dtype, const char *what
 
 cfz_status check_groups(double groups)
 {
-    if (groups >= 2147483648.0)
-        return fail(CFZ_ERR_SHAPE, "the call needs %.0f work-groups (limit 2^31)", groups);
+    if (groups >= cfz::kKv8MaxGroups)
+        return fail(CFZ_ERR_SHAPE, "the call needs %.0f work-groups (limit 2^23)", groups);
     return CFZ_OK;
 }
 
@@ -127,6 +127,9 @@ cfz_status check_queries(const cfz::Kv8Cache &c, const cfz::Kv8Batch &b, int32_t
         if (blocks->q_block < 1)
             return fail(CFZ_ERR_SHAPE, "blocks: q_block = %d", blocks->q_block);
     }
+    const int64_t most = blocks ? blocks->q_block : b.tokens;
+    if ((b.max_rows < most ? b.max_rows : most) * (q_heads / c.heads) > 1 << 30)
+        return fail(CFZ_ERR_SHAPE, "more than 2^30 rows (queries, query heads) read a KV head");
     return CFZ_OK;
 }
 

@@ -3,11 +3,13 @@
 // With key codes c_t and value codes e_t, page scales s_t and z_t, and y_t = scale log2(e)
 // s_t (q . c_t) + log2(z_t), the output is
 //   out = sum_t 2^(y_t - m) e_t / sum_t 2^(y_t - m) / z_t
-// for any m: the key scale multiplies the score, the value scale joins the exponent, and both products
-// run on the codes themselves, which fp16 holds exactly (v_mfma_f32_*_f16).  One pass over the keys keeps
-// the running maximum m of y; the accumulators are rescaled only where it grew by more than
-// kSlack, and the weights carry 2^kLift so that the ones that fp16 flushes are under
-// 2^-(24 + kLift) of the largest.
+// for any m: the key scale multiplies the score, the value scale joins the exponent, and both
+// products run on the codes themselves, which fp16 holds exactly (v_mfma_f32_*_f16).  One pass over
+// the keys keeps m near the running maximum of y: it is moved, and the accumulators rescaled, only
+// where the weights would grow out of fp16's range.  The weights carry 2^kLift, so that the ones that
+// fp16 flushes are under 2^-(24 + kLift) of the one at m.  A query row is rounded to fp16 after a
+// power of two has brought its largest entry to [2^14, 2^15) (exact for bf16 entries down to
+// 2^-29 of it); scores, statistics and output sums are fp32.
 //
 // Both kernels compute S^T = K Q^T: in the accumulator's layout a lane then holds scores of ONE query
 // (its column), so maximum, sum and rescaling need no exchange inside the loop, and the
@@ -31,12 +33,9 @@ typedef float f16v __attribute__((ext_vector_type(16)));
 typedef float f2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 
-#ifndef KLIFT
-#define KLIFT 6
-#endif
-constexpr float kLift = KLIFT;
-constexpr float kSlack = 5.0f;  // weights reach 2^(kLift + kSlack) = 2^15 < 65504
-constexpr float kLimit = 60000.0f;
+constexpr float kLift = 6.0f;
+constexpr float kSlack = 5.0f;      // (few rows) a row's maximum is moved where it is off by more
+constexpr float kLimit = 60000.0f;  // (many rows) ... or where a lane's weights sum to more
 constexpr float kNone = -3.0e38f;
 constexpr float kTiny = -100.0f;  // log2 of the value scale up to which codes count as zeros
 constexpr int kBlock = 64;  // keys per step
@@ -285,7 +284,7 @@ __device__ inline Half find_half(const Kv8Cache &c, const Kv8Batch &b, const Kv8
     int logical = vt >> c.log2page;
     if (t.list)
         logical = logical < a.count ? t.list[logical] : -1;
-    if (logical >= b.width)
+    if (logical < 0 || logical >= b.width)
         logical = -1;
     h.tok = logical * c.page + (vt & (c.page - 1));
     h.page = logical >= 0 && h.tok < reach_max ? kv8_page(c, b, t.seq, logical) : -1;
@@ -407,7 +406,10 @@ __device__ inline float *partial(const Kv8Attend &a, int64_t slot)
 //
 // 16 rows per work-group; its four waves take every fourth step of 64 keys, straight from memory into
 // registers (each code is used by one wave only, so LDS would add a trip), and join their
-// sums at the end.  Bound by the codes' bytes: at head_dim 128 a wave has 16 KB in flight.
+// sums at the end.  The pages and scales of many steps are looked up together, and the next step's
+// codes are under way while this one's weights are formed (each looked up in its own step, 147 us
+// instead of 80).  Bound by the codes' bytes: 16 sequences of up to 16411 tokens, 8 KV heads of
+// 128, 32 query heads, in 80 us, 5.1 TB/s, and 6 us for the join.
 template <int FMT, int D>
 __global__ __launch_bounds__(256, 2) void kv8_attend_narrow_kernel(Kv8Cache c, Kv8Batch b,
                                                                    Kv8Attend a, Kv8Plan p)
@@ -426,207 +428,214 @@ __global__ __launch_bounds__(256, 2) void kv8_attend_narrow_kernel(Kv8Cache c, K
     Run run = first_run<256, BM>(c, b, a, p, prefix, waves, wg);
     Tile t;
     while (next_run<BM>(c, b, a, p, prefix, wg, run, t)) {
-    const int r = t.r0 + col;
-    const bool have = r < t.rows;
-    const int qi = t.q0 + (have ? r : t.rows - 1) / a.group;
-    const int qh = t.head * a.group + (have ? r : t.rows - 1) % a.group;
-    const int reach_min = t.reach_min, reach_max = t.reach_max;
-    const int mine = reach(t, a.causal, qi);
+        const int r = t.r0 + col;
+        const bool have = r < t.rows;
+        const int qi = t.q0 + (have ? r : t.rows - 1) / a.group;
+        const int qh = t.head * a.group + (have ? r : t.rows - 1) % a.group;
+        const int reach_min = t.reach_min, reach_max = t.reach_max;
+        const int mine = reach(t, a.causal, qi);
 
-    // the query row, lane group g holding dimensions g D/4 .. (the order of the dimensions in the
-    // contraction is free: it follows the keys' 16-byte loads)
-    h8 q[KS];
-    float qmul;
-    {
-        float x[D / 4];
-        const uint16_t *at = (const uint16_t *)a.q + (int64_t)(t.row0 + qi) * a.q_stride +
-                             (int64_t)qh * D + g * (D / 4);
+        // the query row, lane group g holding dimensions g D/4 .. (the order of the dimensions in the
+        // contraction is free: it follows the keys' 16-byte loads)
+        h8 q[KS];
+        float qmul;
+        {
+            float x[D / 4];
+            const uint16_t *at = (const uint16_t *)a.q + (int64_t)(t.row0 + qi) * a.q_stride +
+                                 (int64_t)qh * D + g * (D / 4);
 #pragma unroll
-        for (int i = 0; i < D / 4; i += 8)
-            widen_q(*(const u4 *)(at + i), a.f16, x + i);
-        float big = 0.0f;
+            for (int i = 0; i < D / 4; i += 8)
+                widen_q(*(const u4 *)(at + i), a.f16, x + i);
+            float big = 0.0f;
 #pragma unroll
-        for (int i = 0; i < D / 4; ++i)
-            big = fmaxf(big, fabsf(x[i]));
-        big = fmaxf(big, __shfl_xor(big, 16));
-        big = fmaxf(big, __shfl_xor(big, 32));
-        float inv;
-        const float up = row_scale(big, inv);
-        qmul = inv * (a.scale * 1.4426950408889634f);
+            for (int i = 0; i < D / 4; ++i)
+                big = fmaxf(big, fabsf(x[i]));
+            big = fmaxf(big, __shfl_xor(big, 16));
+            big = fmaxf(big, __shfl_xor(big, 32));
+            float inv;
+            const float up = row_scale(big, inv);
+            qmul = inv * (a.scale * 1.4426950408889634f);
 #pragma unroll
-        for (int s = 0; s < KS; ++s)
+            for (int s = 0; s < KS; ++s)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                q[s][j] = (_Float16)(x[s * 8 + j] * up);
-    }
+                for (int j = 0; j < 8; ++j)
+                    q[s][j] = (_Float16)(x[s * 8 + j] * up);
+        }
 
-    f4 o[DT];
-#pragma unroll
-    for (int i = 0; i < DT; ++i)
-        o[i] = f4{0, 0, 0, 0};
-    float m = kNone, l = 0.0f;
-
-    // Key row `col` of tile u is token 16 (col / 4) + 4 u + col % 4: accumulator i of lane group g
-    // in tile u is then token 16 g + 4 u + i.
-    const int64_t page_bytes = (int64_t)c.page * D;
-    const int kchunk = col >> 2, krow = (col & 3) + 16 * (kchunk & 1);
-
-    // A lane's share of a step: 16-byte pieces of 4 key rows and of D / 16 value rows, and the half
-    // that its scores and values belong to.  (Of a half without a page, page 0 is read and nothing of
-    // it used.)
-    u4 kr[4][KL], vr[DT];
-    Half next;
-    const uint32_t koff = krow * D + g * (D / 4), voff = col * c.page + 16 * (g & 1);
-    auto load = [&](int i) {
-        const Half hk = halves[2 * i + (kchunk >> 1)];
-        next = halves[2 * i + (g >> 1)];
-        const uint8_t *kp = c.k + ((int64_t)(hk.page < 0 ? 0 : hk.page) * c.heads + t.head) * page_bytes +
-                            ((hk.tok & (c.page - 1)) * D + koff);
-        const uint8_t *vp = c.v +
-                            ((int64_t)(next.page < 0 ? 0 : next.page) * c.heads + t.head) * page_bytes +
-                            ((next.tok & (c.page - 1)) + voff);
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-            for (int j = 0; j < KL; ++j)
-                kr[u][j] = *(const u4 *)(kp + u * 4 * D + j * 16);
+        f4 o[DT];
 #pragma unroll
         for (int i = 0; i < DT; ++i)
-            vr[i] = *(const u4 *)(vp + i * 16 * c.page);
-    };
+            o[i] = f4{0, 0, 0, 0};
+        float m = kNone, l = 0.0f;
 
-    for (int first = run.s0; first < run.s1; first += AHEAD) {
-    const int last = first + AHEAD < run.s1 ? first + AHEAD : run.s1;
-    __syncthreads();
-    for (int i = threadIdx.x; i < 2 * (last - first); i += 256) {
-        Half h = find_half(c, b, a, t, first * kBlock + 32 * i, reach_max);
-        find_scales(c, t, h);
-        halves[i] = h;
-    }
-    __syncthreads();
-    int s = first + wave;
-    if (s < last)
-        load(s - first);
-    for (; s < last; s += 4) {
-        // scores
-        f4 acc[4];
+        // Key row `col` of tile u is token 16 (col / 4) + 4 u + col % 4: accumulator i of lane group g
+        // in tile u is then token 16 g + 4 u + i.
+        const int64_t page_bytes = (int64_t)c.page * D;
+        const int kchunk = col >> 2, krow = (col & 3) + 16 * (kchunk & 1);
+
+        // A lane's share of a step: 16-byte pieces of 4 key rows and of D / 16 value rows, and the
+        // half that its scores and values belong to.  (Of a half without a page, page 0 is read
+        // and nothing of it used.)
+        u4 kr[4][KL], vr[DT];
+        Half next;
+        const uint32_t koff = krow * D + g * (D / 4), voff = col * c.page + 16 * (g & 1);
+        auto load = [&](int i) {
+            const Half hk = halves[2 * i + (kchunk >> 1)];
+            next = halves[2 * i + (g >> 1)];
+            const int64_t kpage = hk.page < 0 ? 0 : hk.page, vpage = next.page < 0 ? 0 : next.page;
+            const uint8_t *kp = c.k + (kpage * c.heads + t.head) * page_bytes +
+                                ((hk.tok & (c.page - 1)) * D + koff);
+            const uint8_t *vp = c.v + (vpage * c.heads + t.head) * page_bytes +
+                                ((next.tok & (c.page - 1)) + voff);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            acc[u] = f4{0, 0, 0, 0};
+            for (int u = 0; u < 4; ++u)
 #pragma unroll
-            for (int j = 0; j < KS; ++j) {
-                const u4 w = kr[u][j / 2];
-                acc[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                    to_half8<FMT>(w[j % 2 * 2], w[j % 2 * 2 + 1]), q[j], acc[u], 0, 0, 0);
+                for (int j = 0; j < KL; ++j)
+                    kr[u][j] = *(const u4 *)(kp + u * 4 * D + j * 16);
+#pragma unroll
+            for (int i = 0; i < DT; ++i)
+                vr[i] = *(const u4 *)(vp + i * 16 * c.page);
+        };
+
+        for (int first = run.s0; first < run.s1; first += AHEAD) {
+            const int last = first + AHEAD < run.s1 ? first + AHEAD : run.s1;
+            __syncthreads();
+            for (int i = threadIdx.x; i < 2 * (last - first); i += 256) {
+                Half h = find_half(c, b, a, t, first * kBlock + 32 * i, reach_max);
+                find_scales(c, t, h);
+                halves[i] = h;
+            }
+            __syncthreads();
+            int s = first + wave;
+            if (s < last)
+                load(s - first);
+            for (; s < last; s += 4) {
+                // scores
+                f4 acc[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    acc[u] = f4{0, 0, 0, 0};
+#pragma unroll
+                    for (int j = 0; j < KS; ++j) {
+                        const u4 w = kr[u][j / 2];
+                        acc[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                            to_half8<FMT>(w[j % 2 * 2], w[j % 2 * 2 + 1]), q[j], acc[u], 0, 0, 0);
+                    }
+                }
+                const Half h = next;
+                u4 v[DT];
+#pragma unroll
+                for (int i = 0; i < DT; ++i)
+                    v[i] = vr[i];
+                load((s + 4 < last ? s + 4 : s) - first);
+                const Factor f = factor(h, qmul);
+                const int tok = h.tok + 16 * (g & 1);
+                float y[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    y[i] = fmaf(acc[i / 4][i % 4], f.mul, f.add);
+                if (__any(h.page < 0 || h.tok + 32 > reach_min || flushed(h))) {
+                    const bool none = h.page < 0;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        y[i] = none || tok + i >= mine ? -__builtin_inff() : y[i];
+#pragma unroll
+                    for (int i = 0; i < DT; ++i)
+                        v[i] = flushed(h) ? u4{0, 0, 0, 0} : keep_live(v[i], tok, t.len);
+                }
+                float top = y[0];
+#pragma unroll
+                for (int i = 1; i < 16; ++i)
+                    top = fmaxf(top, y[i]);
+                if (__any(top > m + kSlack)) {
+                    top = fmaxf(top, __shfl_xor(top, 16));
+                    top = fmaxf(top, __shfl_xor(top, 32));
+                    // (each row on its own terms: what it gets does not depend on the rows beside it)
+                    const float now = top > m + kSlack ? top : m, fall = exp2_fast(m - now);
+                    m = now;
+                    l *= fall;
+#pragma unroll
+                    for (int i = 0; i < DT; ++i)
+                        o[i] *= fall;
+                }
+                float sum = 0.0f;
+                h8 w[2];
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    const float e0 = exp2_fast(y[i] + (kLift - m));
+                    const float e1 = exp2_fast(y[i + 1] + (kLift - m));
+                    sum += e0 + e1;
+                    const h2 e = pack(e0, e1);
+                    w[i / 8][i % 8] = e[0];
+                    w[i / 8][i % 8 + 1] = e[1];
+                }
+                l = fmaf(sum, f.back, l);
+#pragma unroll
+                for (int i = 0; i < DT; ++i) {
+                    o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                        to_half8<FMT>(v[i][0], v[i][1]), w[0], o[i], 0, 0, 0);
+                    o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                        to_half8<FMT>(v[i][2], v[i][3]), w[1], o[i], 0, 0, 0);
+                }
             }
         }
-        const Half h = next;
-        u4 v[DT];
+        l += __shfl_xor(l, 16);
+        l += __shfl_xor(l, 32);
+
+        // join the four waves
+        if (g == 0) {
+            om[wave][col] = m;
+            ol[wave][col] = l;
+        }
 #pragma unroll
         for (int i = 0; i < DT; ++i)
-            v[i] = vr[i];
-        load((s + 4 < last ? s + 4 : s) - first);
-        const Factor f = factor(h, qmul);
-        const int tok = h.tok + 16 * (g & 1);
-        float y[16];
+            *(f4 *)&oo[wave][col][i * 16 + g * 4] = o[i];
+        __syncthreads();
+        for (int i = threadIdx.x; i < BM * (D / 4); i += 256) {
+            const int row = i / (D / 4), d = i % (D / 4) * 4, rr = t.r0 + row;
+            if (rr >= t.rows)
+                break;
+            float mm = fmaxf(fmaxf(om[0][row], om[1][row]), fmaxf(om[2][row], om[3][row]));
+            // a NaN row stays one: its sums are NaN whatever the weights
+            float ll = 0.0f;
+            f4 s = {0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            y[i] = fmaf(acc[i / 4][i % 4], f.mul, f.add);
-        if (__any(h.page < 0 || h.tok + 32 > reach_min || flushed(h))) {
-            const bool none = h.page < 0;
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                y[i] = none || tok + i >= mine ? -__builtin_inff() : y[i];
-#pragma unroll
-            for (int i = 0; i < DT; ++i)
-                v[i] = flushed(h) ? u4{0, 0, 0, 0} : keep_live(v[i], tok, t.len);
+            for (int w = 0; w < 4; ++w) {
+                const float e = exp2_fast(om[w][row] - mm);
+                ll += ol[w][row] * e;
+                s += *(const f4 *)&oo[w][row][d] * e;
+            }
+            if (run.slot >= 0) {
+                float *out = partial<BM, D>(a, run.slot);
+                if (d == 0)
+                    *(f2 *)(out + BM * D + 2 * row) = f2{mm, ll};
+                *(f4 *)(out + 4 * i) = s;
+            } else {
+                const int64_t qrow = t.row0 + t.q0 + rr / a.group;
+                const int head = t.head * a.group + rr % a.group;
+                const float inv = ll > 0.0f ? 1.0f / ll : (ll == ll ? 0.0f : ll);
+                store_out(a, qrow * a.out_stride + (int64_t)head * D + d, s[0] * inv, s[1] * inv,
+                          s[2] * inv, s[3] * inv);
+                if (a.lse && d == 0)
+                    a.lse[qrow * a.q_heads + head] = lse_of(mm, ll);
+            }
         }
-        float top = y[0];
-#pragma unroll
-        for (int i = 1; i < 16; ++i)
-            top = fmaxf(top, y[i]);
-        if (__any(top > m + kSlack)) {
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            // (each row on its own terms: what it gets does not depend on the rows beside it)
-            const float now = top > m + kSlack ? top : m, fall = exp2_fast(m - now);
-            m = now;
-            l *= fall;
-#pragma unroll
-            for (int i = 0; i < DT; ++i)
-                o[i] *= fall;
-        }
-        float sum = 0.0f;
-        h8 w[2];
-#pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-            const float e0 = exp2_fast(y[i] + (kLift - m)), e1 = exp2_fast(y[i + 1] + (kLift - m));
-            sum += e0 + e1;
-            const h2 e = pack(e0, e1);
-            w[i / 8][i % 8] = e[0];
-            w[i / 8][i % 8 + 1] = e[1];
-        }
-        l = fmaf(sum, f.back, l);
-#pragma unroll
-        for (int i = 0; i < DT; ++i) {
-            o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(to_half8<FMT>(v[i][0], v[i][1]), w[0],
-                                                          o[i], 0, 0, 0);
-            o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(to_half8<FMT>(v[i][2], v[i][3]), w[1],
-                                                          o[i], 0, 0, 0);
-        }
-    }
-    }
-    l += __shfl_xor(l, 16);
-    l += __shfl_xor(l, 32);
-
-    // join the four waves
-    if (g == 0) {
-        om[wave][col] = m;
-        ol[wave][col] = l;
-    }
-#pragma unroll
-    for (int i = 0; i < DT; ++i)
-        *(f4 *)&oo[wave][col][i * 16 + g * 4] = o[i];
-    __syncthreads();
-    for (int i = threadIdx.x; i < BM * (D / 4); i += 256) {
-        const int row = i / (D / 4), d = i % (D / 4) * 4, rr = t.r0 + row;
-        if (rr >= t.rows)
-            break;
-        float mm = fmaxf(fmaxf(om[0][row], om[1][row]), fmaxf(om[2][row], om[3][row]));
-        // a NaN row stays one: its sums are NaN whatever the weights
-        float ll = 0.0f;
-        f4 s = {0, 0, 0, 0};
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const float e = exp2_fast(om[w][row] - mm);
-            ll += ol[w][row] * e;
-            s += *(const f4 *)&oo[w][row][d] * e;
-        }
-        if (run.slot >= 0) {
-            float *out = partial<BM, D>(a, run.slot);
-            if (d == 0)
-                *(f2 *)(out + BM * D + 2 * row) = f2{mm, ll};
-            *(f4 *)(out + 4 * i) = s;
-        } else {
-            const int64_t qrow = t.row0 + t.q0 + rr / a.group;
-            const int head = t.head * a.group + rr % a.group;
-            const float inv = ll > 0.0f ? 1.0f / ll : (ll == ll ? 0.0f : ll);
-            store_out(a, qrow * a.out_stride + (int64_t)head * D + d, s[0] * inv, s[1] * inv,
-                      s[2] * inv, s[3] * inv);
-            if (a.lse && d == 0)
-                a.lse[qrow * a.q_heads + head] = lse_of(mm, ll);
-        }
-    }
-    __syncthreads();  // om, ol and oo are read
+        __syncthreads();  // om, ol and oo are read
     }
 }
 
 // ------------------------------------------------------------------ many rows
 //
-// 128 rows per work-group, 32 per wave (v_mfma_f32_32x32x16_f16).  Each step's codes are read
-// once per work-group, one step ahead, converted to fp16 on the way into LDS (each code once instead of once
-// per wave) and read from there by all four waves.  16-byte chunks of a row are exchanged by an XOR of
-// row bits, so that the eight lanes that LDS serves together read eight different bank groups.
+// 32 R rows per wave (v_mfma_f32_32x32x16_f16), NW waves, 32 H keys a step.  Each step's codes are
+// read once per work-group, ahead of their use, and converted to fp16 on the way into LDS (each
+// code once instead of once per wave).  At NW = 8 two waves share a SIMD and run a phase apart:
+// one multiplies while the other forms weights, since a step's weights (an fp32 product, an
+// exponential and half a conversion per score) take about as long as its products.  Measured with the
+// join: 1024 queries over 4096 keys, 24 heads of 128, 99 us, 520 TFLOP/s; 4388 queries over 17552 keys,
+// 30 heads of 64, 820 us, 720 TFLOP/s; products alone reach 1900 in this instruction.  With both
+// kinds of work in every wave, one step's products between the other's weights, the registers
+// spilled; with products and weights one after the other it was 1141 us.
+//
 // The XOR of a key row's chunk number: 16 lanes that read one chunk of 16 key rows (in the order
 // that the tile's rows have) must meet 16 different positions of the 256 bytes that LDS serves at
 // once; a row is 256 bytes at head_dim 128, and half of that at 64, where the row's lowest bit counts.
@@ -840,11 +849,12 @@ __global__ __launch_bounds__(NW * 64, 2) void kv8_attend_wide_kernel(Kv8Cache c,
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
                         acc[y][x][j] = 0.0f;
-                acc[y][x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[y][i % KS], acc[y][x], 0, 0, 0);
+                acc[y][x] =
+                    __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[y][i % KS], acc[y][x], 0, 0, 0);
             }
         };
-        // Between them goes the staging of what the next step needs: the matrix unit works on while the
-        // codes are converted.
+        // Between them goes the staging of what the next step needs: the matrix unit works on
+        // while the codes are converted.
         auto multiply = [&](int s, auto scores) {
             constexpr bool MORE = decltype(scores)::value;
             constexpr int A = NV, N = A + (MORE ? NS : 0);
@@ -1125,20 +1135,29 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8Cache c, Kv8Batch b, K
     }
 }
 
-constexpr int64_t kNarrowRows = 32;  // rows of a query block up to which the narrow kernel is taken
+// Rows of a query block up to which the narrow kernel is taken, although it reads the keys again for
+// every 16 rows: over 16 sequences of 8192 tokens and 8 heads, with 32 rows 70 us against 100
+// at head_dim 128 and 33 against 87 at 64; with 48 rows 130 against 111 and 68 against 88; with 64
+// rows 55 against 88 at 64.
+inline int64_t narrow_rows(int dim) { return dim == 64 ? 64 : 32; }
 
-// The launch's shapes: rows per tile, threads, and work-groups that are resident at once.
+// The launch's shapes: rows per tile, and work-groups that are resident at once.
 struct Shape {
-    int rows, threads, slots;
+    int rows, slots;
 };
 
+// Taller tiles read the keys less often and need fewer LDS reads a product; lower ones waste less on
+// few rows, and two or more of their work-groups share a CU.  Over 4 sequences of 8192 tokens and
+// 24 heads, tiles of 128 / 256 / 512 rows take (us), at head_dim 64 with 64 rows 81 / 86 / 130, with
+// 128 95 / 89 / 136, with 256 117 / 106 / 145, with 384 151 / 167 / 150, with 1000 333 / 325 / 262;
+// at head_dim 128 with 128 rows 107 / 119, with 192 159 / 135, with 1000 529 / 441.
 Shape shape_of(bool wide, int dim, int64_t rows)
 {
     if (!wide)
-        return {16, 256, 512};
+        return {16, 512};
     if (rows <= 128)
-        return dim == 64 ? Shape{128, 128, 1024} : Shape{128, 256, 512};
-    return dim == 64 && rows > 256 ? Shape{512, 512, 256} : Shape{256, 512, 256};
+        return dim == 64 ? Shape{128, 1024} : Shape{128, 512};
+    return dim == 64 && rows > 256 ? Shape{512, 256} : Shape{256, 256};
 }
 
 }  // namespace
@@ -1151,7 +1170,7 @@ Kv8Plan kv8_plan(const Kv8Cache &c, const Kv8Batch &b, int q_heads, int64_t max_
     if (!listed || q_block > b.max_rows)
         q_block = b.max_rows;
     const int64_t rows = q_block * group;
-    p.wide = rows > kNarrowRows;
+    p.wide = rows > narrow_rows(c.dim);
     const Shape sh = shape_of(p.wide, c.dim, rows);
     const double units = (double)((b.max_rows + q_block - 1) / q_block);
     const double tiles = (double)((rows + sh.rows - 1) / sh.rows);
@@ -1161,17 +1180,18 @@ Kv8Plan kv8_plan(const Kv8Cache &c, const Kv8Batch &b, int q_heads, int64_t max_
     p.groups = 1;
     p.ws_bytes = 0;
     p.rows = sh.rows;
-    p.threads = sh.threads;
-    if (p.whole >= 2147483648.0)
+    if (p.whole >= kKv8MaxGroups)
         return p;  // refused by the caller
     p.units = (int)units;
     p.tiles = (int)tiles;
     p.items = (int)(units * tiles) * b.batch;
     p.groups = (int64_t)p.items * c.heads;
-    const int64_t keys = listed && (int64_t)count * c.page < max_kv ? (int64_t)count * c.page : max_kv;
+    const int64_t keys = listed ? (int64_t)count * c.page : max_kv;  // as find_tile has it
     const int64_t steps = (keys + kBlock - 1) / kBlock;
     // Runs of equal length instead of whole tiles: only where a run is long enough to be worth
-    // joining (a narrow one has 4 waves, each of which should have some steps).
+    // joining (a narrow one has 4 waves, each of which should have some steps).  Half and twice
+    // as many: 18 and 25 us instead of 20 for 4 single queries x 4096 tokens x 8 heads, 55 and 37
+    // instead of 36 for 4 x 256 queries x 1024 tokens.
     const int64_t least = p.wide ? 4 : 16;
     if (p.items <= kMaxItems && steps > least && p.whole * steps < 2147483648.0) {
         int64_t runs = p.groups * steps / least;

@@ -383,8 +383,9 @@ __device__ inline void append_keys(const Kv8Cache &c, const T *k, int64_t k_stri
         c.km[pl.ph * D + tid] = (float)((double)sums[tid] / 512.0 * (double)scale / (double)hi);
 }
 
-// Values: units of 4 tokens x 8 dimensions (4 in the smallest page), transposed in registers and merged into the page's
-// [dim][token] bytes in LDS, so that the page is written in whole 16-byte vectors.
+// Values: units of 4 tokens x 8 dimensions (4 in the smallest page), transposed in registers and
+// merged into the page's [dim][token] bytes in LDS, so that the page is written in whole 16-byte
+// vectors.
 template <class T, int D, int P>
 __device__ inline void append_values(const Kv8Cache &c, const T *v, int64_t v_stride,
                                      const Place &pl, int head)
@@ -479,11 +480,11 @@ __device__ inline void append_values(const Kv8Cache &c, const T *v, int64_t v_st
 #pragma unroll
             for (int j = 0; j < W; ++j) {
                 const uint32_t was = o[j * ROW];
-                const double y = slot >= lo ? (double)(t == 0   ? w[i][0][j]
-                                                       : t == 1 ? w[i][1][j]
-                                                       : t == 2 ? w[i][2][j]
-                                                                : w[i][3][j])
-                                            : (double)code_value((was >> (8 * t)) & 0xff, c.fmt) * prior;
+                const float pair0 = t & 1 ? w[i][1][j] : w[i][0][j];
+                const float pair1 = t & 1 ? w[i][3][j] : w[i][2][j];
+                const float now = t & 2 ? pair1 : pair0;
+                const double y = slot >= lo ? (double)now
+                                            : (double)code_value(was >> (8 * t) & 0xff, c.fmt) * prior;
                 o[j * ROW] = (was & ~(0xffu << (8 * t))) | encode(y, scale, rinv, c.fmt) << (8 * t);
             }
         }
@@ -703,8 +704,8 @@ __global__ __launch_bounds__(kThreads) void kv8_score_kernel(Kv8Cache c, Kv8Batc
 }
 
 // The `count` largest keys of one list: the threshold is found 8 bits at a time by counting
-// (the same work whatever the keys), then the pages above it and, in index order, as many at it as are left
-// are written in ascending order.
+// (the same work whatever the keys), then the pages above it and, in index order, as many at it as
+// are left are written in ascending order.
 __global__ __launch_bounds__(kThreads) void kv8_pick_kernel(Kv8Cache c, Kv8Batch b, Kv8Select a,
                                                             int units, int stride)
 {

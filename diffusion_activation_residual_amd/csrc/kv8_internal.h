@@ -36,17 +36,20 @@ hipError_t launch_kv8_append(const Kv8Cache &c, const Kv8Batch &b, int dtype, co
 hipError_t launch_kv8_gather(const Kv8Cache &c, const Kv8Batch &b, int dtype, void *k, void *v,
                              hipStream_t st);
 
+// Work-groups of a launch stay below this: the grid in threads is a 32-bit number.
+constexpr double kKv8MaxGroups = 8388608.0;
+
 // How a call's query rows and keys are cut up; the same for the workspace query and the launch.
 struct Kv8Plan {
     bool wide;         // row tiles with the keys staged in LDS, else 16-row tiles
     int joined;        // equal runs of steps, joined by a second launch; else one tile a work-group
-    int rows, threads; // per work-group
+    int rows;          // per tile
     int units;         // query blocks per sequence (1 without block lists)
     int tiles;         // row tiles per query block
     int items;         // tiles per head
     int64_t groups;    // work-groups of the launch
     int64_t ws_bytes;
-    double whole;      // tiles in all; the launch is possible below 2^31
+    double whole;      // tiles in all; the launch is possible below kKv8MaxGroups
 };
 
 struct Kv8Attend {

@@ -69,7 +69,9 @@ typedef struct {
  *   max_rows: an upper bound of the rows of one sequence, known on the host; rows
  *            past it are left out.
  * 0 <= batch <= 65535, 1 <= table_width, table_width * page_tokens < 2^31,
- * 0 <= tokens < 2^31 (0 is a no-op).  The integer arrays need 4-byte alignment only. */
+ * 0 <= tokens < 2^31 (0 is a no-op).  The integer arrays need 4-byte alignment only.
+ * A call that would need 2^23 or more work-groups (append: about one for the keys and
+ * one for the values of each page and head) is refused. */
 typedef struct {
     int32_t batch;
     int32_t table_width;
@@ -137,7 +139,7 @@ typedef struct {
  *   out = sum_t softmax_t(scale * q . k_t) v_t,  lse = log sum_t exp(scale * q . k_t).
  * q: rows of q_heads * head_dim values of `dtype` (BF16 or F16), row t at q + t * q_stride
  * (elements; a multiple of 8); q_heads a multiple of kv_heads (at most 64 query heads to
- * one), query head h reads KV head h / (q_heads / kv_heads).  out: like q, row stride
+ * one; at most 2^30 rows of queries and query heads to one KV head), query head h reads KV head h / (q_heads / kv_heads).  out: like q, row stride
  * out_stride.  lse: [tokens][q_heads] fp32 or NULL.
  * Query i of n sees the tokens t < length, and with causal != 0 only t <= length - n + i.
  * blocks (NULL: all pages) restricts it to its block's listed pages.  A row that sees
@@ -147,8 +149,8 @@ typedef struct {
  * and > 0.  The products run on the codes in fp16 (which holds every code exactly; each
  * query row is first scaled by a power of two, so that a bf16 or fp16 q is held exactly down to
  * 2^-29 of its largest entry), accumulate in fp32, and the weights enter the second
- * product rounded to fp16; the softmax statistics are fp32.  Value scales under 2^-100
- * count as 0.  Results do not depend on the run.
+ * product rounded to fp16; the softmax statistics are fp32.  Value scales of 2^-100
+ * or less count as 0.  Results do not depend on the run.
  * workspace: cfz_kv8_attend_workspace_bytes(...) bytes, 256-byte aligned (may be NULL
  * if that is 0), overwritten by the call; calls that may run at the same time need one
  * each.  q, out and lse must not overlap.

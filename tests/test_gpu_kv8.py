@@ -291,7 +291,7 @@ def check_attend(x, counts, group, causal, dtype, lengths=None, lists=None, q_bl
         worst = (np.abs(got - want) / np.maximum(to, 1e-300)).max(initial=0)
         empty = np.isneginf(wl)
         assert np.array_equal(np.isneginf(gl), empty) and not got[empty].any()
-        worst_l = (np.abs(gl - wl)[~empty] / tl[~empty]).max(initial=0)
+        worst_l = (np.abs(gl[~empty] - wl[~empty]) / tl[~empty]).max(initial=0)
         say(f"      sequence {b}: {worst:.3f} of the bound, lse {worst_l:.3f}")
         assert worst <= 1 and worst_l <= 1
         at += c
@@ -344,7 +344,7 @@ def test_attend_splits(dim, fmt):
     check_attend(x, [70, 3], 1, True, "f16")
 
 
-@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("rows", [1, 40, 100])
 def test_attend_ignores_memory_behind_the_tokens(rows):
     """e4m3 pages whose unwritten bytes are NaN codes, scales and table entries that nothing may read."""
     x = Both(2, 5, 1, 64, 32, "e4m3", seed=14, fill=0x7F)
@@ -356,7 +356,7 @@ def test_attend_ignores_memory_behind_the_tokens(rows):
     check_attend(x, [rows, rows], 1, True, "bf16", lengths=[65, 1])
 
 
-@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("rows", [1, 40, 100])
 def test_attend_bad_pages_hold_nothing(rows):
     x = Both(2, 4, 2, 64, 32, "int8", seed=15)
     x.fill_up([100, 128])
@@ -366,7 +366,7 @@ def test_attend_bad_pages_hold_nothing(rows):
     check_attend(x, [rows, rows], 2, False, "bf16")
 
 
-@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("rows", [1, 40, 100])
 def test_attend_sharp_and_flat_scores(rows):
     for size, scale in ((30.0, 0.5), (1e-3, 1e-3), (200.0, 1e-3)):
         x = Both(1, 6, 1, 64, 32, "int8", seed=16)
@@ -374,7 +374,7 @@ def test_attend_sharp_and_flat_scores(rows):
         check_attend(x, [rows], 1, False, "bf16", scale=scale, size=size)
 
 
-@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("rows", [1, 40, 100])
 def test_attend_pages_of_very_different_size(rows):
     """Value scales from 0 over 1e-20 to 1e4: the large ones must not drown the weights' sum."""
     x = Both(1, 6, 1, 64, 32, "int8", seed=17)
@@ -386,7 +386,7 @@ def test_attend_pages_of_very_different_size(rows):
     check_attend(x, [rows], 1, True, "bf16", lengths=[31])
 
 
-@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("rows", [1, 40, 100])
 def test_attend_nan_and_infinite_queries_stay_in_their_rows(rows):
     x = Both(1, 4, 1, 64, 32, "int8", seed=18)
     x.fill_up([100])
@@ -401,6 +401,88 @@ def test_attend_nan_and_infinite_queries_stay_in_their_rows(rows):
     q[rows, 0, 3] = float("inf")
     got, _ = x.cache.attend(q, *args)
     assert torch.equal(got[keep], clean[keep])
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("dim,rows", [(64, 64), (64, 65), (64, 256), (64, 257), (64, 513), (64, 700),
+                                      (128, 128), (128, 129), (128, 257), (128, 300)])
+def test_attend_row_tiles(dim, rows, causal):
+    """Row counts at and beside the heights of the row tiles, with a few and with many keys."""
+    x = Both(2, 6, 1, dim, 128, "int8" if dim == 64 else "e4m3", seed=rows)
+    x.fill_up([rows // 2, 765])
+    check_attend(x, [rows, rows], 1, causal, "bf16")
+
+
+@pytest.mark.parametrize("max_q,group", [(1, 64), (2, 64), (1, 32), (1, 33)])
+def test_attend_many_query_heads_to_one(max_q, group):
+    x = Both(2, 4, 1, 64, 32, "int8", seed=28)
+    x.fill_up([128, 77])
+    check_attend(x, [max_q, 1], group, True, "bf16")
+
+
+@pytest.mark.parametrize("dim,max_q,keys", [(64, 1, 8300), (128, 3, 8300), (64, 100, 8300),
+                                            (128, 100, 8300), (128, 200, 33000), (64, 300, 33000)])
+def test_attend_long_sequences_among_many(dim, max_q, keys):
+    """More tiles than are cut into equal runs, and sequences whose pages are looked up in
+    several goes; most sequences are empty."""
+    page = 128
+    x = Both(1, -(-keys // page), 1, dim, page, "int8", seed=29, spare=0)
+    x.fill_up([keys])
+    others = 1030
+    x.table = np.repeat(x.table, others + 2, axis=0)
+    few = min(max_q, 5)
+    check_attend(x, [0] * others + [few, 1], 1, True, "bf16",
+                 lengths=[0] * others + [keys, keys - 77], max_q=max_q)
+
+
+@pytest.mark.parametrize("group,dim", [(1, 64), (40, 128)])
+def test_attend_more_query_blocks_than_runs(group, dim):
+    x = Both(2, 4, 1, dim, 32, "int8", seed=30)
+    x.fill_up([100, 128])
+    lists = ints(np.sort(np.argsort(x.rng.random((2, 520, 1, 4)), axis=-1)[..., :2], axis=-1))
+    check_attend(x, [520, 515], group, False, "bf16", lists=lists, q_block=1)
+
+
+def test_attend_lists_longer_than_the_keys():
+    """A list may have far more places than max_kv has pages."""
+    x = Both(2, 8, 2, 64, 32, "int8", seed=31)
+    x.fill_up([5 * 32, 40])
+    lists = torch.full((2, 1, 2, 4096), -1, dtype=torch.int32, device=DEV)
+    lists[0, 0, :, 4000:4003] = ints([0, 2, 4])
+    lists[1, 0, :, 7], lists[1, 0, :, 4095] = 1, 0
+    for rows in (1, 70):
+        check_attend(x, [rows, rows], 1, True, "bf16", lists=lists, q_block=rows, max_kv=5 * 32)
+
+
+@pytest.mark.parametrize("rows", [1, 70])
+def test_attend_without_keys_or_pages(rows):
+    x = Both(2, 4, 2, 64, 32, "int8", seed=32)
+    x.fill_up([100, 60])
+    q = x.rows(2 * rows)
+    args = (ints(x.table), ints(x.held), cumulative([rows, rows]), rows)
+    none = kv8.Cache(0, 2, 64, 32, "int8", device=DEV)
+    for cache, max_kv in ((x.cache, 0), (none, 128)):
+        out, lse = cache.attend(q, *args, max_kv)
+        assert not out.any() and torch.isneginf(lse).all()
+        assert (cache.select(q, *args, max_kv, 16, 2) == -1).all()
+    k, v = none.gather(ints(x.table), ints([0, 0]), cumulative([5, 6]), 11, 6)
+    assert not k.any() and not v.any()
+    none.append(x.rows(11), x.rows(11), ints(x.table), ints([0, 0]), cumulative([5, 6]), 6)
+    torch.cuda.synchronize()
+
+
+def test_offsets_out_of_order_or_range_are_clamped():
+    """Offsets that fall, or pass the token rows, describe sequences that are short or empty."""
+    x = Both(4, 4, 1, 64, 32, "int8", seed=33)
+    x.fill_up([100, 60, 128, 30])
+    table, held = ints(x.table), ints(x.held)
+    q = x.rows(20)
+    out, lse = torch.full_like(q, 5.0), torch.full((20, 1), 5.0, device=DEV)
+    x.cache.attend(q, table, held, ints([-3, 5, 2, -9, 1 << 30]), 15, 128, out=out, lse=lse)
+    # sequence 0 has rows 0 .. 4; 1 and 2 have none; 3 has rows 0 .. 14 (of those up to 20)
+    a, al = x.cache.attend(q, table[3:].contiguous(), held[3:].contiguous(), ints([0, 15]), 15, 128)
+    assert torch.equal(out[5:15], a[5:15]) and torch.equal(lse[5:15], al[5:15])
+    assert (out[15:] == 5).all() and (lse[15:] == 5).all()
 
 
 def test_attend_strided_rows_and_max_kv():

@@ -193,3 +193,22 @@ def test_launches_past_the_grid_limit_are_refused():
     b = batch(batch=65535, tokens=(1 << 31) - 1, max_rows=(1 << 31) - 1)
     for call in CALLS:
         assert call(b=b) in (cfz.CFZ_ERR_SHAPE, cfz.CFZ_ERR_WORKSPACE)
+
+
+def test_row_and_grid_limits():
+    b = batch(batch=1, tokens=1 << 25, max_rows=1 << 25)
+    kw = dict(c=cache(kv_heads=1), heads=64, qs=64 * 64)
+    assert attend(b=b, os_=64 * 64, **kw) == cfz.CFZ_ERR_SHAPE
+    assert select(b=b, bl=lists(q_block=1 << 25), **kw) == cfz.CFZ_ERR_SHAPE
+    assert append(c=cache(kv_heads=128), b=batch(tokens=1 << 21, max_rows=1 << 21), ks=8192,
+                  vs=8192) == cfz.CFZ_ERR_SHAPE
+    assert cfz.cfz_last_error().endswith("work-groups (limit 2^23)")
+
+
+def test_lists_count_whole_in_the_workspace():
+    """The parts of a call with lists are counted by the lists' places, whatever max_kv is."""
+    c, b = cache(), batch(table_width=64)
+    need = [cfz._lib.cfz_kv8_attend_workspace_bytes(C.byref(c), C.byref(b), 2, kv,
+                                                    C.byref(lists(count=4096, q_block=16)))
+            for kv in (2, 2048)]
+    assert need[0] == need[1] > 0

@@ -480,11 +480,9 @@ __device__ inline void append_values(const Kv8Cache &c, const T *v, int64_t v_st
 #pragma unroll
             for (int j = 0; j < W; ++j) {
                 const uint32_t was = o[j * ROW];
-                const float pair0 = t & 1 ? w[i][1][j] : w[i][0][j];
-                const float pair1 = t & 1 ? w[i][3][j] : w[i][2][j];
-                const float now = t & 2 ? pair1 : pair0;
-                const double y = slot >= lo ? (double)now
-                                            : (double)code_value(was >> (8 * t) & 0xff, c.fmt) * prior;
+                double y = t == 0 ? w[i][0][j] : t == 1 ? w[i][1][j] : t == 2 ? w[i][2][j] : w[i][3][j];
+                if (slot < lo)
+                    y = (double)code_value(was >> (8 * t) & 0xff, c.fmt) * prior;
                 o[j * ROW] = (was & ~(0xffu << (8 * t))) | encode(y, scale, rinv, c.fmt) << (8 * t);
             }
         }

@@ -1,7 +1,9 @@
 """libcfz for AMD Instinct MI355X: the CompactFusion residual-compression codec
 (fused residual + error feedback + group int4/int2 quantization, decode + base
-update) and the rank-r subspace-iteration compressor, as hand-written HIP for
-gfx950 behind a C ABI (``include/cfz.h``).  ``cfz`` is the ctypes binding.
+update), the rank-r subspace-iteration compressor, and the 8-bit paged K/V cache
+that receives what was exchanged, with the attention over it, as hand-written HIP
+for gfx950 behind C ABIs (``include/cfz.h``, ``include/cfz_kv8.h``).  ``cfz`` and
+``kv8`` are the ctypes bindings.
 
 The binding is imported on first use, not with the package, so that
 ``diffusion_activation_residual_amd.build`` can compile ``libcfz.so`` in a tree

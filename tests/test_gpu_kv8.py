@@ -622,6 +622,91 @@ def test_codec_to_cache_to_attention():
         check_attend(x, [rows], 1, False, "bf16", lists=lists, q_block=32)
 
 
+@pytest.mark.parametrize("count,group", [(None, 1), (3, 2)])
+def test_layers_of_shares_on_streams(count, group):
+    """Three layers over an own share and two received ones of other sizes, two items each: on
+    two streams eagerly and in a replayed graph, against one stream and the model."""
+    from diffusion_activation_residual_amd import cadence
+    heads, dim, page, batch, tokens, nq, L = 2, 64, 32, 2, [40, 96, 33], 40, 3
+    turn = rotation(sum(tokens), dim, "halves")
+    plan = cadence.SharePlan(batch, tokens, nq, page, turn, 16, count, 0, 1, device=DEV)
+    gen = torch.Generator().manual_seed(34)
+
+    def randn(n, h):
+        return torch.randn((n, h, dim), generator=gen).bfloat16().to(DEV)
+
+    x0 = [[(randn(batch * n, heads), randn(batch * n, heads)) for n in tokens] for _ in range(L)]
+    snd = [[[cfz.Sender(len(t), heads * dim, x0=t) for t in pair] for pair in layer[1:]]
+           for layer in x0]
+    q = [randn(batch * nq, heads * group) for _ in range(L)]
+
+    class Side:
+        def __init__(self):
+            self.rcv = [[[cfz.Receiver(len(t), heads * dim, x0=t) for t in pair]
+                         for pair in layer[1:]] for layer in x0]
+            self.own = [[t.clone() for t in layer[0]] for layer in x0]
+            self.caches = [kv8.Cache(plan.pages, heads, dim, page, device=DEV) for _ in range(L)]
+            self.out = [torch.full_like(t, 5.0) for t in q]
+
+        def step(self, streams):
+            layers = [[cadence.Share(*self.own[l])] +
+                      [cadence.Share(*(r.base.view(-1, heads, dim) for r in rs),
+                                     tuple(r.handle for r in rs), tuple(s.codes for s in ss),
+                                     tuple(s.scales for s in ss))
+                       for rs, ss in zip(self.rcv[l], snd[l])] for l in range(L)]
+            cadence.enqueue_layer_attention(plan, layers, self.caches, q, self.out, streams)
+
+    a, b, g = Side(), Side(), Side()
+    cap = torch.cuda.Stream()
+    streams = [torch.cuda.current_stream(), torch.cuda.Stream()]
+    for step in range(4):
+        for l in range(L):
+            for side in (a, b, g):
+                for t, z in zip(side.own[l], x0[l][0]):
+                    t.copy_(z * (1.0 + step))
+            for pair, ss in zip(x0[l][1:], snd[l]):
+                for t, s in zip(pair, ss):
+                    s.compress((t.float() * (1.0 + 0.1 * step)).bfloat16())
+        say(f"[gpu] step {step}")
+        a.step(streams)
+        b.step(streams[:1])
+        if step == 0:
+            torch.cuda.synchronize()
+            g.step(streams[:1])  # (the captured step starts from the second one)
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=cap):
+                g.step([cap, streams[1]])
+        else:
+            graph.replay()
+        torch.cuda.synchronize()
+        for l in range(L):
+            for side in (b, g):
+                assert torch.equal(a.out[l], side.out[l]), f"step {step}, layer {l}"
+                assert torch.equal(a.caches[l].k, side.caches[l].k)
+                assert torch.equal(a.caches[l].v, side.caches[l].v)
+    x = Both(batch, plan.width, heads, dim, page, "int8", spare=0)
+    x.cache, x.table, x.held = a.caches[0], plan.table.cpu().numpy(), [sum(tokens)] * batch
+    x.model.ks[:], x.model.vs[:], x.model.km[:] = 0, 0, 0
+    x.fill = 0  # (the pool was allocated as zeros)
+    rot = (to64(turn.cos), to64(turn.sin), False)
+    shares = [a.own[0]] + [[r.base.view(-1, heads, dim) for r in rs] for rs in a.rcv[0]]
+    # (every step writes all shares from the first token on: earlier steps leave nothing)
+    for item in range(batch):
+        for i, n in enumerate(tokens):
+            k, v = (to64(t[item * n:(item + 1) * n]) for t in shares[i])
+            x.model.append(k, v, x.table[item], sum(tokens[:i]), rot, None)
+    x.check()
+    check_attend(x, [nq] * batch, group, False, "bf16")
+    lists = None
+    if count:
+        lists = a.caches[0].select(q[0], plan.table, plan.lengths, plan.q_offsets, nq, plan.tokens,
+                                   16, count, 0, 1)
+    want, _ = a.caches[0].attend(q[0], plan.table, plan.lengths, plan.q_offsets, nq, plan.tokens,
+                                 blocks=lists, q_block=16)
+    assert torch.equal(a.out[0], want)
+
+
 @pytest.mark.parametrize("rows", [1, 48])
 def test_captured_step_replays_like_eager(rows):
     """Append, select and both attentions in one HIP graph: lengths on the device move on from replay

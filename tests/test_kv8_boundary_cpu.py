@@ -212,3 +212,40 @@ def test_lists_count_whole_in_the_workspace():
                                                     C.byref(lists(count=4096, q_block=16)))
             for kv in (2, 2048)]
     assert need[0] == need[1] > 0
+
+
+def test_share_plan():
+    from diffusion_activation_residual_amd import cadence
+    p = cadence.SharePlan(2, [40, 96, 33], 40, 32, device="cpu")
+    assert (p.tokens, p.width, p.pages) == (169, 6, 12)
+    assert p.table.tolist() == [[0, 1, 2, 3, 4, 5], [6, 7, 8, 9, 10, 11]]
+    assert [s.tolist() for s in p.starts] == [[0, 0], [40, 40], [136, 136]]
+    assert [o.tolist() for o in p.offsets] == [[0, 40, 80], [0, 96, 192], [0, 33, 66]]
+    assert p.lengths.tolist() == [169, 169] and p.q_offsets.tolist() == [0, 40, 80]
+    for bad in (dict(batch=0), dict(share_tokens=[]), dict(share_tokens=[3, 0]), dict(queries=0),
+                dict(page_tokens=48), dict(count=0), dict(count=2, first=2, last=1),
+                dict(count=1, q_block=0), dict(count=1, first=-1)):
+        kw = dict(batch=1, share_tokens=[8], queries=1, page_tokens=32, device="cpu")
+        with pytest.raises(ValueError):
+            cadence.SharePlan(**{**kw, **bad})
+
+
+def test_layer_attention_refusals():
+    """Everything is checked before a stream is touched (none of these calls gets that far)."""
+    from types import SimpleNamespace as N
+
+    import torch
+
+    from diffusion_activation_residual_amd import cadence
+    plan = cadence.SharePlan(2, [8, 8], 4, 32, device="cpu")
+    t, q = torch.zeros(16, 2, 64), torch.zeros(8, 2, 64)
+    pool, share = N(page_tokens=32, pages=2), cadence.Share(t, t)
+    good = dict(layers=[[share, share]], caches=[pool], q=[q], out=[q], streams=[])
+    for bad in (dict(), dict(layers=[]), dict(out=[q, q]), dict(layers=[[share]]),
+                dict(layers=[[share, cadence.Share(t[1:], t)]]),
+                dict(layers=[[share, cadence.Share(t, t, receivers=(1, 2))]]),
+                dict(layers=[[share, cadence.Share(t, t, codes=(t, t), scales=(t, t))]]),
+                dict(q=[q[1:]]), dict(caches=[N(page_tokens=64, pages=2)]),
+                dict(caches=[N(page_tokens=32, pages=1)])):
+        with pytest.raises(ValueError):
+            cadence.enqueue_layer_attention(plan, **{**good, **bad})

@@ -118,8 +118,8 @@ cfz_status check_queries(const cfz::Kv8Cache &c, const cfz::Kv8Batch &b, int32_t
 {
     if (q_heads < c.heads || q_heads % c.heads != 0 || q_heads / c.heads > 64)
         return fail(CFZ_ERR_SHAPE, "q_heads = %d with kv_heads = %d", q_heads, c.heads);
-    if (max_kv < 0 || max_kv > (int64_t)b.width * c.page)
-        return fail(CFZ_ERR_SHAPE, "max_kv = %lld (table: %lld)", (long long)max_kv,
+    if (max_kv < 0 || max_kv > (int64_t)b.width * c.page || max_kv > 1 << 30)
+        return fail(CFZ_ERR_SHAPE, "max_kv = %lld (table: %lld, at most 2^30)", (long long)max_kv,
                     (long long)b.width * c.page);
     if (blocks) {
         if (blocks->count < 1 || blocks->count > 4096)

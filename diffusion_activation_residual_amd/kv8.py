@@ -183,6 +183,8 @@ class Cache:
         return with_both
 
     def _call(self, call, stream, *args):
+        if stream is not None and not isinstance(stream, int) and stream.device != self.device:
+            raise ValueError(f"stream on {stream.device}, the cache is on {self.device}")
         if torch.cuda.current_device() == self.device.index:
             st = call(*args, cfz._stream(stream))
         else:

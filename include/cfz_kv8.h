@@ -145,7 +145,7 @@ typedef struct {
  * blocks (NULL: all pages) restricts it to its block's listed pages.  A row that sees
  * nothing gets out = 0 and lse = -infinity.
  * max_kv: an upper bound of the lengths, known on the host (it decides into how many
- * parts the keys are split; longer sequences are cut off there).  scale is finite
+ * parts the keys are split; longer sequences are cut off there), at most 2^30.  scale is finite
  * and > 0.  The products run on the codes in fp16 (which holds every code exactly; each
  * query row is first scaled by a power of two, so that a bf16 or fp16 q is held exactly down to
  * 2^-29 of its largest entry), accumulate in fp32, and the weights enter the second

@@ -203,6 +203,8 @@ def test_row_and_grid_limits():
     assert append(c=cache(kv_heads=128), b=batch(tokens=1 << 21, max_rows=1 << 21), ks=8192,
                   vs=8192) == cfz.CFZ_ERR_SHAPE
     assert cfz.cfz_last_error().endswith("work-groups (limit 2^23)")
+    assert attend(b=batch(table_width=(1 << 25) + 1), max_kv=(1 << 30) + 1) == cfz.CFZ_ERR_SHAPE
+    assert cfz.cfz_last_error().endswith("at most 2^30)")
 
 
 def test_lists_count_whole_in_the_workspace():

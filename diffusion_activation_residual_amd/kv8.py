@@ -9,7 +9,6 @@ before any device work) tensors that do not fit the call."""
 from __future__ import annotations
 
 import ctypes as C
-from contextlib import ExitStack, nullcontext
 from dataclasses import dataclass
 from typing import Optional
 
@@ -86,7 +85,7 @@ def _ints(t, shape, device, what):
         raise ValueError(f"{what}: on {t.device}, the cache is on {device}")
     if not t.is_contiguous():
         raise ValueError(f"{what}: must be contiguous")
-    if shape is not None and tuple(t.shape) != shape:
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {shape}")
     return t.data_ptr()
 
@@ -95,11 +94,12 @@ def _rows(t, heads, dim, device, what):
     """[tokens, heads, dim] with dense rows; returns the row stride in elements."""
     if t.device != device:
         raise ValueError(f"{what}: on {t.device}, the cache is on {device}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected [tokens, {heads}, {dim}]")
-    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim)):
-        raise ValueError(f"{what}: a token's heads must lie side by side (strides {t.stride()})")
-    return t.stride(0) if t.shape[0] > 1 else heads * dim
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{what}: shape {tuple(shape)}, expected [tokens, {heads}, {dim}]")
+    if (stride[2] != 1 or (heads > 1 and stride[1] != dim)) and t.numel():
+        raise ValueError(f"{what}: a token's heads must lie side by side (strides {stride})")
+    return stride[0] if shape[0] > 1 else heads * dim
 
 
 class Cache:
@@ -173,23 +173,28 @@ class Cache:
                              _ints(offsets, (batch + 1,), self.device, "offsets"),
                              _ints(lengths, (batch,), self.device, "lengths"), tokens, max_rows)
 
-    def _on(self, stream):
-        """The cache's device and `stream`, for the allocations of a call."""
-        if stream is None and torch.cuda.current_device() == self.device.index:
-            return nullcontext()
-        with_both = ExitStack()
-        with_both.enter_context(torch.cuda.device(self.device))
-        with_both.enter_context(torch.cuda.stream(stream))
-        return with_both
+    def _empty(self, stream, shape, dtype):
+        """Memory that belongs to the work queued on `stream` (None: the current one)."""
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        if isinstance(stream, int):
+            raise ValueError("a raw stream handle needs explicit outputs and workspace")
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
 
     def _call(self, call, stream, *args):
-        if stream is not None and not isinstance(stream, int) and stream.device != self.device:
-            raise ValueError(f"stream on {stream.device}, the cache is on {self.device}")
-        if torch.cuda.current_device() == self.device.index:
-            st = call(*args, cfz._stream(stream))
+        index = self.device.index
+        if stream is None:  # (the public current_stream() costs as much as the rest of a call)
+            stream = torch._C._cuda_getCurrentRawStream(index)
+        elif not isinstance(stream, int):
+            if stream.device != self.device:
+                raise ValueError(f"stream on {stream.device}, the cache is on {self.device}")
+            stream = stream.cuda_stream
+        if torch.cuda.current_device() == index:
+            st = call(*args, stream)
         else:
-            with torch.cuda.device(self.device):
-                st = call(*args, cfz._stream(stream))
+            with torch.cuda.device(index):
+                st = call(*args, stream)
         if st != CFZ_OK:
             raise CfzError(st, call.__name__)
 
@@ -202,10 +207,7 @@ class Cache:
             return workspace, workspace.numel() * workspace.element_size()
         if nbytes == 0:
             return None, 0
-        if isinstance(stream, int):
-            raise ValueError("a raw stream handle needs an explicit workspace")
-        with self._on(stream):
-            return torch.empty(nbytes, dtype=torch.uint8, device=self.device), nbytes
+        return self._empty(stream, nbytes, torch.uint8), nbytes
 
     # ---- calls
 
@@ -243,11 +245,8 @@ class Cache:
         no sequence are then left unset)."""
         shape = (tokens, self.kv_heads, self.head_dim)
         if k is None and v is None:
-            if isinstance(stream, int):
-                raise ValueError("a raw stream handle needs explicit outputs")
-            with self._on(stream):
-                k = torch.empty(shape, dtype=dtype, device=self.device)
-                v = torch.empty(shape, dtype=dtype, device=self.device)
+            k = self._empty(stream, shape, dtype)
+            v = self._empty(stream, shape, dtype)
         for t, what in ((k, "k"), (v, "v")):
             if t is not None and (tuple(t.shape) != shape or t.dtype != dtype or
                                   t.device != self.device or not t.is_contiguous()):
@@ -281,8 +280,6 @@ class Cache:
         not given are allocated (rows of no sequence are then left unset)."""
         stride = self._queries(q)
         tokens, heads = q.shape[:2]
-        if stream is not None and isinstance(stream, int) and (out is None or lse is None):
-            raise ValueError("a raw stream handle needs explicit outputs")
         batch = self._batch(page_table, lengths, offsets, tokens, max_q)
         lists = None
         if blocks is not None:
@@ -293,18 +290,17 @@ class Cache:
         need = _lib.cfz_kv8_attend_workspace_bytes(self._ref, C.byref(batch), heads,
                                                    max_kv, lists)
         workspace, have = self._workspace(need, workspace, stream)
-        if out is None or lse is None:
-            with self._on(stream):
-                if out is None:
-                    out = torch.empty((tokens, heads, self.head_dim), dtype=q.dtype,
-                                      device=self.device)
-                if lse is None:
-                    lse = torch.empty((tokens, heads), dtype=torch.float32, device=self.device)
-        ostride = _rows(out, heads, self.head_dim, self.device, "out")
-        if out.dtype != q.dtype or out.shape != q.shape:
-            raise ValueError("out: must have q's shape and dtype")
-        if (tuple(lse.shape) != (tokens, heads) or lse.dtype != torch.float32 or
-                lse.device != self.device or not lse.is_contiguous()):
+        ostride = heads * self.head_dim
+        if out is None:
+            out = self._empty(stream, (tokens, heads, self.head_dim), q.dtype)
+        else:
+            ostride = _rows(out, heads, self.head_dim, self.device, "out")
+            if out.dtype != q.dtype or out.shape != q.shape:
+                raise ValueError("out: must have q's shape and dtype")
+        if lse is None:
+            lse = self._empty(stream, (tokens, heads), torch.float32)
+        elif (lse.shape != (tokens, heads) or lse.dtype != torch.float32 or
+              lse.device != self.device or not lse.is_contiguous()):
             raise ValueError(f"lse: expected a contiguous fp32 tensor {(tokens, heads)}")
         self._call(_lib.cfz_kv8_attend, stream, self._ref, C.byref(batch), _REALS[q.dtype],
                    q.data_ptr(), stride, heads, bool(causal),
@@ -326,11 +322,8 @@ class Cache:
             raise ValueError(f"q_block = {q_block}, count = {count}: at least 1")
         batch = self._batch(page_table, lengths, offsets, q.shape[0], max_q)
         if blocks is None:
-            if isinstance(stream, int):
-                raise ValueError("a raw stream handle needs explicit outputs")
-            with self._on(stream):
-                blocks = torch.empty((batch.batch, -(-max_q // q_block), self.kv_heads, count),
-                                     dtype=torch.int32, device=self.device)
+            blocks = self._empty(stream, (batch.batch, -(-max_q // q_block), self.kv_heads, count),
+                                 torch.int32)
         lists = self._lists(blocks, batch, max_q, q_block, count)
         need = _lib.cfz_kv8_select_workspace_bytes(self._ref, C.byref(batch), max_kv,
                                                    C.byref(lists))

@@ -464,11 +464,16 @@ __device__ inline void append_values(const Kv8Cache &c, const T *v, int64_t v_st
         if (tq >= P / 4 || (tq * 4 >= hi) || (tq * 4 + 4 <= lo && !grown))
             continue;
         uint32_t *o = vpage + dq * W * ROW + tq;
-        if (mid && tq * 4 >= lo && tq * 4 + 4 <= hi) {
+        if (mid && (tq * 4 >= lo || !grown)) {
+            // the bytes of the unit's new tokens
+            const int skip = lo - tq * 4, end = hi - tq * 4;
+            const uint32_t fresh = (end >= 4 ? ~0u : (1u << (8 * end)) - 1u) &
+                                   (skip <= 0 ? ~0u : ~0u << (8 * skip));
 #pragma unroll
             for (int j = 0; j < W; ++j) {
                 const double x[4] = {w[i][0][j], w[i][1][j], w[i][2][j], w[i][3][j]};
-                o[j * ROW] = encode4(x, scale, rinv, c.fmt);
+                const uint32_t code = encode4(x, scale, rinv, c.fmt);
+                o[j * ROW] = fresh == ~0u ? code : (o[j * ROW] & ~fresh) | (code & fresh);
             }
             continue;
         }

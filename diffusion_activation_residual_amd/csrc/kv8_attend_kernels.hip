@@ -1069,7 +1069,7 @@ __global__ __launch_bounds__(NW * 64, 2) void kv8_attend_wide_kernel(Kv8Cache c,
 
 // Joins the runs of the tile that work-group blockIdx.x began and did not finish: kPieces 16-byte
 // pieces per thread, read together.
-constexpr int kPieces = 4;
+constexpr int kPieces = 2;
 
 template <int BM, int D>
 __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8Cache c, Kv8Batch b, Kv8Attend a,

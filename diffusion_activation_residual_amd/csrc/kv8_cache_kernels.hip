@@ -227,12 +227,15 @@ __device__ inline bool find_place(const Kv8Cache &c, const Kv8Batch &b, int span
 // values of 8 bits lie near one time and again.
 //
 // Keys: units of 8 dimensions (two groups of 4 that hold whole rotation pairs).
-template <class T, int D, int P, bool ROT>
+constexpr int kStay = 0, kPairs = 1, kHalves = 2;  // how keys turn
+
+template <class T, int D, int P, int TURN>
 __device__ inline void append_keys(const Kv8Cache &c, const T *k, int64_t k_stride,
                                    const Kv8Rotation &rot, const Place &pl, int head)
 {
     constexpr int U = D / 8;                // key units per token
     constexpr int NK = P * U / kThreads;    // key units per thread
+    constexpr bool ROT = TURN != kStay;
     using Held = std::conditional_t<ROT, double, float>;  // what holds a key exactly
     __shared__ int sums[D];
     __shared__ Held red[4];
@@ -242,7 +245,7 @@ __device__ inline void append_keys(const Kv8Cache &c, const T *k, int64_t k_stri
     // (all units of a thread are of the same dimensions: U divides kThreads)
     const int half = ROT ? rot.dim / 2 : 0;
     const int u = tid % U;
-    const bool turn = 8 * u < 2 * half, split = turn && !rot.interleaved;
+    const bool turn = ROT && 8 * u < 2 * half, split = TURN == kHalves && turn;
     const int d0 = split ? 4 * u : 8 * u, d1 = split ? half + 4 * u : 8 * u + 4;
     const T *src = k + pl.src0 * k_stride + (int64_t)head * D;
     if (tid < D)
@@ -287,32 +290,35 @@ __device__ inline void append_keys(const Kv8Cache &c, const T *k, int64_t k_stri
                 if (turn) {
                     const float cc[4] = {cs[i].x, cs[i].y, cs[i].z, cs[i].w};
                     const float ss[4] = {sn[i].x, sn[i].y, sn[i].z, sn[i].w};
-                    double r[8];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
+                        const int p0 = TURN == kHalves ? j : 2 * j;
+                        const int p1 = TURN == kHalves ? 4 + j : 2 * j + 1;
                         // products of two fp32 values are exact in fp64
-                        const double y0 = split ? a[i][j] : a[i][2 * j];
-                        const double y1 = split ? a[i][4 + j] : a[i][2 * j + 1];
-                        const double co = cc[j], si = ss[j];
+                        const double y0 = a[i][p0], y1 = a[i][p1], co = cc[j], si = ss[j];
                         bad = fmaf(cc[j], 0.0f, fmaf(ss[j], 0.0f, bad));
-                        r[2 * j] = fma(y0, co, -(y1 * si));
-                        r[2 * j + 1] = fma(y0, si, y1 * co);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        x[i][j] = split ? r[2 * j] : r[j];
-                        x[i][4 + j] = split ? r[2 * j + 1] : r[4 + j];
+                        x[i][p0] = fma(y0, co, -(y1 * si));
+                        x[i][p1] = fma(y0, si, y1 * co);
                     }
                 }
             }
         }
     }
+    // a thread that holds something not finite looks through its values again
     const bool odd = !(bad == 0.0f);
 #pragma unroll
     for (int i = 0; i < NK; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            big = fmax(big, odd ? (Held)finite_or_zero(x[i][j]) : (Held)fabs(x[i][j]));
+            big = fmax(big, (Held)fabs(x[i][j]));
+    if (odd) {
+        big = 0;
+#pragma unroll
+        for (int i = 0; i < NK; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                big = fmax(big, (Held)finite_or_zero(x[i][j]));
+    }
     big = block_max(big, red);
     const double qmax = c.fmt == CFZ_KV8_INT8 ? 127.0 : 448.0;
     const float scale = fmaxf(prior, (float)((double)big / qmax));
@@ -499,7 +505,7 @@ __device__ inline void append_values(const Kv8Cache &c, const T *v, int64_t v_st
     }
 }
 
-template <class T, int D, int P, bool ROT>
+template <class T, int D, int P, int TURN>
 __global__ __launch_bounds__(kThreads) void kv8_append_kernel(Kv8Cache c, Kv8Batch b, const T *k,
                                                               const T *v, int64_t k_stride,
                                                               int64_t v_stride, Kv8Rotation rot,
@@ -513,7 +519,7 @@ __global__ __launch_bounds__(kThreads) void kv8_append_kernel(Kv8Cache c, Kv8Bat
     if (blockIdx.x & 1)
         append_values<T, D, P>(c, v, v_stride, pl, head);
     else
-        append_keys<T, D, P, ROT>(c, k, k_stride, rot, pl, head);
+        append_keys<T, D, P, TURN>(c, k, k_stride, rot, pl, head);
 }
 
 // Reads one page of one head back: keys straight, values through LDS (their codes are dimension-major),
@@ -825,7 +831,9 @@ hipError_t append_as(const Kv8Cache &c, const Kv8Batch &b, const void *k, const 
     const dim3 grid((unsigned)(2 * page_groups(c, b, span)));
 #define CFZ_KV8_CASE(D, P)                                                                         \
     if (c.dim == D && c.page == P)                                                                 \
-        (rot.cos ? kv8_append_kernel<T, D, P, true> : kv8_append_kernel<T, D, P, false>)            \
+        (!rot.cos          ? kv8_append_kernel<T, D, P, kStay>                                      \
+         : rot.interleaved ? kv8_append_kernel<T, D, P, kPairs>                                     \
+                           : kv8_append_kernel<T, D, P, kHalves>)                                   \
             <<<grid, kThreads, 0, st>>>(c, b, (const T *)k, (const T *)v, ks, vs, rot, span);
     CFZ_KV8_CASE(64, 32)
     CFZ_KV8_CASE(64, 64)

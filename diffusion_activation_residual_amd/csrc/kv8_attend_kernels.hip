@@ -631,8 +631,8 @@ __global__ __launch_bounds__(256, 2) void kv8_attend_narrow_kernel(Kv8Cache c, K
 // code once instead of once per wave).  At NW = 8 two waves share a SIMD and run a phase apart:
 // one multiplies while the other forms weights, since a step's weights (an fp32 product, an
 // exponential and half a conversion per score) take about as long as its products.  Measured with the
-// join: 1024 queries over 4096 keys, 24 heads of 128, 99 us, 520 TFLOP/s; 4388 queries over 17552 keys,
-// 30 heads of 64, 820 us, 720 TFLOP/s; products alone reach 1900 in this instruction.  With both
+// join: 1024 queries over 4096 keys, 24 heads of 128, 92 us, 560 TFLOP/s; 4388 queries over 17552
+// keys, 30 heads of 64, 740 to 760 us, 790 TFLOP/s; products alone reach 1900 in this instruction.  With both
 // kinds of work in every wave, one step's products between the other's weights, the registers
 // spilled; with products and weights one after the other it was 1141 us.
 //

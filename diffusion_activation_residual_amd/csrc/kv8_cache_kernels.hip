@@ -10,11 +10,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-template <int DT> struct Src;
-template <> struct Src<CFZ_KV8_BF16> { using T = uint16_t; };
-template <> struct Src<CFZ_KV8_F16> { using T = _Float16; };
-template <> struct Src<CFZ_KV8_F32> { using T = float; };
-
 __device__ inline float widen(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
 __device__ inline float widen(_Float16 h) { return (float)h; }
 __device__ inline float widen(float f) { return f; }
@@ -141,7 +136,7 @@ template <class T> __device__ inline T block_max(T x, T *red)
     return fmax(fmax(red[0], red[1]), fmax(red[2], red[3]));
 }
 
-// The same for four finite x whose magnitudes are at most a step of fp32 above the largest code
+// encode() for four finite x whose magnitudes are at most a step of fp32 above the largest code
 // times s, and s within 2^-100 .. 2^100: nothing to cut off, no remainder lost.
 __device__ inline uint32_t encode4(const double (&x)[4], double s, double rinv, int fmt)
 {
@@ -223,8 +218,12 @@ __device__ inline bool find_place(const Kv8Cache &c, const Kv8Batch &b, int span
 // mean, and change if the scale grows).  Rotation and quotients are in fp64: a product by 1 / s alone
 // loses ties (49 (1 / 49) < 1), with the remainder put right it is the rounded quotient.  What is not
 // finite, and scales far from 1, take a slower way.  fp32 with a test for quotients near a border,
-// and fp64 for those alone, was slower (130 against 105 us on 4 x 4388 tokens x 30 heads of 64, bf16):
-// values of 8 bits lie near one time and again.
+// and fp64 for those alone, was slower (130 against 97 us on 4 x 4388 tokens x 30 heads of 64, bf16):
+// values of 8 bits lie near one time and again.  The rotated keys' fp64 values leave 4 waves a SIMD,
+// which bounds it: 4 x 4388 tokens x 30 heads of 64 from bf16 in 72 us, 2.8 TB/s, against 48 us, 4.2
+// TB/s, without rotation (int8, the same buffers again and again; other buffers each time, e4m3, 97
+// us); from fp32 5.1 TB/s.  Few tokens wait for dependent reads (offset,
+// length, page, codes): 32 single tokens x 8 heads of 128 in 8 us.
 //
 // Keys: units of 8 dimensions (two groups of 4 that hold whole rotation pairs).
 constexpr int kStay = 0, kPairs = 1, kHalves = 2;  // how keys turn
@@ -523,7 +522,8 @@ __global__ __launch_bounds__(kThreads) void kv8_append_kernel(Kv8Cache c, Kv8Bat
 }
 
 // Reads one page of one head back: keys straight, values through LDS (their codes are dimension-major),
-// rows written in vectors of 4 values.
+// rows written in vectors of 4 values.  Bound by the bytes written: 4 x 4388 tokens x 30 heads of 64
+// to fp32 in 58 us, 5.8 TB/s.
 template <class T, int D, int P>
 __global__ __launch_bounds__(kThreads) void kv8_gather_kernel(Kv8Cache c, Kv8Batch b, T *k, T *v,
                                                               int span)
@@ -609,7 +609,7 @@ __device__ inline uint64_t order_key(double s)
 // queries are summed in fp64 and the products are too: 64 bits where two pages' scores may differ in
 // the last bit of fp32.  A query row is read by D / 8 lanes (16 bytes each) and a page's mean by 8
 // lanes, so that loads are wide and the sums across lanes short.  Bound by latency (a few dozen KB
-// per work-group).
+// per work-group): 35 blocks of 128 queries x 138 pages x 30 heads of 64 in 18.5 us.
 constexpr int kScorePages = 64;
 
 template <int D>
@@ -714,7 +714,9 @@ __global__ __launch_bounds__(kThreads) void kv8_score_kernel(Kv8Cache c, Kv8Batc
 
 // The `count` largest keys of one list: the threshold is found 8 bits at a time by counting
 // (the same work whatever the keys), then the pages above it and, in index order, as many at it as
-// are left are written in ascending order.
+// are left are written in ascending order.  Launch, dependent reads and the passes' barriers: 10.8 us
+// for 1050 lists of 138 pages, 10 us for 128 of up to 512; copies of the keys in LDS, and one wave a
+// list counting by ballots, took 10.3 and 9.0 to 13.9.
 __global__ __launch_bounds__(kThreads) void kv8_pick_kernel(Kv8Cache c, Kv8Batch b, Kv8Select a,
                                                             int units, int stride)
 {

@@ -41,7 +41,7 @@ typedef enum { CFZ_KV8_BF16 = 0, CFZ_KV8_F16 = 1, CFZ_KV8_F32 = 2 } cfz_kv8_dtyp
  *   k:       [pages][kv_heads][page_tokens][head_dim] codes
  *   v:       [pages][kv_heads][head_dim][page_tokens] codes (dimension-major: the
  *            order in which the product with the weights reads them)
- *   k_scale, v_scale: [pages][kv_heads] fp32
+ *   k_scale, v_scale: [pages][kv_heads] fp32, finite and >= 0 wherever tokens are held
  *   k_mean:  [pages][kv_heads][head_dim] fp32, the mean of the page's keys as held
  *            (scale times code); may be NULL if cfz_kv8_select is not used.
  * Together 2 * kv_heads * head_dim bytes a token.  Element counts may pass 2^32. */

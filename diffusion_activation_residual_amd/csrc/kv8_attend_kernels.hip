@@ -11,6 +11,14 @@
 // power of two has brought its largest entry to [2^14, 2^15) (exact for bf16 entries down to
 // 2^-29 of it); scores, statistics and output sums are fp32.
 //
+// A denominator's terms are then 2^(y_t - m) / z_t, and fp32 holds the ones that count only while the z_t
+// lie near each other: from 2^-32 to 2^32 the weight of a key whose score is 2^-54 of the highest is
+// still a normal number, and the sum over 2^30 keys is finite (6 + 16 + 32 + 30 powers of two).  Pages
+// whose values are zeros take part with z = 2^-32, at which nothing of them is lost or in the way.
+// Where a page that is looked up has a z outside of that range, the run goes on with the denominator
+// on its own: a second set of exponentials, of the scores alone, relative to a maximum ms of their own,
+// so that out = 2^(m - ms) sum_t 2^(y_t - m) e_t / sum_t 2^(score_t - ms).  In the ordinary case ms is m.
+//
 // Both kernels compute S^T = K Q^T: in the accumulator's layout a lane then holds scores of ONE query
 // (its column), so maximum, sum and rescaling need no exchange inside the loop, and the
 // weights are, as they lie, the B operand of O^T = V^T P^T.  The order of the keys inside a
@@ -38,9 +46,13 @@ constexpr float kSlack = 5.0f;      // (few rows) a row's maximum is moved where
 constexpr float kLimit = 60000.0f;  // (many rows) ... or where a lane's weights sum to more
 constexpr float kNone = -3.0e38f;
 constexpr float kTiny = -100.0f;  // log2 of the value scale up to which codes count as zeros
+constexpr float kNear = 32.0f;    // ordinary value scales lie within 2^-kNear .. 2^kNear
+constexpr float kApart = -kNear - kTiny;
+constexpr float kApartPower = 0x1p68f;  // 2^kApart; sums of 2^30 weights times codes (2^55) stay finite
 constexpr int kBlock = 64;  // keys per step
 constexpr int kMaxItems = 1023;  // tiles per head whose steps a work-group counts
 constexpr int kPrefixWords = kMaxItems + 1;
+constexpr int kRowWords = 4;     // of a part, for each row: m, ms, l
 constexpr int kCutWords = 4096;  // of the workspace: a Cut for each of at most 1024 work-groups
 
 __device__ inline float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -303,8 +315,22 @@ __device__ inline void find_scales(const Kv8Cache &c, const Tile &t, Half &h)
     }
 }
 
-// The value codes of a half count as zeros: a scale of 2^-100 or less (0 above all).
-__device__ inline bool flushed(const Half &h) { return !(h.add > kTiny); }
+// The value scale of a half that holds values lies outside of the ordinary range.
+__device__ inline bool is_far(const Half &h)
+{
+    return h.add > kTiny && !(h.add > -kNear && h.add <= kNear);
+}
+
+// The half as it is used: what counts as zeros (a scale of 2^-100 or less, 0 above all) has the lowest
+// z of all, and K's scale with its sign set to tell.
+__device__ inline Half settled(Half h, int apart)
+{
+    h.kscale = h.add > kTiny ? h.kscale : -h.kscale;
+    h.add = fmaxf(h.add, apart ? kTiny : -kNear);
+    return h;
+}
+
+__device__ inline bool flushed(const Half &h) { return (int)__float_as_uint(h.kscale) < 0; }
 
 // What a lane needs of a half: y = acc * mul + add, and the weight's share of the denominator, 2^-add.
 struct Factor {
@@ -315,7 +341,7 @@ __device__ inline Factor factor(const Half &h, float qmul)
 {
     Factor f;
     // not 0, so that the masked scores' -infinity stays one (the codes of scale 0 are zeros)
-    f.mul = fmaxf(h.kscale * qmul, 0x1p-120f);
+    f.mul = fmaxf(fabsf(h.kscale) * qmul, 0x1p-120f);
     f.add = h.add;
     f.back = exp2_fast(-h.add);
     return f;
@@ -388,18 +414,21 @@ __device__ inline void store_out(const Kv8Attend &a, int64_t at, float x0, float
     *(uint2 *)((uint16_t *)a.out + at) = w;
 }
 
-__device__ inline float lse_of(float m, float l)
+__device__ inline float lse_of(float ms, float l)
 {
-    return l > 0.0f ? (m - kLift + __builtin_log2f(l)) * 0.69314718055994531f
+    return l > 0.0f ? (ms - kLift + __builtin_log2f(l)) * 0.69314718055994531f
                     : (l == l ? -__builtin_inff() : l);
 }
 
+// 2^(m - ms) as a product of two equal factors (value scales reach 2^121).
+__device__ inline float half_power(float m, float ms) { return exp2_fast(0.5f * (m - ms)); }
+
 // A run's sums of its tile, fp32: 16-byte pieces of the rows' sums in the order in which the kernel's
-// lanes hold them, so that a store instruction covers one span, then m and l of each row.
+// lanes hold them, so that a store instruction covers one span, then m, ms, l and 0 of each row.
 template <int BM, int D>
 __device__ inline float *partial(const Kv8Attend &a, int64_t slot)
 {
-    return a.ws + kCutWords + slot * (BM * (D + 2));
+    return a.ws + kCutWords + slot * (BM * (D + kRowWords));
 }
 
 // ------------------------------------------------------------------ few rows
@@ -421,7 +450,8 @@ __global__ __launch_bounds__(256, 2) void kv8_attend_narrow_kernel(Kv8Cache c, K
     __shared__ int prefix[kPrefixWords], waves[4];
     constexpr int AHEAD = 128;  // steps whose pages are looked up together
     __shared__ Half halves[2 * AHEAD];
-    __shared__ float om[4][16], ol[4][16], oo[4][16][D + 4];
+    __shared__ int far[4];
+    __shared__ float om[4][16], os[4][16], ol[4][16], oo[4][16][D + 4];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
     const uint32_t wg = by_xcd((uint32_t)p.groups);
@@ -466,7 +496,8 @@ __global__ __launch_bounds__(256, 2) void kv8_attend_narrow_kernel(Kv8Cache c, K
 #pragma unroll
         for (int i = 0; i < DT; ++i)
             o[i] = f4{0, 0, 0, 0};
-        float m = kNone, l = 0.0f;
+        float m = kNone, ms = kNone, l = 0.0f;
+        int apart = 0;       // the denominator is summed on its own
 
         // Key row `col` of tile u is token 16 (col / 4) + 4 u + col % 4: accumulator i of lane group g
         // in tile u is then token 16 g + 4 u + i.
@@ -499,12 +530,27 @@ __global__ __launch_bounds__(256, 2) void kv8_attend_narrow_kernel(Kv8Cache c, K
 
         for (int first = run.s0; first < run.s1; first += AHEAD) {
             const int last = first + AHEAD < run.s1 ? first + AHEAD : run.s1;
-            __syncthreads();
-            for (int i = threadIdx.x; i < 2 * (last - first); i += 256) {
-                Half h = find_half(c, b, a, t, first * kBlock + 32 * i, reach_max);
-                find_scales(c, t, h);
-                halves[i] = h;
+            static_assert(2 * AHEAD == 256, "a half for each thread");
+            const int mine_at = threadIdx.x;
+            Half found = {-1, 0, 0.0f, kTiny};
+            if (mine_at < 2 * (last - first)) {
+                found = find_half(c, b, a, t, first * kBlock + 32 * mine_at, reach_max);
+                find_scales(c, t, found);
             }
+            const bool any_far = __any(is_far(found));
+            if (lane == 0)
+                far[wave] = any_far;
+            __syncthreads();
+            if (!apart && __builtin_amdgcn_readfirstlane(far[0] | far[1] | far[2] | far[3])) {
+                // from the lowest z of the ordinary range to the lowest of all
+                apart = 1;
+                ms = m;
+                m -= kApart;
+#pragma unroll
+                for (int i = 0; i < DT; ++i)
+                    o[i] *= kApartPower;
+            }
+            halves[mine_at] = settled(found, apart);
             __syncthreads();
             int s = first + wave;
             if (s < last)
@@ -553,7 +599,7 @@ __global__ __launch_bounds__(256, 2) void kv8_attend_narrow_kernel(Kv8Cache c, K
                     // (each row on its own terms: what it gets does not depend on the rows beside it)
                     const float now = top > m + kSlack ? top : m, fall = exp2_fast(m - now);
                     m = now;
-                    l *= fall;
+                    l *= apart ? 1.0f : fall;
 #pragma unroll
                     for (int i = 0; i < DT; ++i)
                         o[i] *= fall;
@@ -569,7 +615,28 @@ __global__ __launch_bounds__(256, 2) void kv8_attend_narrow_kernel(Kv8Cache c, K
                     w[i / 8][i % 8] = e[0];
                     w[i / 8][i % 8 + 1] = e[1];
                 }
-                l = fmaf(sum, f.back, l);
+                if (__builtin_expect(!apart, 1)) {
+                    l = fmaf(sum, f.back, l);
+                } else {
+                    // (the scores are y - add)
+                    float peak = y[0];
+#pragma unroll
+                    for (int i = 1; i < 16; ++i)
+                        peak = fmaxf(peak, y[i]);
+                    peak -= f.add;
+                    if (__any(peak > ms + kSlack)) {
+                        peak = fmaxf(peak, __shfl_xor(peak, 16));
+                        peak = fmaxf(peak, __shfl_xor(peak, 32));
+                        const float now = peak > ms + kSlack ? peak : ms;
+                        l *= exp2_fast(ms - now);
+                        ms = now;
+                    }
+                    sum = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        sum += exp2_fast(y[i] - f.add + (kLift - ms));
+                    l += sum;
+                }
 #pragma unroll
                 for (int i = 0; i < DT; ++i) {
                     o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
@@ -585,6 +652,7 @@ __global__ __launch_bounds__(256, 2) void kv8_attend_narrow_kernel(Kv8Cache c, K
         // join the four waves
         if (g == 0) {
             om[wave][col] = m;
+            os[wave][col] = apart ? ms : m;
             ol[wave][col] = l;
         }
 #pragma unroll
@@ -596,31 +664,34 @@ __global__ __launch_bounds__(256, 2) void kv8_attend_narrow_kernel(Kv8Cache c, K
             if (rr >= t.rows)
                 break;
             float mm = fmaxf(fmaxf(om[0][row], om[1][row]), fmaxf(om[2][row], om[3][row]));
+            float mms = fmaxf(fmaxf(os[0][row], os[1][row]), fmaxf(os[2][row], os[3][row]));
             // a NaN row stays one: its sums are NaN whatever the weights
             float ll = 0.0f;
             f4 s = {0, 0, 0, 0};
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
                 const float e = exp2_fast(om[w][row] - mm);
-                ll += ol[w][row] * e;
+                ll += ol[w][row] * exp2_fast(os[w][row] - mms);
                 s += *(const f4 *)&oo[w][row][d] * e;
             }
             if (run.slot >= 0) {
                 float *out = partial<BM, D>(a, run.slot);
                 if (d == 0)
-                    *(f2 *)(out + BM * D + 2 * row) = f2{mm, ll};
+                    *(f4 *)(out + BM * D + kRowWords * row) = f4{mm, mms, ll, 0.0f};
                 *(f4 *)(out + 4 * i) = s;
             } else {
                 const int64_t qrow = t.row0 + t.q0 + rr / a.group;
                 const int head = t.head * a.group + rr % a.group;
                 const float inv = ll > 0.0f ? 1.0f / ll : (ll == ll ? 0.0f : ll);
-                store_out(a, qrow * a.out_stride + (int64_t)head * D + d, s[0] * inv, s[1] * inv,
-                          s[2] * inv, s[3] * inv);
+                const float p = half_power(mm, mms);
+                s *= inv * p;
+                store_out(a, qrow * a.out_stride + (int64_t)head * D + d, s[0] * p, s[1] * p,
+                          s[2] * p, s[3] * p);
                 if (a.lse && d == 0)
-                    a.lse[qrow * a.q_heads + head] = lse_of(mm, ll);
+                    a.lse[qrow * a.q_heads + head] = lse_of(mms, ll);
             }
         }
-        __syncthreads();  // om, ol and oo are read
+        __syncthreads();  // om, os, ol and oo are read
     }
 }
 
@@ -669,6 +740,8 @@ __global__ __launch_bounds__(NW * 64, 2) void kv8_attend_wide_kernel(Kv8Cache c,
     __shared__ h8 ks[2][BK][D / 8];
     __shared__ h8 vs[2][D][VC];
     __shared__ Half halves[H * AHEAD];
+    __shared__ int far[NW];
+    __shared__ float alone[R][T];     // ms of the rows, where it is not m (seldom: not worth registers)
     __shared__ int prefix[kPrefixWords], waves[NW];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -723,6 +796,7 @@ __global__ __launch_bounds__(NW * 64, 2) void kv8_attend_wide_kernel(Kv8Cache c,
 
         f16v o[R][DT];
         float m[R], l[R];
+        int apart = 0;       // the denominator is summed on its own
 #pragma unroll
         for (int y = 0; y < R; ++y) {
 #pragma unroll
@@ -884,6 +958,39 @@ __global__ __launch_bounds__(NW * 64, 2) void kv8_attend_wide_kernel(Kv8Cache c,
         // its sums are rescaled and its weights are formed again: rare after the first steps, and one
         // comparison instead of a maximum over the scores of every step.  (Each row on its
         // own terms: what it gets does not depend on the rows beside it.)
+        // (The denominator on its own, from the masked scores: in the same way.)
+        auto add_alone = [&](int y, const Factor (&f)[H]) {
+            float ms = alone[y][tid];
+            auto weigh = [&]() {
+                float sum = 0.0f;
+#pragma unroll
+                for (int x = 0; x < H; ++x)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        sum += exp2_fast(fmaf(acc[y][x][j], f[x].mul, kLift - ms));
+                return sum;
+            };
+            float sum = weigh();
+            const int over = !(sum <= kLimit);
+            if (__any(over)) {
+                float top = kNone;
+#pragma unroll
+                for (int x = 0; x < H; ++x) {
+                    float z = acc[y][x][0];
+#pragma unroll
+                    for (int j = 1; j < 16; ++j)
+                        z = fmaxf(z, acc[y][x][j]);
+                    top = fmaxf(top, z * f[x].mul);
+                }
+                top = fmaxf(top, __shfl_xor(top, 32));
+                const bool move = over | __shfl_xor(over, 32);
+                const float now = move ? fmaxf(ms, top) : ms;
+                l[y] *= exp2_fast(ms - now);
+                ms = alone[y][tid] = now;
+                sum = weigh();
+            }
+            l[y] += sum;
+        };
         auto weights = [&](const Half (&h)[H]) {
 #pragma unroll
             for (int x = 0; x < H; ++x)
@@ -941,7 +1048,7 @@ __global__ __launch_bounds__(NW * 64, 2) void kv8_attend_wide_kernel(Kv8Cache c,
                     const bool move = over | __shfl_xor(over, 32);
                     const float now = move ? fmaxf(m[y], top) : m[y], fall = exp2_fast(m[y] - now);
                     m[y] = now;
-                    l[y] *= fall;
+                    l[y] *= apart ? 1.0f : fall;
 #pragma unroll
                     for (int i = 0; i < DT; ++i)
 #pragma unroll
@@ -950,11 +1057,22 @@ __global__ __launch_bounds__(NW * 64, 2) void kv8_attend_wide_kernel(Kv8Cache c,
                     weigh(y);
                 }
             }
+            float before[R];
 #pragma unroll
-            for (int y = 0; y < R; ++y)
+            for (int y = 0; y < R; ++y) {
+                before[y] = l[y];
 #pragma unroll
                 for (int x = 0; x < H; ++x)
                     l[y] = fmaf(sum[y][x], f[y][x].back, l[y]);
+            }
+            // (behind the ordinary sum and instead of it: a branch before it costs up to 2% of the kernel)
+            if (__builtin_expect(apart, 0)) {
+#pragma unroll
+                for (int y = 0; y < R; ++y) {
+                    l[y] = before[y];
+                    add_alone(y, f[y]);
+                }
+            }
         };
 
         // Two phases a step, a barrier after each: the matrix products (the previous step's values,
@@ -970,13 +1088,44 @@ __global__ __launch_bounds__(NW * 64, 2) void kv8_attend_wide_kernel(Kv8Cache c,
             none[x] = Half{-1, 0, 0.0f, kTiny};
         const int begin = run.s0 * (2 / H), end = run.s1 * (2 / H);
         auto look_up = [&]() {
+            constexpr int EACH = H * AHEAD / T;  // halves of a thread
             last = first + AHEAD < end ? first + AHEAD : end;
-            __syncthreads();
-            for (int i = tid; i < H * (last - first); i += T) {
-                Half h = find_half(c, b, a, t, first * BK + 32 * i, t.reach_max);
-                find_scales(c, t, h);
-                halves[i] = h;
+            Half found[EACH];
+            bool any_far = false;
+#pragma unroll
+            for (int i = 0; i < EACH; ++i) {
+                found[i] = Half{-1, 0, 0.0f, kTiny};
+                if (tid + i * T < H * (last - first)) {
+                    found[i] = find_half(c, b, a, t, first * BK + 32 * (tid + i * T), t.reach_max);
+                    find_scales(c, t, found[i]);
+                }
+                any_far |= is_far(found[i]);
             }
+            any_far = __any(any_far);
+            if (lane == 0)
+                far[wave] = any_far;
+            __syncthreads();
+            int all_far = 0;
+#pragma unroll
+            for (int i = 0; i < NW; ++i)
+                all_far |= far[i];
+            if (!apart && __builtin_amdgcn_readfirstlane(all_far)) {
+                // from the lowest z of the ordinary range to the lowest of all
+                apart = 1;
+#pragma unroll
+                for (int y = 0; y < R; ++y) {
+                    alone[y][tid] = m[y];
+                    m[y] -= kApart;
+#pragma unroll
+                    for (int i = 0; i < DT; ++i)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            o[y][i][j] *= kApartPower;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < EACH; ++i)
+                halves[tid + i * T] = settled(found[i], apart);
             __syncthreads();
         };
         first = begin;
@@ -1040,6 +1189,7 @@ __global__ __launch_bounds__(NW * 64, 2) void kv8_attend_wide_kernel(Kv8Cache c,
             if (wave_row + y * 32 + col >= t.rows)
                 continue;
             const int64_t row = t.row0 + qrow[y];
+            const float ms = apart ? alone[y][tid] : m[y];
             if (run.slot >= 0) {
                 float *out = partial<BM, D>(a, run.slot) + (wave * R + y) * 32 * D;
 #pragma unroll
@@ -1048,20 +1198,21 @@ __global__ __launch_bounds__(NW * 64, 2) void kv8_attend_wide_kernel(Kv8Cache c,
                         f4{o[y][i / 4][i % 4 * 4], o[y][i / 4][i % 4 * 4 + 1],
                            o[y][i / 4][i % 4 * 4 + 2], o[y][i / 4][i % 4 * 4 + 3]};
                 if (g == 0)
-                    *(f2 *)(partial<BM, D>(a, run.slot) + BM * D +
-                            2 * ((wave * R + y) * 32 + col)) = f2{m[y], all};
+                    *(f4 *)(partial<BM, D>(a, run.slot) + BM * D +
+                            kRowWords * ((wave * R + y) * 32 + col)) = f4{m[y], ms, all, 0.0f};
             } else {
-                const float inv = all > 0.0f ? 1.0f / all : (all == all ? 0.0f : all);
+                const float p = half_power(m[y], ms);
+                const float inv = (all > 0.0f ? 1.0f / all : (all == all ? 0.0f : all)) * p;
                 const int64_t at = row * a.out_stride + (int64_t)qhead[y] * D + g * 4;
 #pragma unroll
                 for (int i = 0; i < DT; ++i)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        store_out(a, at + i * 32 + j * 8, o[y][i][4 * j] * inv,
-                                  o[y][i][4 * j + 1] * inv, o[y][i][4 * j + 2] * inv,
-                                  o[y][i][4 * j + 3] * inv);
+                        store_out(a, at + i * 32 + j * 8, o[y][i][4 * j] * inv * p,
+                                  o[y][i][4 * j + 1] * inv * p, o[y][i][4 * j + 2] * inv * p,
+                                  o[y][i][4 * j + 3] * inv * p);
                 if (a.lse && g == 0)
-                    a.lse[row * a.q_heads + qhead[y]] = lse_of(m[y], all);
+                    a.lse[row * a.q_heads + qhead[y]] = lse_of(ms, all);
             }
         }
     }
@@ -1082,7 +1233,7 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8Cache c, Kv8Batch b, K
         return;
     const int i0 = blockIdx.y * (N * 256) + threadIdx.x;  // the first piece
     int row[N], d[N];
-    f2 ml[N];
+    f4 ml[N];  // m, ms, l
     f4 o[N];
     // the first part lies in the beginning work-group's second slot, the others in first ones
     const float *x = partial<BM, D>(a, 2 * w + 1);
@@ -1096,24 +1247,25 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8Cache c, Kv8Batch b, K
             row[n] = i / (8 * D) * 32 + i % 32;
             d[n] = i % (8 * D) / 64 * 8 + i % 64 / 32 * 4;
         }
-        ml[n] = *(const f2 *)(x + BM * D + 2 * row[n]);
+        ml[n] = *(const f4 *)(x + BM * D + kRowWords * row[n]);
         o[n] = *(const f4 *)(x + 4 * i);
     }
     for (int k = 1; k <= cut.more; ++k) {
         x = partial<BM, D>(a, 2 * (w + k));
-        f2 more[N];
+        f4 more[N];
         f4 v[N];
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            more[n] = *(const f2 *)(x + BM * D + 2 * row[n]);
+            more[n] = *(const f4 *)(x + BM * D + kRowWords * row[n]);
             v[n] = *(const f4 *)(x + 4 * (i0 + n * 256));
         }
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            const float now = fmaxf(ml[n][0], more[n][0]);
-            const float e0 = exp2_fast(ml[n][0] - now), e1 = exp2_fast(more[n][0] - now);
-            ml[n] = f2{now, ml[n][1] * e0 + more[n][1] * e1};
-            o[n] = o[n] * e0 + v[n] * e1;
+            const float now = fmaxf(ml[n][0], more[n][0]), nows = fmaxf(ml[n][1], more[n][1]);
+            o[n] = o[n] * exp2_fast(ml[n][0] - now) + v[n] * exp2_fast(more[n][0] - now);
+            const float l = ml[n][2] * exp2_fast(ml[n][1] - nows) +
+                            more[n][2] * exp2_fast(more[n][1] - nows);
+            ml[n] = f4{now, nows, l, 0.0f};
         }
     }
     Tile t;
@@ -1127,11 +1279,12 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8Cache c, Kv8Batch b, K
         const int query = quotient(r, a.group);
         const int64_t qrow = t.row0 + t.q0 + query;
         const int qhead = (t.head - query) * a.group + r;
-        const float l = ml[n][1], inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
-        store_out(a, qrow * a.out_stride + (int64_t)qhead * D + d[n], o[n][0] * inv, o[n][1] * inv,
-                  o[n][2] * inv, o[n][3] * inv);
+        const float l = ml[n][2], p = half_power(ml[n][0], ml[n][1]);
+        o[n] *= (l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l)) * p;
+        store_out(a, qrow * a.out_stride + (int64_t)qhead * D + d[n], o[n][0] * p, o[n][1] * p,
+                  o[n][2] * p, o[n][3] * p);
         if (a.lse && d[n] == 0)
-            a.lse[qrow * a.q_heads + qhead] = lse_of(ml[n][0], l);
+            a.lse[qrow * a.q_heads + qhead] = lse_of(ml[n][1], l);
     }
 }
 
@@ -1198,7 +1351,7 @@ Kv8Plan kv8_plan(const Kv8Cache &c, const Kv8Batch &b, int q_heads, int64_t max_
         runs = runs < sh.slots ? runs : sh.slots;
         p.joined = 1;
         p.groups = runs;
-        p.ws_bytes = ((int64_t)kCutWords + 2 * runs * sh.rows * (c.dim + 2)) * sizeof(float);
+        p.ws_bytes = ((int64_t)kCutWords + 2 * runs * sh.rows * (c.dim + kRowWords)) * sizeof(float);
     }
     return p;
 }

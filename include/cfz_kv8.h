@@ -150,7 +150,9 @@ typedef struct {
  * query row is first scaled by a power of two, so that a bf16 or fp16 q is held exactly down to
  * 2^-29 of its largest entry), accumulate in fp32, and the weights enter the second
  * product rounded to fp16; the softmax statistics are fp32.  Value scales of 2^-100
- * or less count as 0.  Results do not depend on the run.
+ * or less count as 0; others may lie as far apart as fp32 has them (outside of 2^-32 ..
+ * 2^32 the denominators are summed on their own, which takes longer).  Results do not
+ * depend on the run.
  * workspace: cfz_kv8_attend_workspace_bytes(...) bytes, 256-byte aligned (may be NULL
  * if that is 0), overwritten by the call; calls that may run at the same time need one
  * each.  q, out and lse must not overlap.

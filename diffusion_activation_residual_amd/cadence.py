@@ -13,12 +13,14 @@ every share's K and V is decoded, the shares are written into the layer's 8-bit 
 device's own queries attend over all of them.
 
 Host logic only: every launch is a call of the C ABI through the binding."""
+import ctypes as C
+from contextlib import contextmanager
 from dataclasses import dataclass
 from typing import Optional
 
 import torch
 
-from . import cfz
+from . import cfz, kv8
 
 
 @dataclass
@@ -74,6 +76,25 @@ class SharePlan:
         self.lengths = ints([self.tokens] * batch)
         self.q_offsets = ints([i * queries for i in range(batch + 1)])
 
+    def _check_sizes(self, cache, q, keys):
+        """Raises what the library refuses about these sizes."""
+        for i, k in enumerate(keys):
+            batch = cache._batch(self.table, self.starts[i], self.offsets[i], len(k),
+                                 self.share_tokens[i])
+            row = cache.kv_heads * cache.head_dim
+            cache._fits(kv8._lib.cfz_kv8_append, batch, kv8._REALS[k.dtype], None, None, row, row,
+                        cache._turn(self.rotation, len(k)), None)
+        batch = cache._batch(self.table, self.lengths, self.q_offsets, len(q), self.queries)
+        heads, dtype = q.shape[1], kv8._REALS[q.dtype]
+        row, lists = heads * cache.head_dim, None
+        if self.count is not None:
+            lists = C.byref(kv8.cfz_kv8_blocks(None, self.count, self.q_block))
+            cache._fits(kv8._lib.cfz_kv8_select, batch, dtype, None, row, heads, 0, self.tokens,
+                        self.first, self.last, lists, None, 0, None)
+        scale = cache.head_dim ** -0.5 if self.scale is None else self.scale
+        cache._fits(kv8._lib.cfz_kv8_attend, batch, dtype, None, row, heads, 0, scale, self.tokens,
+                    lists, None, row, None, None, 0, None)
+
     def write(self, cache, index, share, stream=None):
         """Writes share ``index`` into its place of the items' sequences.  Shares are written in
         order: a page that two of them share ends with the later one's first tokens."""
@@ -102,15 +123,14 @@ def enqueue_layer_step(layers, senders, receivers, x, codes, scales, streams, xh
 
     senders / receivers: cfz handles per tensor; x, codes, scales (and xhat, or None): device
     tensors per tensor index.  The tensors of different layers must not share buffers."""
-    _fork(streams)
-    for l, c in enumerate(layers):
-        st = streams[l % len(streams)]
-        cfz.cfz_compress_group([senders[i] for i in c], [x[i] for i in c], [codes[i] for i in c],
-                               [scales[i] for i in c], stream=st)
-        cfz.cfz_decompress_group([receivers[i] for i in c], [codes[i] for i in c],
-                                 [scales[i] for i in c],
-                                 None if xhat is None else [xhat[i] for i in c], stream=st)
-    _join(streams)
+    with _spread(streams):
+        for l, c in enumerate(layers):
+            st = streams[l % len(streams)]
+            cfz.cfz_compress_group([senders[i] for i in c], [x[i] for i in c],
+                                   [codes[i] for i in c], [scales[i] for i in c], stream=st)
+            cfz.cfz_decompress_group([receivers[i] for i in c], [codes[i] for i in c],
+                                     [scales[i] for i in c],
+                                     None if xhat is None else [xhat[i] for i in c], stream=st)
 
 
 def enqueue_layer_attention(plan, layers, caches, q, out, streams):
@@ -119,11 +139,37 @@ def enqueue_layer_attention(plan, layers, caches, q, out, streams):
     their tokens into caches[l] (``kv8.Cache`` of at least ``plan.pages`` pages), and the
     attention of q[l] over all of them into out[l], on streams[l % len(streams)], ordered as in
     ``enqueue_layer_step``.  Works eagerly and under capture.  The layers must not share
-    caches, tensors or receivers."""
+    caches, tensors or receivers.
+
+    A step that does not fit is refused whole, before anything is queued: a decode moves its
+    receivers' bases on, so a step may not be tried twice."""
+    _check_step(plan, layers, caches, q, out, streams)
+    with _spread(streams):
+        for l, shares in enumerate(layers):
+            st = streams[l % len(streams)]
+            got = [s for s in shares if s.receivers is not None]
+            if got:
+                cfz.cfz_decompress_group(*_payload(got), stream=st)
+            for i, s in enumerate(shares):
+                plan.write(caches[l], i, s, stream=st)
+            # (the log-sum-exp is not wanted: its buffer lives as long as the work on st)
+            plan.attend(caches[l], q[l], out=out[l], stream=st)
+
+
+def _payload(shares):
+    return ([r for s in shares for r in s.receivers], [c for s in shares for c in s.codes],
+            [c for s in shares for c in s.scales])
+
+
+def _check_step(plan, layers, caches, q, out, streams):
+    """Everything that a launch of the step would refuse."""
+    if not streams:
+        raise ValueError("at least one stream")
     if not len(layers) == len(caches) == len(q) == len(out):
         raise ValueError(f"{len(layers)} layers, {len(caches)} caches, {len(q)} queries and "
                          f"{len(out)} outputs")
-    for l, shares in enumerate(layers):
+    alike = set()  # the plan's sizes are checked once for layers of the same sizes
+    for l, (shares, cache) in enumerate(zip(layers, caches)):
         if len(shares) != len(plan.share_tokens):
             raise ValueError(f"layer {l}: {len(shares)} shares, the plan has "
                              f"{len(plan.share_tokens)}")
@@ -136,31 +182,51 @@ def enqueue_layer_attention(plan, layers, caches, q, out, streams):
         if q[l].shape[0] != plan.batch * plan.queries:
             raise ValueError(f"layer {l}: {q[l].shape[0]} query rows, the plan has "
                              f"{plan.batch} x {plan.queries}")
-        if caches[l].page_tokens != plan.page_tokens or caches[l].pages < plan.pages:
-            raise ValueError(f"layer {l}: a cache of {caches[l].pages} pages of "
-                             f"{caches[l].page_tokens}, the plan needs {plan.pages} of "
+        if cache.page_tokens != plan.page_tokens or cache.pages < plan.pages:
+            raise ValueError(f"layer {l}: a cache of {cache.pages} pages of "
+                             f"{cache.page_tokens}, the plan needs {plan.pages} of "
                              f"{plan.page_tokens}")
-    _fork(streams)
-    for l, shares in enumerate(layers):
+        if plan.count is not None and cache.k_mean is None:
+            raise ValueError(f"layer {l}: selection needs a cache with k_mean (pooled=True)")
         st = streams[l % len(streams)]
+        if st.device != cache.device:
+            raise ValueError(f"layer {l}: stream on {st.device}, the cache is on {cache.device}")
+        for s in shares:
+            ks, vs = cache._new_rows(s.k, s.v)
+            _whole_rows(s.k, ks, l, "k")
+            _whole_rows(s.v, vs, l, "v")
+        _whole_rows(q[l], cache._queries(q[l]), l, "q")
+        if out[l] is not None:
+            _whole_rows(out[l], cache._outputs(q[l], out[l]), l, "out")
         got = [s for s in shares if s.receivers is not None]
-        cfz.cfz_decompress_group([r for s in got for r in s.receivers],
-                                 [c for s in got for c in s.codes],
-                                 [c for s in got for c in s.scales], stream=st)
-        for i, s in enumerate(shares):
-            plan.write(caches[l], i, s, stream=st)
-        # (the log-sum-exp is not wanted: its buffer lives as long as the work on st)
-        plan.attend(caches[l], q[l], out=out[l], stream=st)
-    _join(streams)
+        if got:
+            cfz.check_decompress_group(*_payload(got))
+        sizes = (cache.kv_heads, cache.head_dim, cache.device, q[l].shape[1], q[l].dtype,
+                 tuple(s.k.dtype for s in shares))
+        if sizes not in alike:
+            plan._check_sizes(cache, q[l], [s.k for s in shares])
+            alike.add(sizes)
 
 
-def _fork(streams):
+def _whole_rows(t, stride, layer, what):
+    """Rows side by side or apart, in 16-byte vectors."""
+    _, heads, dim = t.shape
+    if (stride < heads * dim or stride >= 1 << 31 or stride * t.element_size() % 16 or
+            t.data_ptr() % 16):
+        raise ValueError(f"layer {layer}: rows of {what} {stride} elements apart from "
+                         f"{t.data_ptr():#x} on, expected at least {heads * dim}, in multiples of "
+                         "16 bytes")
+
+
+@contextmanager
+def _spread(streams):
+    """streams[1:] start behind what is queued on streams[0], which goes on behind them."""
     if not streams:
         raise ValueError("at least one stream")
     for s in streams[1:]:
         s.wait_stream(streams[0])
-
-
-def _join(streams):
-    for s in streams[1:]:
-        streams[0].wait_stream(s)
+    try:
+        yield
+    finally:
+        for s in streams[1:]:
+            streams[0].wait_stream(s)

@@ -119,6 +119,8 @@ def _ptr(t):
 
 # handle -> sizes its calls touch (elements, codes bytes, scales bytes), for the size checks
 _sizes = {}
+# handle -> what the states of one grouped call have in common (the role last)
+_codecs = {}
 
 
 def _need(t, nbytes, what):
@@ -147,6 +149,7 @@ _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
 def _record(handle, desc):
     n = max(desc.rows * desc.cols, 0)
     _sizes[handle] = (n, _lib.cfz_codes_bytes(C.byref(desc)), _lib.cfz_scales_bytes(C.byref(desc)))
+    _codecs[handle] = (desc.bits, desc.group, desc.ef_mode, desc.state_dtype, desc.role)
 
 
 def _check_state_buffers(desc, prev, base, err, x0=None):
@@ -247,6 +250,7 @@ def cfz_state_resume(desc: cfz_desc, prev=None, base=None, err=None, steps=0):
 
 def cfz_state_destroy(handle) -> None:
     _sizes.pop(handle, None)
+    _codecs.pop(handle, None)
     _check(_lib.cfz_state_destroy(handle), "cfz_state_destroy")
 
 
@@ -283,6 +287,29 @@ def cfz_compress_group(handles, xs, codes, scales, stream=None) -> None:
     _check(_lib.cfz_compress_group(n, _ptr_array(handles, lambda h: h), _ptr_array(xs, _bf16_ptr),
                                    _ptr_array(codes), _ptr_array(scales), _stream(stream)),
            "cfz_compress_group")
+
+
+def check_decompress_group(handles, codes, scales) -> None:
+    """Raises where ``cfz_decompress_group`` would refuse these arguments; queues nothing.  (Of handles
+    that this module did not make, only their presence and repetition are seen.)"""
+    n = len(handles)
+    if not (len(codes) == len(scales) == n):
+        raise ValueError("all lists must have one entry per state")
+    if len(set(handles)) != n or not all(handles):
+        raise ValueError("receivers: closed, or the same state twice")
+    codec = None
+    for h, c, s in zip(handles, codes, scales):
+        _check_payload(h, codes=c, scales=s)
+        if _ptr(c) % 16 or _ptr(s) % 16:
+            raise ValueError("codes and scales must be 16-byte aligned")
+        mine = _codecs.get(h)
+        if mine is None:
+            continue
+        if mine[-1] != CFZ_RECEIVER:
+            raise ValueError("not a receiver state")
+        if codec is not None and mine != codec:
+            raise ValueError("the receivers of a group must have one codec")
+        codec = mine
 
 
 def cfz_decompress_group(handles, codes, scales, xhats=None, stream=None) -> None:

@@ -185,12 +185,12 @@ cfz_status cfz_kv8_append(const cfz_kv8_cache *cache, const cfz_kv8_batch *batch
     bound_rows(&b);
     if (empty(b))
         return CFZ_OK;
+    CFZ_TRY(check_pages(c, b));
     CFZ_TRY(check_pointers(c, b));
     if (!k || !v)
         return fail(CFZ_ERR_NULL, "k and v are required");
     if (!aligned(k, 16) || !aligned(v, 16))
         return fail(CFZ_ERR_ALIGN, "k and v must be 16-byte aligned");
-    CFZ_TRY(check_pages(c, b));
     return hip_status(cfz::launch_kv8_append(c, b, dtype, k, v, k_stride, v_stride, rot,
                                              (hipStream_t)hip_stream),
                       "append launch");
@@ -250,15 +250,15 @@ cfz_status cfz_kv8_attend(const cfz_kv8_cache *cache, const cfz_kv8_batch *batch
         bound_rows(&b);
     if (empty(b))
         return CFZ_OK;
+    const cfz::Kv8Plan p = cfz::kv8_plan(c, b, q_heads, max_kv, blocks != nullptr,
+                                         blocks ? blocks->q_block : 1, blocks ? blocks->count : 0);
+    CFZ_TRY(check_groups(p.whole));
     CFZ_TRY(check_pointers(c, b));
     if (!q || !out || (blocks && !blocks->blocks))
         return fail(CFZ_ERR_NULL, "q, out and the block lists are required");
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
         (blocks && !aligned(blocks->blocks, 4)))
         return fail(CFZ_ERR_ALIGN, "q and out must be 16-byte, lse and lists 4-byte aligned");
-    const cfz::Kv8Plan p = cfz::kv8_plan(c, b, q_heads, max_kv, blocks != nullptr,
-                                         blocks ? blocks->q_block : 1, blocks ? blocks->count : 0);
-    CFZ_TRY(check_groups(p.whole));
     CFZ_TRY(check_workspace(workspace, ws_bytes, (size_t)p.ws_bytes));
     cfz::Kv8Attend a;
     a.q = q;
@@ -313,14 +313,14 @@ cfz_status cfz_kv8_select(const cfz_kv8_cache *cache, const cfz_kv8_batch *batch
         return fail(CFZ_ERR_SHAPE, "%lld pages per sequence (at most 2^20)", (long long)pages);
     if (empty(b))
         return CFZ_OK;
+    const double lists =
+        (double)((b.max_rows + blocks->q_block - 1) / blocks->q_block) * c.heads * b.batch;
+    CFZ_TRY(check_groups(lists * ((double)(pages + 63) / 64 + 1)));
     CFZ_TRY(check_pointers(c, b));
     if (!q || !blocks->blocks || (c.pages > 0 && !c.km))
         return fail(CFZ_ERR_NULL, "q, the block lists and the cache's k_mean are required");
     if (!aligned(q, 16) || !aligned(blocks->blocks, 4))
         return fail(CFZ_ERR_ALIGN, "q must be 16-byte, the block lists 4-byte aligned");
-    const double lists =
-        (double)((b.max_rows + blocks->q_block - 1) / blocks->q_block) * c.heads * b.batch;
-    CFZ_TRY(check_groups(lists * ((double)(pages + 63) / 64 + 1)));
     CFZ_TRY(check_workspace(workspace, ws_bytes,
                             cfz::kv8_select_workspace_bytes(c, b, max_kv, blocks->q_block)));
     cfz::Kv8Select a;

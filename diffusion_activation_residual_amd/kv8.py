@@ -15,7 +15,7 @@ from typing import Optional
 import torch
 
 from . import cfz
-from .cfz import CFZ_OK, CfzError
+from .cfz import CFZ_ERR_NULL, CFZ_OK, CfzError
 
 CFZ_KV8_INT8, CFZ_KV8_E4M3 = 0, 1
 CFZ_KV8_BF16, CFZ_KV8_F16, CFZ_KV8_F32 = 0, 1, 2
@@ -209,31 +209,53 @@ class Cache:
             return None, 0
         return self._empty(stream, nbytes, torch.uint8), nbytes
 
-    # ---- calls
-
-    def append(self, k, v, page_table, lengths, offsets, max_new, rotation=None, stream=None):
-        """Appends token rows k, v [tokens, kv_heads, head_dim] (bf16, fp16 or fp32; the rows may
-        be strided) behind the ``lengths`` tokens each sequence holds, the keys rotated on the way.
-        The caller adds the new counts to its lengths."""
+    def _new_rows(self, k, v):
+        """Row strides of new keys and values."""
         ks = _rows(k, self.kv_heads, self.head_dim, self.device, "k")
         vs = _rows(v, self.kv_heads, self.head_dim, self.device, "v")
         if k.dtype not in _REALS or v.dtype != k.dtype:
             raise TypeError(f"k and v: {k.dtype} and {v.dtype}, expected one of bf16, fp16, fp32")
         if k.shape[0] != v.shape[0]:
             raise ValueError(f"k has {k.shape[0]} token rows, v {v.shape[0]}")
-        rot = None
-        if rotation is not None:
-            cos, sin, pos = rotation.cos, rotation.sin, rotation.positions
-            if cos.dim() != 2 or cos.shape != sin.shape:
-                raise ValueError("rotation: cos and sin must be [rows, rot_dim / 2]")
-            for t in (cos, sin):
-                if t.dtype != torch.float32 or not t.is_contiguous() or t.device != self.device:
-                    raise ValueError("rotation: cos and sin must be contiguous fp32 tensors on "
-                                     "the cache's device")
-            rot = C.byref(cfz_kv8_rotation(
-                cos.data_ptr(), sin.data_ptr(),
-                None if pos is None else _ints(pos, (k.shape[0],), self.device, "positions"),
-                cos.shape[0], 2 * cos.shape[1], bool(rotation.interleaved)))
+        return ks, vs
+
+    def _turn(self, rotation, tokens):
+        if rotation is None:
+            return None
+        cos, sin, pos = rotation.cos, rotation.sin, rotation.positions
+        if cos.dim() != 2 or cos.shape != sin.shape:
+            raise ValueError("rotation: cos and sin must be [rows, rot_dim / 2]")
+        for t in (cos, sin):
+            if t.dtype != torch.float32 or not t.is_contiguous() or t.device != self.device:
+                raise ValueError("rotation: cos and sin must be contiguous fp32 tensors on "
+                                 "the cache's device")
+        return C.byref(cfz_kv8_rotation(
+            cos.data_ptr(), sin.data_ptr(),
+            None if pos is None else _ints(pos, (tokens,), self.device, "positions"),
+            cos.shape[0], 2 * cos.shape[1], bool(rotation.interleaved)))
+
+    def _outputs(self, q, out):
+        """Row stride of given outputs."""
+        stride = _rows(out, q.shape[1], self.head_dim, self.device, "out")
+        if out.dtype != q.dtype or out.shape != q.shape:
+            raise ValueError("out: must have q's shape and dtype")
+        return stride
+
+    def _fits(self, call, batch, *args):
+        """Raises what the library refuses about a call whose tensors (of token rows, queries,
+        lists) are left out of ``args``: they are the last thing that it asks for before a workspace."""
+        status = call(self._ref, C.byref(batch), *args)
+        if status != CFZ_ERR_NULL:
+            raise CfzError(status, call.__name__)
+
+    # ---- calls
+
+    def append(self, k, v, page_table, lengths, offsets, max_new, rotation=None, stream=None):
+        """Appends token rows k, v [tokens, kv_heads, head_dim] (bf16, fp16 or fp32; the rows may
+        be strided) behind the ``lengths`` tokens each sequence holds, the keys rotated on the way.
+        The caller adds the new counts to its lengths."""
+        ks, vs = self._new_rows(k, v)
+        rot = self._turn(rotation, k.shape[0])
         batch = self._batch(page_table, lengths, offsets, k.shape[0], max_new)
         self._call(_lib.cfz_kv8_append, stream, self._ref, C.byref(batch), _REALS[k.dtype],
                    k.data_ptr(), v.data_ptr(), ks, vs, rot)
@@ -294,9 +316,7 @@ class Cache:
         if out is None:
             out = self._empty(stream, (tokens, heads, self.head_dim), q.dtype)
         else:
-            ostride = _rows(out, heads, self.head_dim, self.device, "out")
-            if out.dtype != q.dtype or out.shape != q.shape:
-                raise ValueError("out: must have q's shape and dtype")
+            ostride = self._outputs(q, out)
         if lse is None:
             lse = self._empty(stream, (tokens, heads), torch.float32)
         elif (lse.shape != (tokens, heads) or lse.dtype != torch.float32 or

@@ -55,8 +55,8 @@ class SharePlan:
                              "at least one of each")
         if page_tokens not in (32, 64, 128):
             raise ValueError(f"page_tokens = {page_tokens}: 32, 64 or 128")
-        if count is not None and (count < 1 or q_block < 1 or first < 0 or last < 0 or
-                                  first + last > count):
+        if count is not None and (not 1 <= count <= 4096 or not 1 <= q_block < 1 << 31 or
+                                  first < 0 or last < 0 or first + last > count):
             raise ValueError(f"count = {count}, q_block = {q_block}, first = {first}, last = {last}")
         self.batch, self.share_tokens, self.queries = batch, share_tokens, queries
         self.tokens = sum(share_tokens)

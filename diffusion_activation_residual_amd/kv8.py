@@ -78,6 +78,13 @@ class Rotation:
     positions: Optional[torch.Tensor] = None
 
 
+def _fit(bits, **numbers):
+    """Refuses numbers that a field of so many bits would hold cut (ctypes does so silently)."""
+    for what, x in numbers.items():
+        if not -(1 << bits - 1) <= x < 1 << bits - 1:
+            raise ValueError(f"{what} = {x}: does not fit {bits} bits")
+
+
 def _ints(t, shape, device, what):
     if t.dtype != torch.int32:
         raise TypeError(f"{what}: {t.dtype} tensor, expected int32")
@@ -169,6 +176,9 @@ class Cache:
         if page_table.dim() != 2:
             raise ValueError("page_table: expected [batch, width]")
         batch, width = page_table.shape
+        if not (batch < 1 << 31 and width < 1 << 31 and -(1 << 63) <= max_rows < 1 << 63):
+            _fit(32, batch=batch, table_width=width)
+            _fit(64, max_rows=max_rows)
         return cfz_kv8_batch(batch, width, _ints(page_table, None, self.device, "page_table"),
                              _ints(offsets, (batch + 1,), self.device, "offsets"),
                              _ints(lengths, (batch,), self.device, "lengths"), tokens, max_rows)
@@ -289,6 +299,7 @@ class Cache:
         return _rows(q, q.shape[1], self.head_dim, self.device, "q")
 
     def _lists(self, blocks, batch, max_q, q_block, count=None):
+        _fit(32, q_block=q_block)
         shape = (batch.batch, -(-max_q // q_block), self.kv_heads,
                  count if count is not None else blocks.shape[-1])
         return cfz_kv8_blocks(_ints(blocks, shape, self.device, "blocks"), shape[-1], q_block)
@@ -302,6 +313,7 @@ class Cache:
         not given are allocated (rows of no sequence are then left unset)."""
         stride = self._queries(q)
         tokens, heads = q.shape[:2]
+        _fit(64, max_kv=max_kv)
         batch = self._batch(page_table, lengths, offsets, tokens, max_q)
         lists = None
         if blocks is not None:
@@ -340,6 +352,8 @@ class Cache:
             raise ValueError("select needs a cache with k_mean (pooled=True)")
         if q_block < 1 or count < 1:
             raise ValueError(f"q_block = {q_block}, count = {count}: at least 1")
+        _fit(32, q_block=q_block, count=count, first=first, last=last)
+        _fit(64, max_kv=max_kv)
         batch = self._batch(page_table, lengths, offsets, q.shape[0], max_q)
         if blocks is None:
             blocks = self._empty(stream, (batch.batch, -(-max_q // q_block), self.kv_heads, count),

@@ -192,6 +192,15 @@ class Cache:
         with torch.cuda.stream(stream):
             return torch.empty(shape, dtype=dtype, device=self.device)
 
+    def _fill(self, t, value, stream):
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, self.device)
+        if stream is None:
+            t.fill_(value)
+        else:
+            with torch.cuda.stream(stream):
+                t.fill_(value)
+
     def _call(self, call, stream, *args):
         index = self.device.index
         if stream is None:  # (the public current_stream() costs as much as the rest of a call)
@@ -365,4 +374,6 @@ class Cache:
         self._call(_lib.cfz_kv8_select, stream, self._ref, C.byref(batch), _REALS[q.dtype],
                    q.data_ptr(), stride, q.shape[1], bool(causal), max_kv, first, last,
                    C.byref(lists), None if workspace is None else workspace.data_ptr(), have)
+        if q.shape[0] == 0:  # (the library checks such a call and leaves the lists alone)
+            self._fill(blocks, -1, stream)
         return blocks

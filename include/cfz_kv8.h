@@ -69,7 +69,7 @@ typedef struct {
  *   max_rows: an upper bound of the rows of one sequence, known on the host; rows
  *            past it are left out.
  * 0 <= batch <= 65535, 1 <= table_width, table_width * page_tokens < 2^31,
- * 0 <= tokens < 2^31 (0 is a no-op).  The integer arrays need 4-byte alignment only.
+ * 0 <= tokens < 2^31 (0 is a no-op: nothing is written, cfz_kv8_select's lists neither).  The integer arrays need 4-byte alignment only.
  * A call that would need 2^23 or more work-groups (append: about one for the keys and
  * one for the values of each page and head) is refused. */
 typedef struct {

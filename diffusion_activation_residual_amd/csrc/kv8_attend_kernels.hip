@@ -50,7 +50,10 @@ constexpr float kNear = 32.0f;    // ordinary value scales lie within 2^-kNear .
 constexpr float kApart = -kNear - kTiny;
 constexpr float kApartPower = 0x1p68f;  // 2^kApart; sums of 2^30 weights times codes (2^55) stay finite
 constexpr int kBlock = 64;  // keys per step
-constexpr int kMaxItems = 1023;  // tiles per head whose steps a work-group counts
+// Tiles per head whose steps a work-group counts.  A call with more is not cut into runs, and a long
+// sequence among short ones is one work-group's: one single token over 131072 tokens beside others over
+// 256, 8 heads of 128, 284 us and 16 for the join with 1000 sequences, 848 us with 1100.
+constexpr int kMaxItems = 1023;
 constexpr int kPrefixWords = kMaxItems + 1;
 constexpr int kRowWords = 4;     // of a part, for each row: m, ms, l
 constexpr int kCutWords = 4096;  // of the workspace: a Cut for each of at most 1024 work-groups
@@ -438,7 +441,7 @@ __device__ inline float *partial(const Kv8Attend &a, int64_t slot)
 // sums at the end.  The pages and scales of many steps are looked up together, and the next step's
 // codes are under way while this one's weights are formed (each looked up in its own step, 147 us
 // instead of 80).  Bound by the codes' bytes: 16 sequences of up to 16411 tokens, 8 KV heads of
-// 128, 32 query heads, in 80 us, 5.1 TB/s, and 6 us for the join.
+// 128, 32 query heads, in 83 us, 4.9 TB/s, and 6 us for the join.
 template <int FMT, int D>
 __global__ __launch_bounds__(256, 2) void kv8_attend_narrow_kernel(Kv8Cache c, Kv8Batch b,
                                                                    Kv8Attend a, Kv8Plan p)
@@ -701,9 +704,10 @@ __global__ __launch_bounds__(256, 2) void kv8_attend_narrow_kernel(Kv8Cache c, K
 // read once per work-group, ahead of their use, and converted to fp16 on the way into LDS (each
 // code once instead of once per wave).  At NW = 8 two waves share a SIMD and run a phase apart:
 // one multiplies while the other forms weights, since a step's weights (an fp32 product, an
-// exponential and half a conversion per score) take about as long as its products.  Measured with the
-// join: 1024 queries over 4096 keys, 24 heads of 128, 92 us, 560 TFLOP/s; 4388 queries over 17552
-// keys, 30 heads of 64, 740 to 760 us, 790 TFLOP/s; products alone reach 1900 in this instruction.  With both
+// exponential and half a conversion per score) take about as long as its products.  A call, the join
+// included: 1024 queries over 4096 keys, 24 heads of 128, 93 us, 555 TFLOP/s; 4388 queries over 17552
+// keys, 30 heads of 64, 740 to 760 us, 780 to 800 TFLOP/s.  (With the denominators on their own the
+// kernels take 92 us instead of 81, and 1174 instead of 759.)  With both
 // kinds of work in every wave, one step's products between the other's weights, the registers
 // spilled; with products and weights one after the other it was 1141 us.
 //

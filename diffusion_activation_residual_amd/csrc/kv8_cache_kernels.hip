@@ -219,11 +219,14 @@ __device__ inline bool find_place(const Kv8Cache &c, const Kv8Batch &b, int span
 // loses ties (49 (1 / 49) < 1), with the remainder put right it is the rounded quotient.  What is not
 // finite, and scales far from 1, take a slower way.  fp32 with a test for quotients near a border,
 // and fp64 for those alone, was slower (130 against 97 us on 4 x 4388 tokens x 30 heads of 64, bf16):
-// values of 8 bits lie near one time and again.  The rotated keys' fp64 values leave 4 waves a SIMD,
-// which bounds it: 4 x 4388 tokens x 30 heads of 64 from bf16 in 72 us, 2.8 TB/s, against 48 us, 4.2
-// TB/s, without rotation (int8, the same buffers again and again; other buffers each time, e4m3, 97
-// us); from fp32 5.1 TB/s.  Few tokens wait for dependent reads (offset,
-// length, page, codes): 32 single tokens x 8 heads of 128 in 8 us.
+// values of 8 bits lie near one time and again.  The rotated keys' fp64 values bound it: 256 threads
+// hold a page of one head, which leaves 4 waves a SIMD (2 at pages of 128 tokens and head_dim 128).
+// 4 x 4388 tokens from bf16 to int8, three sets of buffers in turn, rotated and not: 30 heads of 64,
+// pages of 128, 85 and 55 us, 2.4 and 3.7 TB/s; 24 heads of 128 in pages of 64, 126 us rotated; in pages
+// of 128, 187 and 101 us.  From fp32 (24 x 128, pages of 64) 142 and 110 us, 3.8 and 4.9 TB/s.
+// Few tokens wait for dependent reads (offset, length, page, codes): 32 single tokens x 8 heads of 128 in
+// 8 us.  A token that raises its page's scale has the page's older codes coded again, a byte at a time:
+// then 14 (int8) and 16 us (e4m3) where every page's scale grows.
 //
 // Keys: units of 8 dimensions (two groups of 4 that hold whole rotation pairs).
 constexpr int kStay = 0, kPairs = 1, kHalves = 2;  // how keys turn
@@ -523,7 +526,7 @@ __global__ __launch_bounds__(kThreads) void kv8_append_kernel(Kv8Cache c, Kv8Bat
 
 // Reads one page of one head back: keys straight, values through LDS (their codes are dimension-major),
 // rows written in vectors of 4 values.  Bound by the bytes written: 4 x 4388 tokens x 30 heads of 64
-// to fp32 in 58 us, 5.8 TB/s.
+// to fp32 in 64 us, 5.3 TB/s.
 template <class T, int D, int P>
 __global__ __launch_bounds__(kThreads) void kv8_gather_kernel(Kv8Cache c, Kv8Batch b, T *k, T *v,
                                                               int span)
@@ -609,7 +612,7 @@ __device__ inline uint64_t order_key(double s)
 // queries are summed in fp64 and the products are too: 64 bits where two pages' scores may differ in
 // the last bit of fp32.  A query row is read by D / 8 lanes (16 bytes each) and a page's mean by 8
 // lanes, so that loads are wide and the sums across lanes short.  Bound by latency (a few dozen KB
-// per work-group): 35 blocks of 128 queries x 138 pages x 30 heads of 64 in 18.5 us.
+// per work-group): 35 blocks of 128 queries x 138 pages x 30 heads of 64 in 19.7 us.
 constexpr int kScorePages = 64;
 
 template <int D>
@@ -715,7 +718,7 @@ __global__ __launch_bounds__(kThreads) void kv8_score_kernel(Kv8Cache c, Kv8Batc
 // The `count` largest keys of one list: the threshold is found 8 bits at a time by counting
 // (the same work whatever the keys), then the pages above it and, in index order, as many at it as
 // are left are written in ascending order.  Launch, dependent reads and the passes' barriers: 10.8 us
-// for 1050 lists of 138 pages, 10 us for 128 of up to 512; copies of the keys in LDS, and one wave a
+// for 1050 lists of 138 pages, 9.9 us for 128 of up to 512; copies of the keys in LDS, and one wave a
 // list counting by ballots, took 10.3 and 9.0 to 13.9.
 __global__ __launch_bounds__(kThreads) void kv8_pick_kernel(Kv8Cache c, Kv8Batch b, Kv8Select a,
                                                             int units, int stride)
@@ -816,7 +819,7 @@ __global__ __launch_bounds__(kThreads) void kv8_pick_kernel(Kv8Cache c, Kv8Batch
         out[i] = -1;
 }
 
-// Work-groups of a page-wise launch over `span` pages per sequence, 0 if there is nothing to do.
+// Work-groups of a page-wise launch over `span` pages per sequence.
 int64_t page_groups(const Kv8Cache &c, const Kv8Batch &b, int &span)
 {
     // a run of max_rows tokens touches one page more than it fills when it starts inside a page

@@ -121,7 +121,11 @@ class Cache:
     pages, ``lengths`` [batch] int32, ``offsets`` [batch + 1] int32 with the token rows of each
     sequence, and an upper bound of one sequence's rows known on the host.  Work is queued on
     ``stream`` (default: the current one of the cache's device); with another stream than the
-    current one the caller orders the tensors' other uses, as for every call of the library."""
+    current one the caller orders the tensors' other uses, as for every call of the library.
+    Nothing is recorded for autograd: results carry no gradient, whatever the inputs require.
+
+    int8 is the finer of the two where a head's channels are of one size.  Channels many times
+    larger than the others leave the others only a few of its steps: e4m3 is meant for such tensors."""
 
     def __init__(self, pages, kv_heads, head_dim, page_tokens=64, fmt="int8", pooled=True,
                  device="cuda"):

@@ -119,7 +119,7 @@ cfz_status cfz_kv8_append(const cfz_kv8_cache *cache, const cfz_kv8_batch *batch
                           int64_t v_stride, const cfz_kv8_rotation *rotation, void *hip_stream);
 
 /* Reads tokens back: token row offsets[b] + i gets token lengths[b] + i of sequence b
- * as scale times code, rounded to `dtype`; k, v: dense rows [tokens][kv_heads][head_dim],
+ * as scale times code, rounded to fp32 and then to `dtype`; k, v: dense rows [tokens][kv_heads][head_dim],
  * either may be NULL.  Tokens past the table's end read as zeros.
  * Errors: as cfz_kv8_append. */
 cfz_status cfz_kv8_gather(const cfz_kv8_cache *cache, const cfz_kv8_batch *batch,

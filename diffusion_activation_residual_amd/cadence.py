@@ -142,7 +142,7 @@ def enqueue_layer_attention(plan, layers, caches, q, out, streams):
     caches, tensors or receivers.
 
     A step that does not fit is refused whole, before anything is queued: a decode moves its
-    receivers' bases on, so a step may not be tried twice."""
+    receivers' bases on, so that a step cannot be tried again after half of it."""
     _check_step(plan, layers, caches, q, out, streams)
     with _spread(streams):
         for l, shares in enumerate(layers):

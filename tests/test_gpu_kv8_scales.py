@@ -103,7 +103,7 @@ PATTERNS = {
 }
 
 
-@pytest.mark.parametrize("rows", [1, 40, 100, 300])
+@pytest.mark.parametrize("rows", [1, 40, 100, 200, 300])
 @pytest.mark.parametrize("pattern", PATTERNS)
 def test_attend_value_scales_of_any_size(pattern, rows):
     x = sized(64, 32, "int8", PATTERNS[pattern], seed=40)
@@ -159,3 +159,31 @@ def test_attend_many_keys_of_zero_values(rows):
     want = np.log(n) + np.where(np.arange(rows) < rows // 2, 0.0, 8.0)
     assert not out.any()
     assert np.abs(to64(lse)[:, 0] - want).max() <= 2.0 ** -7 + 2.0 ** -13
+
+
+@pytest.mark.parametrize("rows", [1, 100, 300])
+def test_scales_that_change_between_replays_of_a_graph(rows):
+    """Which way the denominators are summed is seen on the device, replay by replay."""
+    x = sized(64, 32, "int8", [1.0] * 40, seed=43)
+    q, table, held = x.rows(rows), ints(x.table), ints(x.held)
+    args = (q, table, held, cumulative([rows]), rows, 40 * 32)
+    x.cache.attend(*args)
+    torch.cuda.synchronize()
+    ordinary = x.cache.v_scale.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = x.cache.attend(*args)
+    for far in (None, 1e20, None, 0.0, 1e-20):
+        x.cache.v_scale.copy_(ordinary)
+        if far is not None:
+            x.cache.v_scale[table[0, 7::9].long()] = far
+        graph.replay()
+        want, wl = x.cache.attend(*args)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, wl) and torch.isfinite(lse).all()
+        # the scores do not depend on the values: two results, each off by 2^-21 2^8 (the exponent with
+        # the value scale's logarithm in it) and by the roundings of sum and logarithm
+        if far is None:
+            base_lse = wl.clone()
+        else:
+            assert (wl - base_lse).abs().max() <= 2.0 ** -13 * 2 + 2.0 ** -20 * base_lse.abs().max()

@@ -1,9 +1,10 @@
 """libcfz for AMD Instinct MI355X: the CompactFusion residual-compression codec
 (fused residual + error feedback + group int4/int2 quantization, decode + base
 update), the rank-r subspace-iteration compressor, and the 8-bit paged K/V cache
-that receives what was exchanged, with the attention over it, as hand-written HIP
-for gfx950 behind C ABIs (``include/cfz.h``, ``include/cfz_kv8.h``).  ``cfz`` and
-``kv8`` are the ctypes bindings.
+that receives what was exchanged, with the attention over it, and what lies between
+the residual stream and that cache (norms, rotations, adapters), as hand-written HIP
+for gfx950 behind C ABIs (``include/cfz.h``, ``include/cfz_kv8.h``,
+``include/cfz_block.h``).  ``cfz``, ``kv8`` and ``block`` are the ctypes bindings.
 
 The binding is imported on first use, not with the package, so that
 ``diffusion_activation_residual_amd.build`` can compile ``libcfz.so`` in a tree
@@ -20,7 +21,7 @@ _BINDING_NAMES = frozenset((
 
 
 def __getattr__(name):
-    if name in ("cfz", "kv8"):
+    if name in ("block", "cfz", "kv8"):
         return importlib.import_module("." + name, __name__)
     if name in _BINDING_NAMES:
         return getattr(importlib.import_module(".cfz", __name__), name)

@@ -1,0 +1,288 @@
+// block_api.hip -- the C ABI of cfz_block.h: argument validation and dispatch.  Nothing touches
+// the device until every argument has been checked.
+#include "api_checks.h"
+#include "block_internal.h"
+
+#include <limits.h>
+#include <math.h>
+#include <string.h>
+
+using cfz::aligned;
+using cfz::fail;
+using cfz::hip_status;
+
+namespace {
+
+bool is_dtype(int d) { return d == CFZ_KV8_BF16 || d == CFZ_KV8_F16 || d == CFZ_KV8_F32; }
+int width_of(int dtype) { return dtype == CFZ_KV8_F32 ? 4 : 2; }
+
+cfz_status check_stride(int64_t stride, int64_t row, int dtype, const char *what)
+{
+    if (stride < row || stride > INT_MAX || stride * width_of(dtype) % 16 != 0)
+        return fail(CFZ_ERR_SHAPE, "%s = %lld (at least %lld, a multiple of 16 bytes)", what,
+                    (long long)stride, (long long)row);
+    return CFZ_OK;
+}
+
+cfz_status check_rows(int64_t tokens, int32_t batch, const int32_t *offsets, cfz::BlockRows *rows)
+{
+    if (tokens < 0 || tokens > INT_MAX)
+        return fail(CFZ_ERR_SHAPE, "tokens = %lld", (long long)tokens);
+    if (batch < 1 || batch > 65535)
+        return fail(CFZ_ERR_SHAPE, "batch = %d", batch);
+    if (!offsets && tokens % batch != 0)
+        return fail(CFZ_ERR_SHAPE, "%lld tokens do not divide into %d items", (long long)tokens,
+                    batch);
+    if (!aligned(offsets, 4))
+        return fail(CFZ_ERR_ALIGN, "offsets must be 4-byte aligned");
+    *rows = cfz::BlockRows{offsets, tokens, tokens / batch, batch};
+    return CFZ_OK;
+}
+
+// A vector's type: fp32 or the call's own.
+cfz_status check_vec(const void *p, int dtype, int call, const char *what)
+{
+    if (!p)
+        return CFZ_OK;
+    if (dtype != CFZ_KV8_F32 && dtype != call)
+        return fail(CFZ_ERR_UNSUPPORTED, "%s: dtype = %d with rows of %d", what, dtype, call);
+    if (!aligned(p, 16))
+        return fail(CFZ_ERR_ALIGN, "%s must be 16-byte aligned", what);
+    return CFZ_OK;
+}
+
+cfz_status check_items(const cfz_item_rows &v, int cols, int call, const char *what,
+                       cfz::BlockVec *out)
+{
+    *out = cfz::BlockVec{v.data, v.stride, v.dtype == CFZ_KV8_F32};
+    if (!v.data)
+        return CFZ_OK;
+    CFZ_TRY(check_vec(v.data, v.dtype, call, what));
+    return v.stride == 0 ? CFZ_OK : check_stride(v.stride, cols, v.dtype, what);
+}
+
+cfz_status check_norm(const cfz_norm &n, int call, const char *what, cfz::BlockNormOf *out)
+{
+    if (n.kind < CFZ_NORM_NONE || n.kind > CFZ_NORM_LAYER)
+        return fail(CFZ_ERR_UNSUPPORTED, "%s: kind = %d", what, n.kind);
+    const bool none = n.kind == CFZ_NORM_NONE;
+    if (!none && (!(n.eps >= 0.0f) || !isfinite(n.eps)))
+        return fail(CFZ_ERR_SHAPE, "%s: eps = %g must be finite and not negative", what,
+                    (double)n.eps);
+    if (n.bias && n.kind != CFZ_NORM_LAYER)
+        return fail(CFZ_ERR_UNSUPPORTED, "%s: a bias goes with the LAYER norm only", what);
+    if (n.weight && none)
+        return fail(CFZ_ERR_UNSUPPORTED, "%s: a weight without a norm", what);
+    CFZ_TRY(check_vec(n.weight, n.dtype, call, what));
+    CFZ_TRY(check_vec(n.bias, n.dtype, call, what));
+    const int f32 = n.dtype == CFZ_KV8_F32;
+    *out = cfz::BlockNormOf{n.kind, n.eps, {n.weight, 0, f32}, {n.bias, 0, f32}};
+    return CFZ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+cfz_status cfz_residual_norm(const cfz_residual *r, void *hip_stream)
+{
+    if (!r)
+        return fail(CFZ_ERR_NULL, "args is required");
+    if (!is_dtype(r->x_dtype) || !is_dtype(r->y_dtype) ||
+        (r->x_dtype != r->y_dtype && r->x_dtype != CFZ_KV8_F32))
+        return fail(CFZ_ERR_UNSUPPORTED, "x_dtype = %d with y_dtype = %d", r->x_dtype, r->y_dtype);
+    if (r->cols < 8 || r->cols > 16384 || r->cols % 8 != 0)
+        return fail(CFZ_ERR_SHAPE, "cols = %d (a multiple of 8, 8 .. 16384)", r->cols);
+    cfz::ResidualArgs a;
+    CFZ_TRY(check_rows(r->tokens, r->batch, r->offsets, &a.rows));
+    if (!isfinite(r->gate_scale))
+        return fail(CFZ_ERR_SHAPE, "gate_scale = %g", (double)r->gate_scale);
+    const int call = r->y_dtype;
+    CFZ_TRY(check_items(r->gate, r->cols, call, "gate", &a.gate));
+    CFZ_TRY(check_items(r->scale, r->cols, call, "scale", &a.scale));
+    CFZ_TRY(check_items(r->shift, r->cols, call, "shift", &a.shift));
+    CFZ_TRY(check_norm(r->after, call, "after", &a.after));
+    CFZ_TRY(check_norm(r->before, call, "before", &a.before));
+    CFZ_TRY(check_stride(r->x_stride, r->cols, r->x_dtype, "x_stride"));
+    if (r->y)
+        CFZ_TRY(check_stride(r->y_stride, r->cols, call, "y_stride"));
+    else if (r->gate.data || r->after.kind != CFZ_NORM_NONE)
+        return fail(CFZ_ERR_NULL, "a gate and a norm of y need y");
+    if (r->r)
+        CFZ_TRY(check_stride(r->r_stride, r->cols, r->x_dtype, "r_stride"));
+    if (r->h)
+        CFZ_TRY(check_stride(r->h_stride, r->cols, call, "h_stride"));
+    if (r->tokens == 0)
+        return CFZ_OK;
+    if (!r->x || (!r->r && !r->h))
+        return fail(CFZ_ERR_NULL, "x and one of r and h are required");
+    if (!aligned(r->x, 16) || !aligned(r->y, 16) || !aligned(r->r, 16) || !aligned(r->h, 16))
+        return fail(CFZ_ERR_ALIGN, "x, y, r and h must be 16-byte aligned");
+    if ((r->r == r->x && r->r_stride != r->x_stride) ||
+        (r->y && r->h == r->y && r->h_stride != r->y_stride))
+        return fail(CFZ_ERR_SHAPE, "in place, the strides must be the same");
+    if (r->cols > 4096 && r->tokens >= cfz::kBlockMaxGroups)
+        return fail(CFZ_ERR_SHAPE, "the call needs %lld work-groups (limit 2^23)",
+                    (long long)r->tokens);
+    a.cols = r->cols;
+    a.x = r->x, a.y = r->y, a.r = r->r, a.h = r->h;
+    a.xs = r->x_stride, a.ys = r->y_stride, a.rs = r->r_stride, a.hs = r->h_stride;
+    a.gate_scale = r->gate_scale;
+    return hip_status(cfz::launch_residual_norm(a, r->x_dtype, call, (hipStream_t)hip_stream),
+                      "residual norm launch");
+}
+
+cfz_status cfz_rotation_table(const cfz_rotation_angles *g, int64_t rows, const int32_t *positions,
+                              float *cos, float *sin, void *hip_stream)
+{
+    if (!g)
+        return fail(CFZ_ERR_NULL, "angles is required");
+    if (g->rot_dim < 8 || g->rot_dim > 256 || g->rot_dim % 8 != 0)
+        return fail(CFZ_ERR_SHAPE, "rot_dim = %d (a multiple of 8, 8 .. 256)", g->rot_dim);
+    if (g->axes < 1 || g->axes > 4)
+        return fail(CFZ_ERR_SHAPE, "axes = %d (1 .. 4)", g->axes);
+    if (g->scaling < CFZ_ROTATION_PLAIN || g->scaling > CFZ_ROTATION_PARTS)
+        return fail(CFZ_ERR_UNSUPPORTED, "scaling = %d", g->scaling);
+    const bool base = g->scaling == CFZ_ROTATION_BASE, parts = g->scaling == CFZ_ROTATION_PARTS;
+    int sum = 0;
+    for (int j = 0; j < g->axes; ++j) {
+        const int d = g->axis_dim[j];
+        if (d < 2 || d % 2 != 0 || d > 256 || (base && d == 2))
+            return fail(CFZ_ERR_SHAPE, "axis_dim[%d] = %d", j, d);
+        sum += d;
+    }
+    if (sum != g->rot_dim)
+        return fail(CFZ_ERR_SHAPE, "the axes have %d dimensions, rot_dim is %d", sum, g->rot_dim);
+    if (!(g->base > 1.0) || !isfinite(g->base) || !(g->factor > 0.0) || !isfinite(g->factor) ||
+        !(g->amplitude > 0.0) || !isfinite(g->amplitude))
+        return fail(CFZ_ERR_SHAPE, "base = %g, factor = %g, amplitude = %g", g->base, g->factor,
+                    g->amplitude);
+    if (parts && (!(g->trained > 0.0) || !isfinite(g->trained) || !(g->slow >= 0.0) ||
+                  !(g->fast > g->slow) || !isfinite(g->fast)))
+        return fail(CFZ_ERR_SHAPE, "trained = %g, slow = %g, fast = %g", g->trained, g->slow,
+                    g->fast);
+    if (rows < 0 || rows > INT_MAX)
+        return fail(CFZ_ERR_SHAPE, "rows = %lld", (long long)rows);
+    const int pairs = g->rot_dim / 2;
+    if (rows * pairs / 256 >= cfz::kBlockMaxGroups)
+        return fail(CFZ_ERR_SHAPE, "a table of %lld angles (limit 2^31)", (long long)(rows * pairs));
+    if (!positions && g->axes > 1)
+        return fail(CFZ_ERR_NULL, "more than one axis needs positions");
+    if (!aligned(positions, 4))
+        return fail(CFZ_ERR_ALIGN, "positions must be 4-byte aligned");
+    if (rows == 0)
+        return CFZ_OK;
+    if (!cos || !sin)
+        return fail(CFZ_ERR_NULL, "cos and sin are required");
+    if (!aligned(cos, 16) || !aligned(sin, 16))
+        return fail(CFZ_ERR_ALIGN, "cos and sin must be 16-byte aligned");
+    cfz::TableArgs a;
+    memset(&a, 0, sizeof a);
+    int at = 0;
+    for (int j = 0; j < g->axes; ++j) {
+        const double d = g->axis_dim[j];
+        const double b = base ? g->base * pow(g->factor, d / (d - 2.0)) : g->base;
+        if (!(b > 0.0) || !isfinite(b))
+            return fail(CFZ_ERR_SHAPE, "base = %g, stretched by factor = %g", g->base, g->factor);
+        for (int i = 0; i < g->axis_dim[j] / 2; ++i, ++at) {
+            double speed = pow(b, -2.0 * i / d);
+            if (g->scaling == CFZ_ROTATION_LINEAR)
+                speed /= g->factor;
+            if (parts) {
+                const double n = g->trained * speed / 6.283185307179586476925;
+                double k = (n - g->slow) / (g->fast - g->slow);
+                k = k < 0.0 ? 0.0 : (k > 1.0 ? 1.0 : k);
+                speed *= k + (1.0 - k) / g->factor;
+            }
+            a.speed[at] = speed;
+            a.axis[at] = (uint8_t)j;
+        }
+    }
+    a.pairs = pairs;
+    a.axes = g->axes;
+    a.rows = rows;
+    a.positions = positions;
+    a.amplitude = g->amplitude;
+    a.cos = cos;
+    a.sin = sin;
+    return hip_status(cfz::launch_rotation_table(a, (hipStream_t)hip_stream), "table launch");
+}
+
+cfz_status cfz_rotate(int32_t count, const cfz_rotate_rows *tensors, cfz_kv8_dtype dtype,
+                      int32_t head_dim, int64_t tokens, int32_t batch, const int32_t *offsets,
+                      const int32_t *starts, const cfz_kv8_rotation *rotation, int32_t normed,
+                      float eps, void *hip_stream)
+{
+    if (count < 1 || count > 4)
+        return fail(CFZ_ERR_SHAPE, "count = %d tensors (1 .. 4)", count);
+    if (!tensors)
+        return fail(CFZ_ERR_NULL, "tensors is required");
+    if (!is_dtype(dtype))
+        return fail(CFZ_ERR_UNSUPPORTED, "dtype = %d", dtype);
+    if (head_dim != 32 && head_dim != 64 && head_dim != 128 && head_dim != 256)
+        return fail(CFZ_ERR_UNSUPPORTED, "head_dim = %d (supported: 32, 64, 128, 256)", head_dim);
+    cfz::RotateArgs a;
+    memset(&a, 0, sizeof a);
+    CFZ_TRY(check_rows(tokens, batch, offsets, &a.rows));
+    if (!offsets && batch != 1)
+        return fail(CFZ_ERR_NULL, "%d sequences need offsets", batch);
+    if (!aligned(starts, 4))
+        return fail(CFZ_ERR_ALIGN, "starts must be 4-byte aligned");
+    if (!rotation && !normed)
+        return fail(CFZ_ERR_NULL, "neither a rotation nor a norm");
+    if (normed && (!(eps >= 0.0f) || !isfinite(eps)))
+        return fail(CFZ_ERR_SHAPE, "eps = %g must be finite and not negative", (double)eps);
+    if (rotation) {
+        if (rotation->rot_dim < 8 || rotation->rot_dim > head_dim || rotation->rot_dim % 8 != 0)
+            return fail(CFZ_ERR_SHAPE, "rot_dim = %d (a multiple of 8, at most %d)",
+                        rotation->rot_dim, head_dim);
+        if (rotation->table_rows < 1 || rotation->table_rows > INT_MAX)
+            return fail(CFZ_ERR_SHAPE, "table_rows = %lld", (long long)rotation->table_rows);
+        if (!rotation->cos || !rotation->sin)
+            return fail(CFZ_ERR_NULL, "the rotation's cos and sin are required");
+        if (!aligned(rotation->cos, 16) || !aligned(rotation->sin, 16) ||
+            !aligned(rotation->positions, 4))
+            return fail(CFZ_ERR_ALIGN, "cos and sin must be 16-byte, positions 4-byte aligned");
+        a.cos = rotation->cos;
+        a.sin = rotation->sin;
+        a.pos = rotation->positions;
+        a.table_rows = rotation->table_rows;
+        a.rot = rotation->rot_dim;
+        a.interleaved = rotation->interleaved != 0;
+    }
+    for (int i = 0; i < count; ++i) {
+        const cfz_rotate_rows &t = tensors[i];
+        if (t.heads < 1 || t.heads > 1024)
+            return fail(CFZ_ERR_SHAPE, "tensor %d: heads = %d", i, t.heads);
+        CFZ_TRY(check_stride(t.x_stride, (int64_t)t.heads * head_dim, dtype, "x_stride"));
+        CFZ_TRY(check_stride(t.out_stride, (int64_t)t.heads * head_dim, dtype, "out_stride"));
+        if (t.weight && !normed)
+            return fail(CFZ_ERR_UNSUPPORTED, "tensor %d: a weight without a norm", i);
+        CFZ_TRY(check_vec(t.weight, t.weight_dtype, dtype, "weight"));
+        if (tokens > 0 && (!t.x || !t.out))
+            return fail(CFZ_ERR_NULL, "tensor %d: x and out are required", i);
+        if (!aligned(t.x, 16) || !aligned(t.out, 16))
+            return fail(CFZ_ERR_ALIGN, "tensor %d: x and out must be 16-byte aligned", i);
+        if (t.x == t.out && t.x_stride != t.out_stride)
+            return fail(CFZ_ERR_SHAPE, "in place, the strides must be the same");
+        a.t[i] = cfz::RotateRows{t.x,        t.out,        t.weight,
+                                 t.x_stride, t.out_stride, t.weight_dtype == CFZ_KV8_F32, a.heads};
+        a.heads += t.heads;
+    }
+    a.count = count;
+    a.dim = head_dim;
+    a.log2lanes = head_dim == 32 ? 2 : (head_dim == 64 ? 3 : (head_dim == 128 ? 4 : 5));
+    a.starts = starts;
+    a.normed = normed != 0;
+    a.eps = eps;
+    const int heads = (cfz::kRotateUnits * 64) >> a.log2lanes;  // a wave's
+    a.parts = (a.heads + heads - 1) / heads;
+    if (tokens == 0)
+        return CFZ_OK;
+    if (cfz::rotate_groups(a) >= cfz::kBlockMaxGroups)
+        return fail(CFZ_ERR_SHAPE, "the call needs %lld work-groups (limit 2^23)",
+                    (long long)cfz::rotate_groups(a));
+    return hip_status(cfz::launch_rotate(a, dtype, (hipStream_t)hip_stream), "rotation launch");
+}
+
+}  // extern "C"

@@ -1,0 +1,206 @@
+// block_norm_kernels.hip -- the norms around a block with its gate and its residual sum.
+#include "block_internal.h"
+
+namespace cfz {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Sum over the threads that hold one row: a wave, or the work-group's four.
+template <int G> __device__ inline float row_sum(float x, float *red)
+{
+    x = wave_sum(x);
+    if (G == 64)
+        return x;
+    __syncthreads();  // (what was read from red before)
+    if ((threadIdx.x & 63) == 0)
+        red[threadIdx.x >> 6] = x;
+    __syncthreads();
+    return (red[0] + red[1]) + (red[2] + red[3]);
+}
+
+// v becomes its norm, in two passes over registers: the mean first, so that nothing cancels in
+// the squares' sum.  Vectors past the row hold zeros and are left out of the second pass.
+template <class T, int V, int G>
+__device__ inline void normalise(float (&v)[V][8], const BlockNormOf &n, int cols, int tid, float *red)
+{
+    if (n.kind == CFZ_NORM_NONE)
+        return;
+    const float inv = 1.0f / (float)cols;
+    float mean = 0.0f;
+    if (n.kind == CFZ_NORM_LAYER) {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                s += v[i][j];
+        mean = row_sum<G>(s, red) * inv;
+    }
+    float q = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        if ((i * G + tid) * 8 < cols) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[i][j] -= mean;
+                q = fmaf(v[i][j], v[i][j], q);
+            }
+        }
+    }
+    const float f = 1.0f / sqrtf(row_sum<G>(q, red) * inv + n.eps);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int at = (i * G + tid) * 8;
+        if (at < cols) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[i][j] *= f;
+            float w[8];
+            if (n.w.p) {
+                load_vec<T>(n.w, at, w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[i][j] *= w[j];
+            }
+            if (n.b.p) {
+                load_vec<T>(n.b, at, w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[i][j] += w[j];
+            }
+        }
+    }
+}
+
+// A row stays in registers from its load to its stores: x and y are read once, r and h written once.
+// G threads hold a row, V vectors of 8 values each.
+template <class X, class Y, int V, int G>
+__global__ __launch_bounds__(kThreads) void residual_norm_kernel(ResidualArgs a)
+{
+    __shared__ float red[4];
+    const int tid = G == 64 ? threadIdx.x & 63 : threadIdx.x;
+    const int64_t row = G == 64 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+    if (row >= a.rows.tokens)
+        return;
+    const X *x = (const X *)a.x + row * a.xs;
+    const Y *y = (const Y *)a.y + row * a.ys;
+    float v[V][8];
+    // (rows of no item are not read: the loads wait for the item only where offsets are given)
+    int64_t first;
+    const int item = block_item(a.rows, row, &first);
+    if (item < 0)
+        return;
+    if (a.y) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int at = (i * G + tid) * 8;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[i][j] = 0.0f;
+            if (at < a.cols)
+                load_n(y + at, v[i]);
+        }
+        float u[V][8];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int at = (i * G + tid) * 8;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                u[i][j] = 0.0f;
+            if (at < a.cols)
+                load_n(x + at, u[i]);
+        }
+        normalise<Y, V, G>(v, a.after, a.cols, tid, red);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int at = (i * G + tid) * 8;
+            if (at >= a.cols)
+                continue;
+            float g[8];
+            if (a.gate.p)
+                load_vec<Y>(a.gate, item * a.gate.stride + at, g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[i][j] = fmaf(a.gate.p ? g[j] * a.gate_scale : a.gate_scale, v[i][j], u[i][j]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int at = (i * G + tid) * 8;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[i][j] = 0.0f;
+            if (at < a.cols)
+                load_n(x + at, v[i]);
+        }
+    }
+    if (a.r) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int at = (i * G + tid) * 8;
+            if (at < a.cols)
+                store_n((X *)a.r + row * a.rs + at, v[i]);
+        }
+    }
+    if (!a.h)
+        return;
+    normalise<Y, V, G>(v, a.before, a.cols, tid, red);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int at = (i * G + tid) * 8;
+        if (at >= a.cols)
+            continue;
+        float w[8];
+        if (a.scale.p) {
+            load_vec<Y>(a.scale, item * a.scale.stride + at, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[i][j] *= 1.0f + w[j];
+        }
+        if (a.shift.p) {
+            load_vec<Y>(a.shift, item * a.shift.stride + at, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[i][j] += w[j];
+        }
+        store_n((Y *)a.h + row * a.hs + at, v[i]);
+    }
+}
+
+template <class X, class Y> hipError_t launch_as(const ResidualArgs &a, hipStream_t st)
+{
+    const int64_t t = a.rows.tokens;
+    const bool wide = a.cols > 4096;
+    const int group = wide ? 256 : 64;
+    const int need = (a.cols / 8 + group - 1) / group;
+    const dim3 grid((unsigned)(wide ? t : (t + 3) / 4));
+#define CFZ_NORM_CASE(V, G)                                                                        \
+    if (group == G && need <= V) {                                                                 \
+        residual_norm_kernel<X, Y, V, G><<<grid, kThreads, 0, st>>>(a);                             \
+        return hipGetLastError();                                                                  \
+    }
+    CFZ_NORM_CASE(1, 64)
+    CFZ_NORM_CASE(2, 64)
+    CFZ_NORM_CASE(4, 64)
+    CFZ_NORM_CASE(8, 64)
+    CFZ_NORM_CASE(4, 256)
+    CFZ_NORM_CASE(8, 256)
+#undef CFZ_NORM_CASE
+    return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+hipError_t launch_residual_norm(const ResidualArgs &a, int x_dtype, int y_dtype, hipStream_t st)
+{
+    if (y_dtype == CFZ_KV8_F32)
+        return launch_as<float, float>(a, st);
+    if (y_dtype == CFZ_KV8_BF16)
+        return x_dtype == CFZ_KV8_F32 ? launch_as<float, uint16_t>(a, st)
+                                      : launch_as<uint16_t, uint16_t>(a, st);
+    return x_dtype == CFZ_KV8_F32 ? launch_as<float, _Float16>(a, st)
+                                  : launch_as<_Float16, _Float16>(a, st);
+}
+
+}  // namespace cfz

@@ -1,0 +1,152 @@
+// block_rotate_kernels.hip -- tables of angles, and the norm and rotation of queries and keys.
+#include "block_internal.h"
+
+namespace cfz {
+namespace {
+
+constexpr int kThreads = 256;
+
+// One angle a thread, in 64 bits: an angle past 2^16 in fp32 is only known to 2^-8 radians.
+__global__ __launch_bounds__(kThreads) void rotation_table_kernel(TableArgs a)
+{
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    const int64_t row = i / a.pairs;
+    const int pair = (int)(i - row * a.pairs);
+    if (row >= a.rows)
+        return;
+    const double place =
+        a.positions ? (double)a.positions[row * a.axes + a.axis[pair]] : (double)row;
+    double s, c;
+    sincos(place * a.speed[pair], &s, &c);
+    a.cos[i] = (float)(a.amplitude * c);
+    a.sin[i] = (float)(a.amplitude * s);
+}
+
+constexpr int kStay = 0, kPairs = 1, kHalves = 2;  // how heads turn
+
+// A wave takes kRotateUnits x 64 units of 8 dimensions of one token, the tensors' heads side by
+// side; a head's units lie on neighbouring lanes, so that its norm is a short sum across lanes.  A
+// unit holds whole pairs: 8 neighbours, or 4 of each half.  All of a thread's units have the same
+// place in their heads, so that its cosines and sines are loaded once.
+template <class T, int TURN>
+__global__ __launch_bounds__(kThreads) void rotate_kernel(RotateArgs a)
+{
+    const int lane = threadIdx.x & 63;
+    const int64_t wave = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
+    const int64_t row = wave / a.parts;
+    if (row >= a.rows.tokens)
+        return;
+    int64_t first;
+    const int seq = block_item(a.rows, row, &first);
+    if (seq < 0)
+        return;
+    const int lanes = 1 << a.log2lanes;
+    const int unit = lane & (lanes - 1);
+    const int head0 = (int)(wave % a.parts) * ((kRotateUnits * 64) >> a.log2lanes) +
+                      (lane >> a.log2lanes);
+    const int half = a.rot / 2;
+    const bool turn = TURN != kStay && unit * 8 < a.rot;
+    const bool split = TURN == kHalves && turn;
+    const int d0 = split ? 4 * unit : 8 * unit, d1 = split ? half + 4 * unit : 8 * unit + 4;
+
+    float v[kRotateUnits][8];
+    int which[kRotateUnits];
+#pragma unroll
+    for (int i = 0; i < kRotateUnits; ++i) {
+        const int head = head0 + i * (64 >> a.log2lanes);
+        int t = 0;
+        while (t + 1 < a.count && head >= a.t[t + 1].first)
+            ++t;
+        which[i] = head < a.heads ? t : -1;
+        if (which[i] < 0)
+            continue;
+        const T *x = (const T *)a.t[t].x + row * a.t[t].xs + (head - a.t[t].first) * a.dim;
+        if (split) {
+            load_n(x + d0, *(float(*)[4]) & v[i][0]);
+            load_n(x + d1, *(float(*)[4]) & v[i][4]);
+        } else {
+            load_n(x + d0, v[i]);
+        }
+    }
+    float co[4], si[4];
+    if (turn) {
+        int64_t pos = a.pos ? (int64_t)a.pos[row] : (a.starts ? (int64_t)a.starts[seq] : 0) + (row - first);
+        pos = pos < 0 ? 0 : (pos >= a.table_rows ? a.table_rows - 1 : pos);
+        load_n(a.cos + pos * half + 4 * unit, co);
+        load_n(a.sin + pos * half + 4 * unit, si);
+    }
+#pragma unroll
+    for (int i = 0; i < kRotateUnits; ++i) {
+        // (the lanes of a head go together)
+        if (which[i] < 0)
+            continue;
+        const RotateRows &t = a.t[which[i]];
+        if (a.normed) {
+            float q = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                q = fmaf(v[i][j], v[i][j], q);
+            const float f = 1.0f / sqrtf(lanes_sum(q, lanes) / (float)a.dim + a.eps);
+            float w[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
+            if (t.w) {
+                const BlockVec wv{t.w, 0, t.w_f32};
+                load_vec<T>(wv, d0, *(float(*)[4]) & w[0]);
+                load_vec<T>(wv, d1, *(float(*)[4]) & w[4]);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[i][j] *= f * w[j];
+        }
+        if (turn) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int p0 = TURN == kHalves ? j : 2 * j, p1 = TURN == kHalves ? 4 + j : 2 * j + 1;
+                const float y0 = v[i][p0], y1 = v[i][p1];
+                v[i][p0] = fmaf(y0, co[j], -(y1 * si[j]));
+                v[i][p1] = fmaf(y0, si[j], y1 * co[j]);
+            }
+        }
+        const int head = head0 + i * (64 >> a.log2lanes);
+        T *o = (T *)t.out + row * t.os + (head - t.first) * a.dim;
+        if (split) {
+            store_n(o + d0, *(float(*)[4]) & v[i][0]);
+            store_n(o + d1, *(float(*)[4]) & v[i][4]);
+        } else {
+            store_n(o + d0, v[i]);
+        }
+    }
+}
+
+template <class T> hipError_t rotate_as(const RotateArgs &a, hipStream_t st)
+{
+    const dim3 grid((unsigned)rotate_groups(a));
+    (!a.cos          ? rotate_kernel<T, kStay>
+     : a.interleaved ? rotate_kernel<T, kPairs>
+                     : rotate_kernel<T, kHalves>)<<<grid, kThreads, 0, st>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_rotation_table(const TableArgs &a, hipStream_t st)
+{
+    const int64_t n = a.rows * a.pairs;
+    rotation_table_kernel<<<dim3((unsigned)((n + kThreads - 1) / kThreads)), kThreads, 0, st>>>(a);
+    return hipGetLastError();
+}
+
+int64_t rotate_groups(const RotateArgs &a)
+{
+    return (a.rows.tokens * a.parts + kThreads / 64 - 1) / (kThreads / 64);
+}
+
+hipError_t launch_rotate(const RotateArgs &a, int dtype, hipStream_t st)
+{
+    switch (dtype) {
+    case CFZ_KV8_BF16: return rotate_as<uint16_t>(a, st);
+    case CFZ_KV8_F16: return rotate_as<_Float16>(a, st);
+    default: return rotate_as<float>(a, st);
+    }
+}
+
+}  // namespace cfz

@@ -1,33 +1,16 @@
 // kv8_api.hip -- the C ABI of the 8-bit paged K/V cache: argument validation and dispatch.
 // Nothing touches the device until every argument has been checked.
+#include "api_checks.h"
 #include "kv8_internal.h"
 
 #include <limits.h>
 #include <math.h>
-#include <stdarg.h>
-#include <stdio.h>
+
+using cfz::aligned;
+using cfz::fail;
+using cfz::hip_status;
 
 namespace {
-
-cfz_status fail(cfz_status st, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
-cfz_status fail(cfz_status st, const char *fmt, ...)
-{
-    char text[256];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(text, sizeof text, fmt, ap);
-    va_end(ap);
-    return cfz::report(st, text);
-}
-
-cfz_status hip_status(hipError_t e, const char *what)
-{
-    if (e == hipSuccess)
-        return CFZ_OK;
-    return fail(CFZ_ERR_HIP, "%s: %s (%d)", what, hipGetErrorString(e), (int)e);
-}
-
-bool aligned(const void *p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
 // Sizes only, so that the workspace queries can use it too.
 cfz_status check_sizes(const cfz_kv8_cache *c, const cfz_kv8_batch *b, cfz::Kv8Cache *kc,
@@ -146,13 +129,6 @@ cfz_status check_workspace(const void *ws, size_t have, size_t need)
 }
 
 }  // namespace
-
-#define CFZ_TRY(x)                                                                                 \
-    do {                                                                                           \
-        const cfz_status cfz_st_ = (x);                                                            \
-        if (cfz_st_ != CFZ_OK)                                                                     \
-            return cfz_st_;                                                                        \
-    } while (0)
 
 extern "C" {
 

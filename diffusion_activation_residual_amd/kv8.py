@@ -97,6 +97,50 @@ def _ints(t, shape, device, what):
     return t.data_ptr()
 
 
+def _empty_on(device, stream, shape, dtype):
+    """Memory that belongs to the work queued on `stream` (None: the current one)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if isinstance(stream, int):
+        raise ValueError("a raw stream handle needs explicit outputs and workspace")
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _queue(call, device, stream, *args):
+    """The library's call on `stream` (a stream, its handle, or None: the current one)."""
+    index = device.index
+    if stream is None:  # (the public current_stream() costs as much as the rest of a call)
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    elif not isinstance(stream, int):
+        if stream.device != device:
+            raise ValueError(f"stream on {stream.device}, the tensors are on {device}")
+        stream = stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        st = call(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            st = call(*args, stream)
+    if st != CFZ_OK:
+        raise CfzError(st, call.__name__)
+
+
+def _rotation(rotation, tokens, device):
+    if rotation is None:
+        return None
+    cos, sin, pos = rotation.cos, rotation.sin, rotation.positions
+    if cos.dim() != 2 or cos.shape != sin.shape:
+        raise ValueError("rotation: cos and sin must be [rows, rot_dim / 2]")
+    for t in (cos, sin):
+        if t.dtype != torch.float32 or not t.is_contiguous() or t.device != device:
+            raise ValueError("rotation: cos and sin must be contiguous fp32 tensors on "
+                             "the cache's device")
+    return C.byref(cfz_kv8_rotation(
+        cos.data_ptr(), sin.data_ptr(),
+        None if pos is None else _ints(pos, (tokens,), device, "positions"),
+        cos.shape[0], 2 * cos.shape[1], bool(rotation.interleaved)))
+
+
 def _rows(t, heads, dim, device, what):
     """[tokens, heads, dim] with dense rows; returns the row stride in elements."""
     if t.device != device:
@@ -188,13 +232,7 @@ class Cache:
                              _ints(lengths, (batch,), self.device, "lengths"), tokens, max_rows)
 
     def _empty(self, stream, shape, dtype):
-        """Memory that belongs to the work queued on `stream` (None: the current one)."""
-        if stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        if isinstance(stream, int):
-            raise ValueError("a raw stream handle needs explicit outputs and workspace")
-        with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=self.device)
+        return _empty_on(self.device, stream, shape, dtype)
 
     def _fill(self, t, value, stream):
         if isinstance(stream, int):
@@ -243,19 +281,7 @@ class Cache:
         return ks, vs
 
     def _turn(self, rotation, tokens):
-        if rotation is None:
-            return None
-        cos, sin, pos = rotation.cos, rotation.sin, rotation.positions
-        if cos.dim() != 2 or cos.shape != sin.shape:
-            raise ValueError("rotation: cos and sin must be [rows, rot_dim / 2]")
-        for t in (cos, sin):
-            if t.dtype != torch.float32 or not t.is_contiguous() or t.device != self.device:
-                raise ValueError("rotation: cos and sin must be contiguous fp32 tensors on "
-                                 "the cache's device")
-        return C.byref(cfz_kv8_rotation(
-            cos.data_ptr(), sin.data_ptr(),
-            None if pos is None else _ints(pos, (tokens,), self.device, "positions"),
-            cos.shape[0], 2 * cos.shape[1], bool(rotation.interleaved)))
+        return _rotation(rotation, tokens, self.device)
 
     def _outputs(self, q, out):
         """Row stride of given outputs."""

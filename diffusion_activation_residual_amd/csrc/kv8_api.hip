@@ -128,6 +128,60 @@ cfz_status check_workspace(const void *ws, size_t have, size_t need)
     return CFZ_OK;
 }
 
+// The management calls' sizes and arrays.
+cfz_status check_table(const cfz_kv8_pages *p, cfz::Kv8Pages *out)
+{
+    if (!p)
+        return fail(CFZ_ERR_NULL, "pages is required");
+    if (p->page_tokens != 32 && p->page_tokens != 64 && p->page_tokens != 128)
+        return fail(CFZ_ERR_UNSUPPORTED, "page_tokens = %d (supported: 32, 64, 128)",
+                    p->page_tokens);
+    if (p->pages < 0 || p->pages > INT_MAX)
+        return fail(CFZ_ERR_SHAPE, "pages = %lld", (long long)p->pages);
+    if (p->batch < 1 || p->batch > 65535)
+        return fail(CFZ_ERR_SHAPE, "batch = %d", p->batch);
+    if (p->table_width < 1 || (int64_t)p->table_width * p->page_tokens > INT_MAX)
+        return fail(CFZ_ERR_SHAPE, "table_width = %d", p->table_width);
+    *out = cfz::Kv8Pages{p->page_table, p->lengths,     p->refs, p->pages, p->batch,
+                         p->table_width, p->page_tokens == 32 ? 5 : (p->page_tokens == 64 ? 6 : 7)};
+    return CFZ_OK;
+}
+
+cfz_status check_table_pointers(const cfz::Kv8Pages &p)
+{
+    if (!p.table || !p.len || (p.pages > 0 && !p.refs))
+        return fail(CFZ_ERR_NULL, "page_table, lengths and refs are required");
+    if (!aligned(p.table, 4) || !aligned(p.len, 4) || !aligned(p.refs, 4))
+        return fail(CFZ_ERR_ALIGN, "page_table, lengths and refs must be 4-byte aligned");
+    return CFZ_OK;
+}
+
+// Lists of `count` rows, worked on a thread a place.
+cfz_status check_lists(const cfz::Kv8Pages &p, int32_t count)
+{
+    if (count < 0 || count > 65535)
+        return fail(CFZ_ERR_SHAPE, "count = %d", count);
+    return check_groups((double)count * ((p.width + 255) / 256));
+}
+
+cfz_status check_reserve(const cfz::Kv8Pages &p, int64_t max_new, cfz::Kv8Reserve *r)
+{
+    if (max_new < 0 || max_new > INT_MAX)
+        return fail(CFZ_ERR_SHAPE, "max_new = %lld", (long long)max_new);
+    *r = cfz::kv8_reserve_plan(p, max_new);
+    if (r->places > 1 << 30)
+        return fail(CFZ_ERR_SHAPE, "%lld places for new tokens (limit 2^30)",
+                    (long long)r->places);
+    return CFZ_OK;
+}
+
+cfz_status check_compact(const cfz::Kv8Pages &p)
+{
+    return check_groups((double)p.batch * p.width / 256 + 1);
+}
+
+size_t compact_ints(const cfz::Kv8Pages &p) { return (size_t)cfz::kv8_compact_chunks(p) + p.pages; }
+
 }  // namespace
 
 extern "C" {
@@ -314,6 +368,140 @@ cfz_status cfz_kv8_select(const cfz_kv8_cache *cache, const cfz_kv8_batch *batch
     a.first = first;
     a.last = last;
     return hip_status(cfz::launch_kv8_select(c, b, a, (hipStream_t)hip_stream), "select launch");
+}
+
+cfz_status cfz_kv8_free(const cfz_kv8_pages *pages, int32_t count, const int32_t *rows,
+                        const int32_t *keep, void *hip_stream)
+{
+    cfz::Kv8Pages p;
+    CFZ_TRY(check_table(pages, &p));
+    CFZ_TRY(check_lists(p, count));
+    if (count == 0)
+        return CFZ_OK;
+    CFZ_TRY(check_table_pointers(p));
+    if (!rows)
+        return fail(CFZ_ERR_NULL, "rows is required");
+    if (!aligned(rows, 4) || !aligned(keep, 4))
+        return fail(CFZ_ERR_ALIGN, "rows and keep must be 4-byte aligned");
+    return hip_status(cfz::launch_kv8_free(p, count, rows, keep, (hipStream_t)hip_stream),
+                      "free launch");
+}
+
+cfz_status cfz_kv8_fork(const cfz_kv8_pages *pages, int32_t count, const int32_t *parents,
+                        const int32_t *children, void *hip_stream)
+{
+    cfz::Kv8Pages p;
+    CFZ_TRY(check_table(pages, &p));
+    CFZ_TRY(check_lists(p, count));
+    if (count == 0)
+        return CFZ_OK;
+    CFZ_TRY(check_table_pointers(p));
+    if (!parents || !children)
+        return fail(CFZ_ERR_NULL, "parents and children are required");
+    if (!aligned(parents, 4) || !aligned(children, 4))
+        return fail(CFZ_ERR_ALIGN, "parents and children must be 4-byte aligned");
+    return hip_status(cfz::launch_kv8_fork(p, count, parents, children, (hipStream_t)hip_stream),
+                      "fork launch");
+}
+
+size_t cfz_kv8_reserve_workspace_bytes(const cfz_kv8_pages *pages, int64_t max_new)
+{
+    cfz::Kv8Pages p;
+    cfz::Kv8Reserve r;
+    if (check_table(pages, &p) != CFZ_OK || check_reserve(p, max_new, &r) != CFZ_OK)
+        return 0;
+    return (size_t)cfz::kv8_reserve_ints(p, r) * 4;
+}
+
+cfz_status cfz_kv8_reserve(const cfz_kv8_pages *pages, const int32_t *counts, int64_t max_new,
+                           int32_t *source, int32_t *target, int32_t *missing, void *workspace,
+                           size_t ws_bytes, void *hip_stream)
+{
+    cfz::Kv8Pages p;
+    cfz::Kv8Reserve r;
+    CFZ_TRY(check_table(pages, &p));
+    CFZ_TRY(check_reserve(p, max_new, &r));
+    CFZ_TRY(check_table_pointers(p));
+    if (!counts || !source || !target || !missing)
+        return fail(CFZ_ERR_NULL, "counts, source, target and missing are required");
+    if (!aligned(counts, 4) || !aligned(source, 4) || !aligned(target, 4) || !aligned(missing, 4))
+        return fail(CFZ_ERR_ALIGN, "counts, source, target and missing must be 4-byte aligned");
+    CFZ_TRY(check_workspace(workspace, ws_bytes, (size_t)cfz::kv8_reserve_ints(p, r) * 4));
+    r.counts = counts;
+    r.source = source;
+    r.target = target;
+    r.missing = missing;
+    r.rank = (int32_t *)workspace;
+    r.list = r.rank + r.places;
+    r.owner = r.list + r.fresh;
+    r.writers = r.owner + p.pages;
+    return hip_status(cfz::launch_kv8_reserve(p, r, (hipStream_t)hip_stream), "reserve launch");
+}
+
+size_t cfz_kv8_compact_workspace_bytes(const cfz_kv8_pages *pages)
+{
+    cfz::Kv8Pages p;
+    if (check_table(pages, &p) != CFZ_OK || check_compact(p) != CFZ_OK)
+        return 0;
+    return compact_ints(p) * 4;
+}
+
+cfz_status cfz_kv8_compact(const cfz_kv8_pages *pages, int32_t *source, int32_t *target,
+                           int32_t *live, int32_t *moves, void *workspace, size_t ws_bytes,
+                           void *hip_stream)
+{
+    cfz::Kv8Pages p;
+    CFZ_TRY(check_table(pages, &p));
+    CFZ_TRY(check_compact(p));
+    CFZ_TRY(check_table_pointers(p));
+    if ((p.pages > 1 && (!source || !target)) || !live || !moves)
+        return fail(CFZ_ERR_NULL, "source, target, live and moves are required");
+    if (!aligned(source, 4) || !aligned(target, 4) || !aligned(live, 4) || !aligned(moves, 4))
+        return fail(CFZ_ERR_ALIGN, "source, target, live and moves must be 4-byte aligned");
+    CFZ_TRY(check_workspace(workspace, ws_bytes, compact_ints(p) * 4));
+    cfz::Kv8Compact k;
+    k.counts = (int32_t *)workspace;
+    k.where = k.counts + cfz::kv8_compact_chunks(p);
+    k.source = source;
+    k.target = target;
+    k.live = live;
+    k.moves = moves;
+    return hip_status(cfz::launch_kv8_compact(p, k, (hipStream_t)hip_stream), "packing launch");
+}
+
+cfz_status cfz_kv8_copy(const cfz_kv8_cache *to, const cfz_kv8_cache *from, int64_t count,
+                        const int32_t *source, const int32_t *target, const int32_t *used,
+                        void *hip_stream)
+{
+    const cfz_kv8_batch none = {0, 1, nullptr, nullptr, nullptr, 0, 0};
+    cfz::Kv8Cache a, b;
+    cfz::Kv8Batch batch;
+    if (!from)
+        from = to;
+    CFZ_TRY(check_sizes(to, &none, &b, &batch));
+    CFZ_TRY(check_sizes(from, &none, &a, &batch));
+    if (a.heads != b.heads || a.dim != b.dim || a.page != b.page || a.fmt != b.fmt)
+        return fail(CFZ_ERR_SHAPE, "the caches' pages differ");
+    if (count < 0 || count > INT_MAX)
+        return fail(CFZ_ERR_SHAPE, "count = %lld", (long long)count);
+    if (count == 0 || a.pages == 0 || b.pages == 0)
+        return CFZ_OK;
+    for (const cfz::Kv8Cache *c : {&a, &b}) {
+        if (!c->k || !c->v || !c->ks || !c->vs)
+            return fail(CFZ_ERR_NULL, "the cache's k, v, k_scale and v_scale are required");
+        if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->ks, 16) ||
+            !aligned(c->vs, 16) || !aligned(c->km, 16))
+            return fail(CFZ_ERR_ALIGN, "the cache's buffers must be 16-byte aligned");
+    }
+    if (b.km && !a.km)
+        return fail(CFZ_ERR_NULL, "from needs k_mean if to has it");
+    if (!source || !target)
+        return fail(CFZ_ERR_NULL, "source and target are required");
+    if (!aligned(source, 4) || !aligned(target, 4) || !aligned(used, 4))
+        return fail(CFZ_ERR_ALIGN, "source, target and used must be 4-byte aligned");
+    return hip_status(cfz::launch_kv8_copy(b, a, count, source, target, used,
+                                           (hipStream_t)hip_stream),
+                      "copy launch");
 }
 
 }  // extern "C"

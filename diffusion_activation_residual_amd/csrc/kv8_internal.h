@@ -86,6 +86,46 @@ hipError_t launch_kv8_select(const Kv8Cache &c, const Kv8Batch &b, const Kv8Sele
 // A status with its text for cfz_last_error (cfz_api.hip).
 cfz_status report(cfz_status st, const char *text);
 
+// ---- pages
+
+struct Kv8Pages {
+    int32_t *table, *len, *refs;
+    int64_t pages;
+    int batch, width, log2page;
+};
+
+hipError_t launch_kv8_free(const Kv8Pages &p, int count, const int32_t *rows, const int32_t *keep,
+                           hipStream_t st);
+hipError_t launch_kv8_fork(const Kv8Pages &p, int count, const int32_t *parents,
+                           const int32_t *children, hipStream_t st);
+
+// Places that a row's new tokens may need, and a reserve call's workspace: for every place its rank
+// among those that need a page, the free pages, and two counters of each page.
+struct Kv8Reserve {
+    const int32_t *counts;
+    int64_t max_new;
+    int span;
+    int64_t places, fresh;
+    int32_t *rank, *list, *owner, *writers;
+    int32_t *source, *target, *missing;
+};
+Kv8Reserve kv8_reserve_plan(const Kv8Pages &p, int64_t max_new);
+int64_t kv8_reserve_ints(const Kv8Pages &p, const Kv8Reserve &r);
+hipError_t launch_kv8_reserve(const Kv8Pages &p, const Kv8Reserve &r, hipStream_t st);
+
+constexpr int kKv8RefsChunk = 4096;  // pages that a work-group of the packing looks at
+struct Kv8Compact {
+    int32_t *counts;  // pages in use of each chunk
+    int32_t *where;   // a page's number among the moves, -1: none
+    int32_t *source, *target, *live, *moves;
+};
+int kv8_compact_chunks(const Kv8Pages &p);
+hipError_t launch_kv8_compact(const Kv8Pages &p, const Kv8Compact &k, hipStream_t st);
+
+hipError_t launch_kv8_copy(const Kv8Cache &to, const Kv8Cache &from, int64_t count,
+                           const int32_t *source, const int32_t *target, const int32_t *used,
+                           hipStream_t st);
+
 // Rows of one sequence as the kernels see them: clamped into the call's token rows.
 __device__ inline void kv8_rows(const Kv8Batch &b, int seq, int &first, int &n)
 {

@@ -46,9 +46,15 @@ class cfz_kv8_blocks(C.Structure):
     _fields_ = [("blocks", C.c_void_p), ("count", C.c_int32), ("q_block", C.c_int32)]
 
 
+class cfz_kv8_pages(C.Structure):
+    _fields_ = [("pages", C.c_int64), ("batch", C.c_int32), ("table_width", C.c_int32),
+                ("page_tokens", C.c_int32), ("page_table", C.c_void_p), ("lengths", C.c_void_p),
+                ("refs", C.c_void_p)]
+
+
 _p, _i64, _i32, _sz = C.c_void_p, C.c_int64, C.c_int32, C.c_size_t
 _cache, _batch = C.POINTER(cfz_kv8_cache), C.POINTER(cfz_kv8_batch)
-_blocks = C.POINTER(cfz_kv8_blocks)
+_blocks, _pages = C.POINTER(cfz_kv8_blocks), C.POINTER(cfz_kv8_pages)
 _SIGNATURES = {
     "cfz_kv8_append": ([_cache, _batch, _i32, _p, _p, _i64, _i64, C.POINTER(cfz_kv8_rotation), _p],
                        _i32),
@@ -59,6 +65,13 @@ _SIGNATURES = {
     "cfz_kv8_select": ([_cache, _batch, _i32, _p, _i64, _i32, _i32, _i64, _i32, _i32, _blocks, _p,
                         _sz, _p], _i32),
     "cfz_kv8_select_workspace_bytes": ([_cache, _batch, _i64, _blocks], _sz),
+    "cfz_kv8_free": ([_pages, _i32, _p, _p, _p], _i32),
+    "cfz_kv8_fork": ([_pages, _i32, _p, _p, _p], _i32),
+    "cfz_kv8_reserve": ([_pages, _p, _i64, _p, _p, _p, _p, _sz, _p], _i32),
+    "cfz_kv8_reserve_workspace_bytes": ([_pages, _i64], _sz),
+    "cfz_kv8_compact": ([_pages, _p, _p, _p, _p, _p, _sz, _p], _i32),
+    "cfz_kv8_compact_workspace_bytes": ([_pages], _sz),
+    "cfz_kv8_copy": ([_cache, _cache, _i64, _p, _p, _p, _p], _i32),
 }
 _lib = cfz._lib
 for _name, (_args, _res) in _SIGNATURES.items():
@@ -407,3 +420,123 @@ class Cache:
         if q.shape[0] == 0:  # (the library checks such a call and leaves the lists alone)
             self._fill(blocks, -1, stream)
         return blocks
+
+    def copy(self, moves, origin=None, stream=None):
+        """Copies whole pages: page moves.source[i] of ``origin`` (another cache with pages of the same
+        kind; default: this one) to page moves.target[i], for the first moves.count[0] pairs, or
+        all.  Pairs that name a page outside its pool (-1) are left out.  No target may be another
+        pair's target or, within one cache, its source."""
+        source, target, count = moves.source, moves.target, moves.count
+        shape = (source.numel(),)
+        if origin is not None and origin.device != self.device:
+            raise ValueError(f"origin: on {origin.device}, the cache is on {self.device}")
+        self._call(_lib.cfz_kv8_copy, stream, self._ref, None if origin is None else origin._ref,
+                   shape[0], _ints(source, shape, self.device, "source"),
+                   _ints(target, shape, self.device, "target"),
+                   None if count is None else _ints(count, (1,), self.device, "count"))
+
+
+@dataclass
+class Moves:
+    """Pages to be copied (``Cache.copy``): ``source`` and ``target`` int32, -1 where there is nothing
+    to do; ``count`` int32 [1], how many of them are meant (None: all)."""
+
+    source: torch.Tensor
+    target: torch.Tensor
+    count: Optional[torch.Tensor] = None
+
+
+class Pages:
+    """Who holds which page of a pool: ``table`` [batch, width] int32 (-1: no page), ``lengths``
+    [batch] int32 and ``refs`` [pages] int32, how many places of the table name each page (0: free).
+    The tensors are changed in place; ``table`` and ``lengths`` are what the calls of ``Cache`` take.
+    Layers whose caches have the same number of pages share one ``Pages``: the moves that a
+    call returns are then made in each layer's cache.
+
+        moves, missing = pages.reserve(counts, max_new)  # pages for counts[b] more tokens a row
+        cache.copy(moves)                                # shared pages about to be written
+        cache.append(k, v, pages.table, pages.lengths, offsets, max_new)
+        pages.lengths += counts
+
+    Every call is queued like those of ``Cache``; nothing is read by the host."""
+
+    def __init__(self, table, lengths, refs, page_tokens):
+        if not table.is_cuda:
+            raise ValueError("table: libcfz takes device tensors")
+        if table.dim() != 2 or refs.dim() != 1:
+            raise ValueError(f"table {tuple(table.shape)}, refs {tuple(refs.shape)}: expected "
+                             "[batch, width] and [pages]")
+        self.device = table.device
+        batch, width = table.shape
+        _fit(32, batch=batch, width=width, page_tokens=page_tokens)
+        self.table, self.lengths, self.refs, self.page_tokens = table, lengths, refs, page_tokens
+        self.desc = cfz_kv8_pages(refs.numel(), batch, width, page_tokens,
+                                  _ints(table, None, self.device, "table"),
+                                  _ints(lengths, (batch,), self.device, "lengths"),
+                                  _ints(refs, None, self.device, "refs"))
+        self._ref = C.byref(self.desc)
+
+    @classmethod
+    def empty(cls, pages, batch, width, page_tokens=64, device="cuda"):
+        """``batch`` rows of up to ``width`` pages that hold nothing yet."""
+        return cls(torch.full((batch, width), -1, dtype=torch.int32, device=device),
+                   torch.zeros(batch, dtype=torch.int32, device=device),
+                   torch.zeros(pages, dtype=torch.int32, device=device), page_tokens)
+
+    def _list(self, t, what, like=None):
+        if t.dim() != 1 or (like is not None and t.shape != like.shape):
+            raise ValueError(f"{what}: shape {tuple(t.shape)}, expected "
+                             f"{'[count]' if like is None else tuple(like.shape)}")
+        return _ints(t, None, self.device, what)
+
+    def free(self, rows, keep=None, stream=None):
+        """Cuts the rows (int32) off behind their first ``keep[i]`` tokens (None: 0); pages that no row
+        holds any more are free."""
+        _fit(32, rows=rows.numel())
+        _queue(_lib.cfz_kv8_free, self.device, stream, self._ref, rows.numel(),
+               self._list(rows, "rows"), None if keep is None else self._list(keep, "keep", rows))
+
+    def fork(self, parents, children, stream=None):
+        """Row children[i] holds the pages and length of row parents[i] too, instead of its own.
+        Nothing is copied until one of them is about to write (``reserve``).  A pair is left out if a
+        row is outside the table, if both are one, if an earlier pair has its child, or if
+        its child is the parent of any pair."""
+        _fit(32, children=children.numel())
+        _queue(_lib.cfz_kv8_fork, self.device, stream, self._ref, children.numel(),
+               self._list(parents, "parents", children), self._list(children, "children"))
+
+    def reserve(self, counts, max_new, workspace=None, stream=None):
+        """Pages for counts[b] (int32 [batch], at most ``max_new``) more tokens behind each row's
+        length, and pages of its own where it would write into one that other rows hold too:
+        (moves, missing).  ``moves`` [batch] are to be copied in every cache before the tokens are appended.
+        ``missing`` (int32 [1]) is 0, or how many more free pages it takes: then nothing has changed."""
+        _fit(64, max_new=max_new)
+        batch = self.table.shape[0]
+        counts = _ints(counts, (batch,), self.device, "counts")
+        need = _lib.cfz_kv8_reserve_workspace_bytes(self._ref, max_new)
+        source, target, missing = _empty_on(self.device, stream, 2 * batch + 1, torch.int32).split(
+            (batch, batch, 1))
+        workspace, have = self._workspace(need, workspace, stream)
+        _queue(_lib.cfz_kv8_reserve, self.device, stream, self._ref, counts, max_new,
+               source.data_ptr(), target.data_ptr(), missing.data_ptr(), workspace, have)
+        return Moves(source, target), missing
+
+    def compact(self, workspace=None, stream=None):
+        """Moves the pages in use to the front of the pool, the highest to the lowest free one:
+        (moves, live), the moves to be made in every cache and the number (int32 [1]) of pages in use,
+        which are then 0 .. live - 1."""
+        most = self.refs.numel() // 2
+        need = _lib.cfz_kv8_compact_workspace_bytes(self._ref)
+        source, target, live, count = _empty_on(self.device, stream, 2 * most + 2,
+                                                torch.int32).split((most, most, 1, 1))
+        workspace, have = self._workspace(need, workspace, stream)
+        _queue(_lib.cfz_kv8_compact, self.device, stream, self._ref, source.data_ptr(),
+               target.data_ptr(), live.data_ptr(), count.data_ptr(), workspace, have)
+        return Moves(source, target, count), live
+
+    def _workspace(self, need, workspace, stream):
+        if workspace is None:
+            workspace = _empty_on(self.device, stream, need, torch.uint8)
+        elif workspace.device != self.device or not workspace.is_contiguous():
+            raise ValueError("workspace: must be contiguous and on the table's device")
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size()

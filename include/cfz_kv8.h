@@ -1,7 +1,8 @@
 /*
  * cfz_kv8.h -- C ABI of libcfz's 8-bit paged K/V cache: appending keys and values
  * with the position rotation applied on the way, reading tokens back, attention
- * over the cache, and attention over pages that a cheap score selects.
+ * over the cache, attention over pages that a cheap score selects, and the
+ * management of a pool's pages (cfz_kv8_free and below).
  *
  * What the codec of cfz.h rebuilds on a receiving device -- one layer's K and V of
  * another device's share -- goes into such a cache, and the device's own queries
@@ -186,6 +187,81 @@ cfz_status cfz_kv8_select(const cfz_kv8_cache *cache, const cfz_kv8_batch *batch
                           void *hip_stream);
 size_t cfz_kv8_select_workspace_bytes(const cfz_kv8_cache *cache, const cfz_kv8_batch *batch,
                                       int64_t max_kv, const cfz_kv8_blocks *blocks);
+
+/* ---- managing pages
+ *
+ * Which row of a page table holds which page of a pool.  page_table: [batch][table_width]
+ * int32, -1 where a row has no page; lengths: [batch] tokens held; refs: [pages] int32, how many
+ * places of the table name each page (0: free).  The arrays live on the device, and the calls keep
+ * them in line with each other.  Layers whose caches have the same sizes can share
+ * them: each call's page moves are then done in every layer's cache (cfz_kv8_copy).  A place that
+ * names no page of 0 .. pages - 1 counts as -1; lengths count as clamped to
+ * [0, table_width * page_tokens].  Limits as in cfz_kv8_cache and cfz_kv8_batch, batch >= 1.
+ * The results of every call are the same whatever the order in which its parts run. */
+typedef struct {
+    int64_t pages;
+    int32_t batch;
+    int32_t table_width;
+    int32_t page_tokens;
+    int32_t *page_table;
+    int32_t *lengths;
+    int32_t *refs;
+} cfz_kv8_pages;
+
+/* Cuts rows rows[i], i < count, off behind their first keep[i] tokens (keep NULL or below 0: 0): places
+ * behind ceil(keep / page_tokens) become -1 and let go of their pages, lengths become at most
+ * keep.  Rows outside the table are left out; one that is listed twice keeps the least.
+ * 0 <= count <= 65535.
+ * Errors: CFZ_ERR_NULL, CFZ_ERR_SHAPE, CFZ_ERR_UNSUPPORTED, CFZ_ERR_ALIGN, CFZ_ERR_HIP. */
+cfz_status cfz_kv8_free(const cfz_kv8_pages *pages, int32_t count, const int32_t *rows,
+                        const int32_t *keep, void *hip_stream);
+
+/* Row children[i] becomes a second holder of row parents[i]'s pages and length, i < count; what
+ * it held before is let go of.  No page is copied: cfz_kv8_reserve gives a row a copy of its own of the page
+ * that it is about to write.  A pair is left out if one of its rows is outside the table, if both
+ * are the same, if an earlier pair has the same child, or if its child is the parent of any pair.
+ * 0 <= count <= 65535.  Errors: as cfz_kv8_free. */
+cfz_status cfz_kv8_fork(const cfz_kv8_pages *pages, int32_t count, const int32_t *parents,
+                        const int32_t *children, void *hip_stream);
+
+/* Makes room for counts[b] more tokens (at most max_new; below 0: 0) behind the lengths[b] of each
+ * row: the places of tokens lengths[b] .. lengths[b] + counts[b] - 1 that have no page get a free one,
+ * and those whose page other rows hold too get a page of their own -- except that, where all holders
+ * of a page are among this call's places, the first of them keeps it.  Free pages are given out from the lowest
+ * up, to the places row by row.  Where such a place already holds tokens of its row (lengths[b] inside a
+ * page), source[b] and target[b] (int32 [batch] each) get the old and the new page, whose contents the
+ * caller then copies (cfz_kv8_copy); otherwise they are -1.  Lengths stay as they are, so
+ * calling twice gives out nothing twice.  Places past the table's end are left out.
+ * missing[0] gets 0 -- or, where there are not enough free pages, how many more it takes: then nothing
+ * is given out.
+ * workspace: cfz_kv8_reserve_workspace_bytes(...) bytes, 256-byte aligned, overwritten.
+ * Errors: as cfz_kv8_free, and CFZ_ERR_WORKSPACE. */
+cfz_status cfz_kv8_reserve(const cfz_kv8_pages *pages, const int32_t *counts, int64_t max_new,
+                           int32_t *source, int32_t *target, int32_t *missing, void *workspace,
+                           size_t ws_bytes, void *hip_stream);
+/* 0 if none is needed or the arguments are invalid. */
+size_t cfz_kv8_reserve_workspace_bytes(const cfz_kv8_pages *pages, int64_t max_new);
+
+/* Moves the pages in use to the front of the pool: with n of them, the highest page in use goes to
+ * the lowest free one until all lie in 0 .. n - 1.  live[0] gets n, moves[0] their number m, and
+ * source[i], target[i], i < m, the moves (int32 [pages / 2] each); table and refs are
+ * changed, the pages' contents are the caller's to copy (cfz_kv8_copy with used = moves).
+ * workspace: cfz_kv8_compact_workspace_bytes(...) bytes, 256-byte aligned, overwritten.
+ * Errors: as cfz_kv8_reserve. */
+cfz_status cfz_kv8_compact(const cfz_kv8_pages *pages, int32_t *source, int32_t *target,
+                           int32_t *live, int32_t *moves, void *workspace, size_t ws_bytes,
+                           void *hip_stream);
+size_t cfz_kv8_compact_workspace_bytes(const cfz_kv8_pages *pages);
+
+/* Copies whole pages, codes, scales and mean keys: page source[i] of `from` (NULL: `to` itself) to page
+ * target[i] of `to`, for i < count and, if used is given, i < used[0] (int32 on the device).  A
+ * pair that names a page outside its pool is left out.  A target must not be another pair's target,
+ * nor (in the same cache) its source: such pages would hold parts of either.  The caches have the same heads, head_dim,
+ * page_tokens and format; from needs k_mean if to has it.  0 <= count < 2^31.
+ * Errors: as cfz_kv8_free. */
+cfz_status cfz_kv8_copy(const cfz_kv8_cache *to, const cfz_kv8_cache *from, int64_t count,
+                        const int32_t *source, const int32_t *target, const int32_t *used,
+                        void *hip_stream);
 
 #ifdef __cplusplus
 }

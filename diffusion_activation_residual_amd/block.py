@@ -3,7 +3,8 @@ the 8-bit K/V cache (``kv8``).
 
 ``residual_norm`` adds a block's gated output to the stream and normalises the sum for the next
 block; ``rotation_table`` makes the tables of a ``kv8.Rotation`` and ``rotate`` turns queries and
-keys by them.  Argument marshalling only: every step runs in the library's HIP kernels.  Because it
+keys by them; ``Adapters`` adds the low-rank adapters of many requests to a projection that they
+share.  Argument marshalling only: every step runs in the library's HIP kernels.  Because it
 sees tensor sizes, which the C ABI cannot, this module refuses (``ValueError`` or ``TypeError``,
 before any device work) tensors that do not fit the call.  Work is queued on ``stream`` (default:
 the current one of the tensors' device); with another stream than the current one the caller orders
@@ -55,12 +56,21 @@ class cfz_rotate_rows(C.Structure):
                 ("weight_dtype", C.c_int32)]
 
 
+class cfz_adapters(C.Structure):
+    _fields_ = [("adapters", C.c_int32), ("slices", C.c_int32), ("rank", C.c_int32),
+                ("cols_in", C.c_int32), ("slice_cols", C.c_int32 * 4), ("dtype", C.c_int32),
+                ("a", C.c_void_p), ("b", C.c_void_p), ("scale", C.c_void_p)]
+
+
 _p, _i64, _i32, _f32 = C.c_void_p, C.c_int64, C.c_int32, C.c_float
 _SIGNATURES = {
     "cfz_residual_norm": ([C.POINTER(cfz_residual), _p], _i32),
     "cfz_rotation_table": ([C.POINTER(cfz_rotation_angles), _i64, _p, _p, _p, _p], _i32),
     "cfz_rotate": ([_i32, C.POINTER(cfz_rotate_rows), _i32, _i32, _i64, _i32, _p, _p,
                     C.POINTER(cfz_kv8_rotation), _i32, _f32, _p], _i32),
+    "cfz_adapters_add": ([C.POINTER(cfz_adapters), _i64, _i32, _p, _p, _i64, _p, _i64, _p, _i64,
+                          _p, _i64, _i32, _p, C.c_size_t, _p], _i32),
+    "cfz_adapters_workspace_bytes": ([C.POINTER(cfz_adapters), _i64, _i32], C.c_size_t),
 }
 _lib = cfz._lib
 for _name, (_args, _res) in _SIGNATURES.items():
@@ -291,3 +301,70 @@ def rotate(tensors, rotation, offsets=None, starts=None, weights=None, eps=1e-6,
            None if starts is None else _ints(starts, (batch,), device, "starts"),
            kv8._rotation(rotation, tokens, device), bool(normed), eps)
     return results
+
+
+class Adapters:
+    """Low-rank adapters of one projection: ``a`` [adapters, slices * rank, cols_in] and ``b``
+    [adapters, cols_out, rank], bf16 or fp16, ``scale`` [adapters] fp32 or None (1).  ``slices``: how
+    many parts of equal width the projection's columns have, or a list of their widths (query,
+    key and value of one fused projection); part i is met by rows i * rank .. (i + 1) * rank - 1 of a.
+    rank: a multiple of 8 up to 128; adapters of a lower one are filled up with zeros."""
+
+    def __init__(self, a, b, scale=None, slices=1):
+        self.device = _device(a, "a")
+        if a.dim() != 3 or b.dim() != 3 or a.dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError(f"a: {a.dtype} {tuple(a.shape)}, b: {tuple(b.shape)}, expected bf16 or "
+                             "fp16 [adapters, slices * rank, cols_in] and [adapters, cols_out, rank]")
+        count, cols_out, rank = b.shape
+        if isinstance(slices, int):
+            if slices < 1 or cols_out % slices:
+                raise ValueError(f"slices = {slices} of {cols_out} columns")
+            slices = [cols_out // slices] * slices
+        slices = list(slices)
+        if not 1 <= len(slices) <= 4 or sum(slices) != cols_out or min(slices) < 1:
+            raise ValueError(f"slices = {slices} of {cols_out} columns")
+        if a.shape[:2] != (count, len(slices) * rank):
+            raise ValueError(f"a: shape {tuple(a.shape)}, expected [{count}, {len(slices) * rank}, "
+                             "cols_in]")
+        if b.dtype != a.dtype or b.device != self.device or not a.is_contiguous() or \
+                not b.is_contiguous():
+            raise ValueError("a and b: must be contiguous, of one type and on one device")
+        if scale is not None and (scale.dtype != torch.float32 or scale.shape != (count,) or
+                                  scale.device != self.device or not scale.is_contiguous()):
+            raise ValueError(f"scale: expected a contiguous fp32 tensor of {count} values")
+        _fit(32, adapters=count, rank=rank, cols_in=a.shape[2], cols_out=cols_out)
+        self.a, self.b, self.scale, self.slices = a, b, scale, slices
+        self.rank, self.cols_in, self.cols_out, self.dtype = rank, a.shape[2], cols_out, a.dtype
+        self.desc = cfz_adapters(count, len(slices), rank, self.cols_in, (C.c_int32 * 4)(*slices),
+                                 _REALS[a.dtype], a.data_ptr(), b.data_ptr(),
+                                 None if scale is None else scale.data_ptr())
+        self._ref = C.byref(self.desc)
+
+    def add(self, x, y, ids, offsets, max_rows, out=None, workspace=None, stream=None):
+        """y + scale * (x a^T) b^T for each sequence's own adapter: x [tokens, cols_in], y [tokens,
+        cols_out] (the shared projection's rows, of x's type or fp32), ``ids`` [batch] int32 (-1: no
+        adapter), ``offsets`` [batch + 1] int32 the sequences' rows, at most ``max_rows`` each.
+        ``out`` may be y; without it the result is allocated (rows of no sequence are then left
+        unset)."""
+        if x.dim() != 2 or y.dim() != 2:
+            raise ValueError(f"x {tuple(x.shape)}, y {tuple(y.shape)}: expected [tokens, cols]")
+        tokens, batch = x.shape[0], ids.numel()
+        xs = _matrix(x, (tokens, self.cols_in), (self.dtype,), self.device, "x")
+        ys = _matrix(y, (tokens, self.cols_out), (self.dtype, torch.float32), self.device, "y")
+        _fit(32, batch=batch)
+        _fit(64, max_rows=max_rows)
+        need = _lib.cfz_adapters_workspace_bytes(self._ref, tokens, batch)
+        if out is None:
+            out, os = _empty_on(self.device, stream, y.shape, y.dtype), self.cols_out
+        else:
+            os = _matrix(out, y.shape, (y.dtype,), self.device, "out")
+        if workspace is None:
+            workspace = _empty_on(self.device, stream, need, torch.uint8)
+        elif workspace.device != self.device or not workspace.is_contiguous():
+            raise ValueError("workspace: must be contiguous and on the adapters' device")
+        _queue(_lib.cfz_adapters_add, self.device, stream, self._ref, tokens, batch,
+               _ints(offsets, (batch + 1,), self.device, "offsets"),
+               _ints(ids, (batch,), self.device, "ids"), max_rows, x.data_ptr(), xs, y.data_ptr(), ys,
+               out.data_ptr(), os, _REALS[y.dtype], workspace.data_ptr(),
+               workspace.numel() * workspace.element_size())
+        return out

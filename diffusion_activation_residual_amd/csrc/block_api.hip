@@ -80,6 +80,61 @@ cfz_status check_norm(const cfz_norm &n, int call, const char *what, cfz::BlockN
     return CFZ_OK;
 }
 
+// Sizes only, so that the workspace query can use it too.
+cfz_status check_adapters(const cfz_adapters *w, int64_t tokens, int32_t batch, cfz::AdapterArgs *a)
+{
+    if (!w)
+        return fail(CFZ_ERR_NULL, "adapters is required");
+    memset(a, 0, sizeof *a);
+    if (w->dtype != CFZ_KV8_BF16 && w->dtype != CFZ_KV8_F16)
+        return fail(CFZ_ERR_UNSUPPORTED, "dtype = %d", w->dtype);
+    if (w->adapters < 1 || w->adapters > 1 << 20)
+        return fail(CFZ_ERR_SHAPE, "adapters = %d (1 .. 2^20)", w->adapters);
+    if (w->slices < 1 || w->slices > 4)
+        return fail(CFZ_ERR_SHAPE, "slices = %d (1 .. 4)", w->slices);
+    if (w->rank < 8 || w->rank > 128 || w->rank % 8 != 0 || w->slices * w->rank > 256)
+        return fail(CFZ_ERR_SHAPE, "rank = %d with %d slices (a multiple of 8, 8 .. 128, 256 in all)",
+                    w->rank, w->slices);
+    if (w->cols_in < 8 || w->cols_in > 1 << 20 || w->cols_in % 8 != 0)
+        return fail(CFZ_ERR_SHAPE, "cols_in = %d (a multiple of 8, 8 .. 2^20)", w->cols_in);
+    int cols = 0, groups = 0;
+    for (int i = 0; i < w->slices; ++i) {
+        const int c = w->slice_cols[i];
+        if (c < 16 || c > 1 << 20 || c % 16 != 0)
+            return fail(CFZ_ERR_SHAPE, "slice_cols[%d] = %d (a multiple of 16, 16 .. 2^20)", i, c);
+        a->first_col[i] = cols;
+        a->first_group[i] = groups;
+        cols += c;
+        groups += (c + 63) / 64;
+    }
+    if (cols > 1 << 20)
+        return fail(CFZ_ERR_SHAPE, "%d columns (at most 2^20)", cols);
+    a->first_col[w->slices] = cols;
+    if (tokens < 0 || tokens > INT_MAX)
+        return fail(CFZ_ERR_SHAPE, "tokens = %lld", (long long)tokens);
+    if (batch < 0 || batch > 65535)
+        return fail(CFZ_ERR_SHAPE, "batch = %d", batch);
+    a->rows.tokens = tokens;
+    a->rows.batch = batch;
+    a->adapters = w->adapters;
+    a->slices = w->slices;
+    a->rank = w->rank;
+    a->down = w->slices * w->rank;
+    a->cols_in = w->cols_in;
+    a->cols_out = cols;
+    a->groups = groups;
+    a->col_tiles = (groups + 3) / 4;
+    cfz::adapter_plan(*a);
+    return CFZ_OK;
+}
+
+size_t adapters_bytes(const cfz::AdapterArgs &a)
+{
+    if (a.rows.tokens == 0 || a.rows.batch == 0)
+        return 0;
+    return (size_t)a.splits * a.rows.tokens * a.down * 4;
+}
+
 }  // namespace
 
 extern "C" {
@@ -283,6 +338,65 @@ cfz_status cfz_rotate(int32_t count, const cfz_rotate_rows *tensors, cfz_kv8_dty
         return fail(CFZ_ERR_SHAPE, "the call needs %lld work-groups (limit 2^23)",
                     (long long)cfz::rotate_groups(a));
     return hip_status(cfz::launch_rotate(a, dtype, (hipStream_t)hip_stream), "rotation launch");
+}
+
+size_t cfz_adapters_workspace_bytes(const cfz_adapters *adapters, int64_t tokens, int32_t batch)
+{
+    cfz::AdapterArgs a;
+    return check_adapters(adapters, tokens, batch, &a) == CFZ_OK ? adapters_bytes(a) : 0;
+}
+
+cfz_status cfz_adapters_add(const cfz_adapters *w, int64_t tokens, int32_t batch,
+                            const int32_t *offsets, const int32_t *ids, int64_t max_rows,
+                            const void *x, int64_t x_stride, const void *y, int64_t y_stride,
+                            void *out, int64_t out_stride, int32_t y_dtype, void *workspace,
+                            size_t ws_bytes, void *hip_stream)
+{
+    cfz::AdapterArgs a;
+    CFZ_TRY(check_adapters(w, tokens, batch, &a));
+    if (y_dtype != w->dtype && y_dtype != CFZ_KV8_F32)
+        return fail(CFZ_ERR_UNSUPPORTED, "y_dtype = %d with dtype = %d", y_dtype, w->dtype);
+    if (max_rows < 0 || max_rows > INT_MAX)
+        return fail(CFZ_ERR_SHAPE, "max_rows = %lld", (long long)max_rows);
+    CFZ_TRY(check_stride(x_stride, a.cols_in, w->dtype, "x_stride"));
+    CFZ_TRY(check_stride(y_stride, a.cols_out, y_dtype, "y_stride"));
+    CFZ_TRY(check_stride(out_stride, a.cols_out, y_dtype, "out_stride"));
+    if (tokens == 0 || batch == 0 || max_rows == 0)
+        return CFZ_OK;
+    if (cfz::adapter_groups(a) >= cfz::kBlockMaxGroups)
+        return fail(CFZ_ERR_SHAPE, "the call needs %lld work-groups (limit 2^23)",
+                    (long long)cfz::adapter_groups(a));
+    if (!w->a || !w->b || !offsets || !ids || !x || !y || !out)
+        return fail(CFZ_ERR_NULL, "a, b, offsets, ids, x, y and out are required");
+    if (!aligned(w->a, 16) || !aligned(w->b, 16) || !aligned(x, 16) || !aligned(y, 16) ||
+        !aligned(out, 16))
+        return fail(CFZ_ERR_ALIGN, "a, b, x, y and out must be 16-byte aligned");
+    if (!aligned(offsets, 4) || !aligned(ids, 4) || !aligned(w->scale, 4))
+        return fail(CFZ_ERR_ALIGN, "offsets, ids and scale must be 4-byte aligned");
+    if (y == out && y_stride != out_stride)
+        return fail(CFZ_ERR_SHAPE, "in place, the strides must be the same");
+    const size_t need = adapters_bytes(a);
+    if (!workspace || ws_bytes < need)
+        return fail(CFZ_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed",
+                    workspace ? ws_bytes : (size_t)0, need);
+    if (!aligned(workspace, 256))
+        return fail(CFZ_ERR_ALIGN, "workspace must be 256-byte aligned");
+    a.rows.off = offsets;
+    a.max_rows = max_rows;
+    a.ids = ids;
+    a.a = w->a;
+    a.b = w->b;
+    a.scale = w->scale;
+    a.x = x;
+    a.y = y;
+    a.out = out;
+    a.xs = x_stride;
+    a.ys = y_stride;
+    a.os = out_stride;
+    a.h = (float *)workspace;
+    return hip_status(cfz::launch_adapters(a, w->dtype == CFZ_KV8_F16, y_dtype == CFZ_KV8_F32,
+                                           (hipStream_t)hip_stream),
+                      "adapter launch");
 }
 
 }  // extern "C"

@@ -78,6 +78,29 @@ constexpr int kRotateUnits = 4;  // units of 8 dimensions a thread
 int64_t rotate_groups(const RotateArgs &a);
 hipError_t launch_rotate(const RotateArgs &a, int dtype, hipStream_t st);
 
+struct AdapterArgs {
+    BlockRows rows;
+    int64_t max_rows;
+    const int32_t *ids;
+    const void *a, *b;
+    const float *scale;
+    int adapters, slices, rank, cols_in, cols_out;
+    int down;            // adapter rows of the first product: slices * rank
+    int first_col[5];    // of each slice, and the end
+    int first_group[4];  // of 64 columns
+    int groups, col_tiles;
+    const void *x, *y;
+    void *out;
+    int64_t xs, ys, os;
+    float *h;  // [splits][tokens][down]
+    int splits;
+    bool tall;  // 32 tokens a tile of the first product, else 16
+};
+void adapter_plan(AdapterArgs &a);
+int64_t adapter_tiles(const AdapterArgs &a, int rows);
+int64_t adapter_groups(const AdapterArgs &a);
+hipError_t launch_adapters(const AdapterArgs &a, bool f16, bool y_f32, hipStream_t st);
+
 // ---- device helpers
 
 template <class T> struct BlockType;

@@ -144,6 +144,45 @@ cfz_status cfz_rotate(int32_t count, const cfz_rotate_rows *tensors, cfz_kv8_dty
                       const int32_t *starts, const cfz_kv8_rotation *rotation, int32_t normed,
                       float eps, void *hip_stream);
 
+/* Low-rank adapters of one projection, to be added beside it for several requests at once.
+ *   a: [adapters][slices * rank][cols_in], b: [adapters][cols_out][rank], both of `dtype` (BF16 or
+ *   F16), scale: [adapters] fp32 or NULL (1).
+ * The projection's columns are dealt out to 1 .. 4 slices (query, key and value of one fused
+ * projection) of slice_cols[i] columns each, multiples of 16, cols_out in all; slice i's columns
+ * are met by adapter rows i * rank .. (i + 1) * rank - 1 of a.  rank: a multiple of 8, 8 .. 128,
+ * slices * rank at most 256 (lower ranks: zeros).  cols_in: a multiple of 8, 8 .. 2^20;
+ * cols_out at most 2^20; 1 <= adapters <= 2^20. */
+typedef struct {
+    int32_t adapters;
+    int32_t slices;
+    int32_t rank;
+    int32_t cols_in;
+    int32_t slice_cols[4];
+    int32_t dtype;
+    const void *a;
+    const void *b;
+    const float *scale;
+} cfz_adapters;
+
+/* out = y + scale_a (x a^T) b^T for the token rows offsets[b] .. offsets[b + 1] - 1 of sequence b, with
+ * adapter ids[b] (outside of 0 .. adapters - 1: none, out = y).  x: rows of `dtype`; y and out: rows
+ * of y_dtype (dtype or F32); row strides in elements, multiples of 16 bytes.  out may be y with the same
+ * stride; other overlaps are not allowed.  Rows of no sequence, and rows past a sequence's first
+ * max_rows, are neither read nor written.  The products accumulate in fp32; x a^T enters the second one as the sum of
+ * two numbers of `dtype` (off by 2^-16 of itself for BF16, 2^-21 of its row's largest value for F16).
+ * Results do not depend on the run.
+ * workspace: cfz_adapters_workspace_bytes(...) bytes, 256-byte aligned, overwritten; calls that may
+ * run at the same time need one each.
+ * Errors: CFZ_ERR_NULL, CFZ_ERR_SHAPE, CFZ_ERR_UNSUPPORTED, CFZ_ERR_ALIGN, CFZ_ERR_WORKSPACE,
+ * CFZ_ERR_HIP. */
+cfz_status cfz_adapters_add(const cfz_adapters *adapters, int64_t tokens, int32_t batch,
+                            const int32_t *offsets, const int32_t *ids, int64_t max_rows,
+                            const void *x, int64_t x_stride, const void *y, int64_t y_stride,
+                            void *out, int64_t out_stride, int32_t y_dtype, void *workspace,
+                            size_t ws_bytes, void *hip_stream);
+/* 0 if none is needed or the arguments are invalid. */
+size_t cfz_adapters_workspace_bytes(const cfz_adapters *adapters, int64_t tokens, int32_t batch);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,5 +1,5 @@
-"""Plain 64-bit models (numpy, no GPU) of cfz_residual_norm, cfz_rotation_table and cfz_rotate, and
-bounds on how far fp32 arithmetic may be from them.
+"""Plain 64-bit models (numpy, no GPU) of cfz_residual_norm, cfz_rotation_table, cfz_rotate and
+cfz_adapters_add, and bounds on how far fp32 arithmetic may be from them.
 
 Bounds count roundings, U = 2^-24 each (half a step of fp32).  A sum over a row adds at most 64 values
 in a thread and then 8 levels across threads: within 72 U of the sum of magnitudes, 75 with the
@@ -97,3 +97,27 @@ def rotate(x, cos, sin, interleaved, normed=False, eps=0.0, weight=None):
         e[..., one] = np.abs(c) * ea + np.abs(s) * eb + 2 * U * (np.abs(a * c) + np.abs(b * s))
         e[..., two] = np.abs(s) * ea + np.abs(c) * eb + 2 * U * (np.abs(a * s) + np.abs(b * c))
     return y, e
+
+
+def adapters_add(x, y, a, b, scale, slices, half):
+    """Rows of one sequence with adapter a [slices * rank, cols_in], b [cols_out, rank] in 16 bits:
+    (y + scale (x a^T) b^T, bound of its error before the rounding of the result).
+
+    The products of 16-bit numbers are exact in fp32, so that a sum of n of them in any order is within 2 n U
+    of the sum of magnitudes (two roundings a term); h = scale x a^T takes three more roundings
+    and is then split: `half` ("bf16": 2^-16 of itself, "f16": 2^-21 of its row's largest)."""
+    x, y, a, b = (np.asarray(t, np.float64) for t in (x, y, a, b))
+    rank = b.shape[1]
+    h = scale * (x @ a.T)
+    e = abs(scale) * 2 * (x.shape[1] + 16) * U * (np.abs(x) @ np.abs(a).T) + 3 * U * np.abs(h)
+    out, off, at = y.copy(), np.zeros_like(y), 0
+    for i, n in enumerate(slices):
+        r, c = slice(i * rank, (i + 1) * rank), slice(at, at + n)
+        at += n
+        top = np.abs(h[:, r]) if half == "bf16" else np.abs(h[:, r]).max(-1, keepdims=True)
+        eh = e[:, r] + (2.0 ** -16 if half == "bf16" else 2.0 ** -21) * (top + e[:, r])
+        w = np.abs(b[c]).T
+        out[:, c] += h[:, r] @ b[c].T
+        off[:, c] = eh @ w + 4 * (rank + 8) * U * ((np.abs(h[:, r]) + eh) @ w) + \
+            U * np.abs(out[:, c])
+    return out, off

@@ -68,6 +68,8 @@ _SIGNATURES = {
     "cfz_rotation_table": ([C.POINTER(cfz_rotation_angles), _i64, _p, _p, _p, _p], _i32),
     "cfz_rotate": ([_i32, C.POINTER(cfz_rotate_rows), _i32, _i32, _i64, _i32, _p, _p,
                     C.POINTER(cfz_kv8_rotation), _i32, _f32, _p], _i32),
+    "cfz_adapters_a_bytes": ([C.POINTER(cfz_adapters)], C.c_size_t),
+    "cfz_adapters_put": ([C.POINTER(cfz_adapters), _i32, _i32, _p, _p], _i32),
     "cfz_adapters_add": ([C.POINTER(cfz_adapters), _i64, _i32, _p, _p, _i64, _p, _i64, _p, _i64,
                           _p, _i64, _i32, _p, C.c_size_t, _p], _i32),
     "cfz_adapters_workspace_bytes": ([C.POINTER(cfz_adapters), _i64, _i32], C.c_size_t),
@@ -82,6 +84,12 @@ def _device(t, what):
     if not t.is_cuda:
         raise ValueError(f"{what}: libcfz takes device tensors")
     return t.device
+
+
+def _as_stream(stream, device):
+    if isinstance(stream, int):
+        return torch.cuda.ExternalStream(stream, device)
+    return torch.cuda.current_stream(device) if stream is None else stream
 
 
 def _matrix(t, shape, dtypes, device, what):
@@ -304,13 +312,16 @@ def rotate(tensors, rotation, offsets=None, starts=None, weights=None, eps=1e-6,
 
 
 class Adapters:
-    """Low-rank adapters of one projection: ``a`` [adapters, slices * rank, cols_in] and ``b``
-    [adapters, cols_out, rank], bf16 or fp16, ``scale`` [adapters] fp32 or None (1).  ``slices``: how
+    """Low-rank adapters of one projection, from ``a`` [adapters, slices * rank, cols_in] and ``b``
+    [adapters, cols_out, rank], bf16 or fp16, and ``scale`` [adapters] fp32 or None (1).  ``slices``: how
     many parts of equal width the projection's columns have, or a list of their widths (query,
     key and value of one fused projection); part i is met by rows i * rank .. (i + 1) * rank - 1 of a.
-    rank: a multiple of 8 up to 128; adapters of a lower one are filled up with zeros."""
+    rank: a multiple of 8 up to 128; adapters of a lower one are filled up with zeros.
 
-    def __init__(self, a, b, scale=None, slices=1):
+    a is copied into the layout that the kernels read; b and scale are used as they are.  ``put``
+    replaces adapters in place (a pool that requests bring theirs to)."""
+
+    def __init__(self, a, b, scale=None, slices=1, stream=None):
         self.device = _device(a, "a")
         if a.dim() != 3 or b.dim() != 3 or a.dtype not in (torch.bfloat16, torch.float16):
             raise ValueError(f"a: {a.dtype} {tuple(a.shape)}, b: {tuple(b.shape)}, expected bf16 or "
@@ -323,22 +334,46 @@ class Adapters:
         slices = list(slices)
         if not 1 <= len(slices) <= 4 or sum(slices) != cols_out or min(slices) < 1:
             raise ValueError(f"slices = {slices} of {cols_out} columns")
-        if a.shape[:2] != (count, len(slices) * rank):
-            raise ValueError(f"a: shape {tuple(a.shape)}, expected [{count}, {len(slices) * rank}, "
-                             "cols_in]")
-        if b.dtype != a.dtype or b.device != self.device or not a.is_contiguous() or \
-                not b.is_contiguous():
-            raise ValueError("a and b: must be contiguous, of one type and on one device")
+        if b.dtype != a.dtype or b.device != self.device or not b.is_contiguous():
+            raise ValueError("b: must be contiguous, of a's type and on its device")
         if scale is not None and (scale.dtype != torch.float32 or scale.shape != (count,) or
                                   scale.device != self.device or not scale.is_contiguous()):
             raise ValueError(f"scale: expected a contiguous fp32 tensor of {count} values")
         _fit(32, adapters=count, rank=rank, cols_in=a.shape[2], cols_out=cols_out)
-        self.a, self.b, self.scale, self.slices = a, b, scale, slices
+        self.b, self.scale, self.slices, self.count = b, scale, slices, count
         self.rank, self.cols_in, self.cols_out, self.dtype = rank, a.shape[2], cols_out, a.dtype
         self.desc = cfz_adapters(count, len(slices), rank, self.cols_in, (C.c_int32 * 4)(*slices),
-                                 _REALS[a.dtype], a.data_ptr(), b.data_ptr(),
+                                 _REALS[a.dtype], None, b.data_ptr(),
                                  None if scale is None else scale.data_ptr())
         self._ref = C.byref(self.desc)
+        need = _lib.cfz_adapters_a_bytes(self._ref)
+        if need == 0:  # (the call below says why)
+            _queue(_lib.cfz_adapters_put, self.device, stream, self._ref, 0, 0, None)
+        self.a = _empty_on(self.device, stream, need, torch.uint8)
+        self.desc.a = self.a.data_ptr()
+        self.put(0, a, stream=stream)
+
+    def put(self, first, a, b=None, scale=None, stream=None):
+        """Adapters first .. first + n - 1 become ``a`` [n, slices * rank, cols_in], with ``b`` [n,
+        cols_out, rank] and ``scale`` (n values) copied into theirs where given."""
+        shape = (a.shape[0], len(self.slices) * self.rank, self.cols_in)
+        if a.dtype != self.dtype or a.shape != shape or a.device != self.device or \
+                not a.is_contiguous():
+            raise ValueError(f"a: {a.dtype} {tuple(a.shape)}, expected a contiguous {self.dtype} tensor "
+                             f"{shape} on {self.device}")
+        n = shape[0]
+        if not 0 <= first <= self.count - n:
+            raise ValueError(f"adapters {first} .. {first + n - 1} of {self.count}")
+        if b is not None and (b.shape != (n, self.cols_out, self.rank) or b.dtype != self.dtype):
+            raise ValueError(f"b: {b.dtype} {tuple(b.shape)}, expected {self.dtype} "
+                             f"{(n, self.cols_out, self.rank)}")
+        if scale is not None and (self.scale is None or scale.shape != (n,)):
+            raise ValueError(f"scale: shape {tuple(scale.shape)}, expected ({n},) beside held scales")
+        _queue(_lib.cfz_adapters_put, self.device, stream, self._ref, first, n, a.data_ptr())
+        for held, new in ((self.b, b), (self.scale, scale)):
+            if new is not None:
+                with torch.cuda.stream(_as_stream(stream, self.device)):
+                    held[first:first + n].copy_(new)
 
     def add(self, x, y, ids, offsets, max_rows, out=None, workspace=None, stream=None):
         """y + scale * (x a^T) b^T for each sequence's own adapter: x [tokens, cols_in], y [tokens,

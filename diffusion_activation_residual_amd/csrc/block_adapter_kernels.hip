@@ -9,6 +9,8 @@
 // host needs no list.
 #include "block_internal.h"
 
+#include <type_traits>
+
 namespace cfz {
 namespace {
 
@@ -36,31 +38,44 @@ template <> struct Mfma<_Float16> {
     static __device__ inline float value(uint16_t u) { return (float)__builtin_bit_cast(_Float16, u); }
 };
 
-// The rows of a tile: row0 .. row0 + n - 1 of the call, n <= R.  False: the tile holds nothing.
+// The rows of a tile: row0 .. row0 + n - 1 of the call, n <= R, and their adapter (-1: none).  False: the tile
+// holds nothing.  Up to 63 sequences are looked at together, with one load each.
 template <int R>
-__device__ inline bool find_tile(const AdapterArgs &a, int tile, int &seq, int64_t &row0, int &n)
+__device__ inline bool find_tile(const AdapterArgs &a, int tile, int64_t &row0, int &n, int &id)
 {
     const int lane = threadIdx.x & 63;
     const int64_t t = a.rows.tokens;
-    auto at = [&](int b) {
-        const int64_t o = a.rows.off[b];
-        return o < 0 ? 0 : (o > t ? t : o);
-    };
-    int lo = 0, left = a.rows.batch;  // the last sequence whose first tile is at or before this one
-    while (left > 1) {
-        const int step = (left + 63) / 64;
-        const int b = lo + lane * step;
-        const bool before = lane * step < left && at(b) / R + b <= tile;
-        const uint64_t votes = __ballot(before);
-        const int k = votes ? 63 - __clzll(votes) : 0;
-        left = left - k * step < step ? left - k * step : step;
-        lo += k * step;
+    auto clamp = [&](int64_t o) { return o < 0 ? 0 : (o > t ? t : o); };
+    int seq = 0;  // the last sequence whose first tile is at or before this one
+    int64_t first, end;
+    if (a.rows.batch < 64) {
+        const int b = lane < a.rows.batch ? lane : a.rows.batch;
+        const int o = (int)clamp(a.rows.off[b]);
+        const int ids = a.ids[b < a.rows.batch ? b : 0];
+        const uint64_t votes = __ballot(lane < a.rows.batch && o / R + lane <= tile);
+        seq = votes ? 63 - __clzll(votes) : 0;
+        first = __builtin_amdgcn_readlane(o, seq);
+        end = __builtin_amdgcn_readlane(o, seq + 1);
+        id = __builtin_amdgcn_readlane(ids, seq);
+    } else {
+        int left = a.rows.batch;
+        while (left > 1) {
+            const int step = (left + 63) / 64;
+            const int b = seq + lane * step;
+            const bool before = lane * step < left && clamp(a.rows.off[b]) / R + b <= tile;
+            const uint64_t votes = __ballot(before);
+            const int k = votes ? 63 - __clzll(votes) : 0;
+            left = left - k * step < step ? left - k * step : step;
+            seq += k * step;
+        }
+        first = clamp(a.rows.off[seq]);
+        end = clamp(a.rows.off[seq + 1]);
+        id = __builtin_amdgcn_readfirstlane(a.ids[seq]);
     }
-    seq = lo;
-    const int64_t first = at(lo);
-    int64_t end = at(lo + 1);
+    if (id < 0 || id >= a.adapters)
+        id = -1;
     end = end - first > a.max_rows ? first + a.max_rows : end;
-    const int64_t mine = tile - (first / R + lo);
+    const int64_t mine = tile - (first / R + seq);
     row0 = first + mine * R;
     if (mine < 0 || row0 >= end)
         return false;
@@ -68,235 +83,386 @@ __device__ inline bool find_tile(const AdapterArgs &a, int tile, int &seq, int64
     return true;
 }
 
-__device__ inline uint4 load16(const void *p, bool yes)
+// Orders a wave's own writes to LDS before its reads of what other lanes wrote, and the other way round.
+__device__ inline void wave_sync()
 {
-    return yes ? *(const uint4 *)p : make_uint4(0, 0, 0, 0);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 }
 
-// h of TM x 16 tokens for NB x 16 adapter rows, over one of a.splits runs of the columns.  The four
-// waves take every fourth chunk of 64 columns, and their sums are added in LDS.  A lane holds 16
-// neighbouring columns of a row, 32 bytes: the two matrix instructions of a chunk take 8 each, the
-// same ones of either operand, so that four lanes read 128 bytes of a row.
-template <class T, int NB, int TM>
-__global__ __launch_bounds__(256) void adapter_down_kernel(AdapterArgs a)
+// Steps of 32 columns: whole groups of four, in which the first product goes.
+__host__ __device__ inline int down_steps(const AdapterArgs &a) { return (a.cols_in + 127) / 128 * 4; }
+
+// Lays out A for the matrix instructions: 16 rows x 32 columns side by side, lane 16 q + m's 8 columns 8 q ..
+// 8 q + 7 of row m, zeros past either end.  A thread a piece of 16 bytes.
+__global__ __launch_bounds__(256) void adapter_put_kernel(AdapterArgs a, const uint16_t *rows, int first,
+                                                          int64_t pieces)
 {
-    __shared__ f32x4 part[3][NB * TM][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int tile = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
-    int seq, n;
-    int64_t row0;
-    if (!find_tile<16 * TM>(a, tile, seq, row0, n))
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= pieces)
         return;
-    const int id = a.ids[seq];
-    if (id < 0 || id >= a.adapters)
+    const int steps = down_steps(a), blocks = (a.down + 15) / 16;
+    const int lane = (int)(i % 64);
+    const int64_t at = i / 64;
+    const int step = (int)(at % steps), block = (int)(at / steps % blocks);
+    const int64_t adapter = at / steps / blocks;
+    const int row = block * 16 + (lane & 15), col = step * 32 + (lane >> 4) * 8;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (row < a.down && col < a.cols_in)
+        v = *(const uint4 *)(rows + (adapter * a.down + row) * a.cols_in + col);
+    ((uint4 *)a.a)[(int64_t)first * blocks * steps * 64 + i] = v;
+}
+
+// h = scale x A^T of TM x 16 tokens for NB x 16 adapter rows.  W waves take a run of the columns each, four
+// steps of 32 at a time, and their sums are added in LDS, half of the waves at a time.  The matrix
+// instructions' rows are A's and their columns the tokens.  An operand's lanes are 16 different rows: read
+// so from rows in memory, each lane's 16 bytes are an access of their own, and the first-level cache gives
+// 16 bytes a clock.  So A is laid out once as the instructions take it, and of x four neighbouring
+// lanes read 64 bytes of a row, which the wave turns round in LDS, a row's four pieces shifted by its
+// number so that no bank is met twice.  Four steps of x and two of A are under way.  Tiles start their runs at
+// different places, so that rows a power of two apart are not all read from the same channels.
+//
+// h leaves as the sum of two 16-bit numbers, the operands of the second product: that leaves 2^-16 of it
+// (bf16) or 2^-21 of its row's largest in a slice (fp16, after a power of two that brings the row into
+// range), where the rounding of a result in these types leaves 2^-8 and 2^-11.
+template <class T, int NB, int TM, int W>
+__global__ __launch_bounds__(64 * W) void adapter_down_kernel(AdapterArgs a)
+{
+    constexpr int kBlocks = NB * TM, kHalf = W / 2;
+    constexpr int kRow = NB * 16 + 4;  // of the sums in LDS
+    __shared__ union {
+        uint4 turn[W][TM][64];
+        f32x4 part[kHalf][kBlocks][64];
+        float sum[TM * 16][kRow];
+    } s;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int n, id;
+    int64_t row0;
+    if (!find_tile<16 * TM>(a, blockIdx.x, row0, n, id) || id < 0)
         return;
     const int m = lane & 15, q = lane >> 4;
+    const int r = lane >> 2, piece = lane & 3;  // row of a block and its 16 bytes, as they are read
     const T *x[TM];
 #pragma unroll
-    for (int t = 0; t < TM; ++t) {
+    for (int t = 0; t < TM; ++t)
         // (rows past the tile's end repeat the last one: their sums are not kept)
-        const int r = t * 16 + m < n ? t * 16 + m : n - 1;
-        x[t] = (const T *)a.x + (row0 + r) * a.xs + q * 16;
-    }
-    const T *w[NB];
-#pragma unroll
-    for (int j = 0; j < NB; ++j) {
-        const int r = j * 16 + m < a.down ? j * 16 + m : a.down - 1;
-        w[j] = (const T *)a.a + ((int64_t)id * a.down + r) * a.cols_in + q * 16;
-    }
+        x[t] = (const T *)a.x + (row0 + (t * 16 + r < n ? t * 16 + r : n - 1)) * a.xs + piece * 8;
+    const int steps = down_steps(a), blocks = (a.down + 15) / 16;
+    const uint4 *w = (const uint4 *)a.a + (int64_t)id * blocks * steps * 64;
+    uint4 *put = &s.turn[wave][0][r * 4 + (piece ^ ((r >> 2) & 3))];
+    const uint4 *get = &s.turn[wave][0][m * 4 + (q ^ ((m >> 2) & 3))];
     f32x4 acc[TM][NB];
 #pragma unroll
     for (int t = 0; t < TM; ++t)
 #pragma unroll
         for (int j = 0; j < NB; ++j)
             acc[t][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    const int chunks = (a.cols_in + 63) / 64;
-    const int c0 = (int)((int64_t)chunks * split / a.splits);
-    const int c1 = (int)((int64_t)chunks * (split + 1) / a.splits);
-    for (int c = c0 + wave; c < c1; c += 4) {
-        const int k = c * 64;
-        uint4 xv[TM][2], wv[NB][2];
+    // groups of four steps g0 .. g1 - 1, from one in their midst on and round
+    const int g0 = steps / 4 * wave / W, g1 = steps / 4 * (wave + 1) / W;
+    int step = 0;  // the one under way farthest ahead
+    uint4 xv[4][TM], wv[2][NB];
+    auto load_x = [&](int step, auto at) {
+        const int k = step * 32;
+        const bool in = k + piece * 8 < a.cols_in;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const bool in = k + q * 16 + i * 8 < a.cols_in;
+        for (int t = 0; t < TM; ++t)
+            xv[decltype(at)::value][t] = *(const uint4 *)(x[t] + (in ? k : -piece * 8));
+    };
+    auto load_a = [&](int step, auto at) {
+        // (a block past the last one repeats it: its sums are not kept)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+            wv[decltype(at)::value][j] =
+                (w + ((int64_t)(j < blocks ? j : blocks - 1) * steps + step) * 64)[lane];
+    };
+    auto multiply = [&](int step, auto xat, auto wat) {
+        // past the last column zeros
+        const uint32_t keep = step * 32 + piece * 8 < a.cols_in ? ~0u : 0u;
+#pragma unroll
+        for (int t = 0; t < TM; ++t) {
+            const uint4 v = xv[decltype(xat)::value][t];
+            put[t * 64] = make_uint4(v.x & keep, v.y & keep, v.z & keep, v.w & keep);
+        }
+        wave_sync();
+        uint4 xo[TM];
+#pragma unroll
+        for (int t = 0; t < TM; ++t)
+            xo[t] = get[t * 64];
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
 #pragma unroll
             for (int t = 0; t < TM; ++t)
-                xv[t][i] = load16(x[t] + k + i * 8, in);
-#pragma unroll
-            for (int j = 0; j < NB; ++j)
-                wv[j][i] = load16(w[j] + k + i * 8, in);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < NB; ++j)
-#pragma unroll
-                for (int t = 0; t < TM; ++t)
-                    acc[t][j] = Mfma<T>::mul(wv[j][i], xv[t][i], acc[t][j]);
+                acc[t][j] = Mfma<T>::mul(wv[decltype(wat)::value][j], xo[t], acc[t][j]);
+        wave_sync();
+    };
+    constexpr std::integral_constant<int, 0> i0{};
+    constexpr std::integral_constant<int, 1> i1{};
+    constexpr std::integral_constant<int, 2> i2{};
+    constexpr std::integral_constant<int, 3> i3{};
+    if (g0 < g1) {
+        step = (g0 + blockIdx.x % (g1 - g0)) * 4;
+        load_x(step, i0);
+        load_a(step, i0);
+        load_x(step + 1, i1);
+        load_x(step + 2, i2);
     }
-    if (wave > 0) {
+    for (int g = g0; g < g1; ++g) {
+        // (past the last group the loads repeat the first: no load is under a condition)
+        const int next = step + 4 < g1 * 4 ? step + 4 : g0 * 4;
+        load_x(step + 3, i3);
+        load_a(step + 1, i1);
+        multiply(step, i0, i0);
+        load_x(next, i0);
+        load_a(step + 2, i0);
+        multiply(step + 1, i1, i1);
+        load_x(next + 1, i1);
+        load_a(step + 3, i1);
+        multiply(step + 2, i2, i0);
+        load_x(next + 2, i2);
+        load_a(next, i0);
+        multiply(step + 3, i3, i1);
+        step = next;
+    }
+    __syncthreads();
+    // the upper half's sums to the lower, then the lower half's to all
+    if (wave >= kHalf) {
 #pragma unroll
         for (int t = 0; t < TM; ++t)
 #pragma unroll
             for (int j = 0; j < NB; ++j)
-                part[wave - 1][t * NB + j][lane] = acc[t][j];
+                s.part[wave - kHalf][t * NB + j][lane] = acc[t][j];
     }
     __syncthreads();
-    if (wave > 0)
-        return;
-    float *h = a.h + (int64_t)split * a.rows.tokens * a.down;
+    if (wave < kHalf) {
 #pragma unroll
-    for (int t = 0; t < TM; ++t) {
+        for (int t = 0; t < TM; ++t)
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-            f32x4 s = acc[t][j];
+            for (int j = 0; j < NB; ++j)
+                s.part[wave][t * NB + j][lane] = acc[t][j] + s.part[wave][t * NB + j][lane];
+    }
+    __syncthreads();
+    constexpr int kMine = (kBlocks + W - 1) / W;
+    f32x4 sum[kMine];
+    const float scale = a.scale ? a.scale[id] : 1.0f;
 #pragma unroll
-            for (int i = 0; i < 3; ++i)
-                s += part[i][t * NB + j][lane];
-            // lane: token m, adapter rows 4 q .. 4 q + 3 of the block
-            const int r = j * 16 + q * 4;
-            if (t * 16 + m < n && r < a.down)
-                *(f32x4 *)(h + (row0 + t * 16 + m) * a.down + r) = s;
+    for (int i = 0; i < kMine; ++i) {
+        const int b = i * W + wave;
+        if (b < kBlocks) {
+            sum[i] = s.part[0][b][lane];
+#pragma unroll
+            for (int p = 1; p < kHalf; ++p)
+                sum[i] += s.part[p][b][lane];
+            sum[i] *= scale;
         }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const int b = i * W + wave;
+        // lane: token m, adapter rows 4 q .. 4 q + 3 of the block
+        if (b < kBlocks)
+            *(f32x4 *)&s.sum[b / NB * 16 + m][b % NB * 16 + q * 4] = sum[i];
+    }
+    __syncthreads();
+    const int units = a.down / 8;
+    for (int i = threadIdx.x; i < n * units; i += 64 * W) {
+        const int row = i / units, r = (i - row * units) * 8;
+        const float *v = &s.sum[row][r];
+        float f = 1.0f;
+        if constexpr (__is_same(T, _Float16)) {
+            const int slice = r / a.rank;
+            float top = 0.0f;
+            for (int k = slice * a.rank; k < (slice + 1) * a.rank; k += 4) {
+                const f32x4 u = *(const f32x4 *)&s.sum[row][k];
+                top = fmaxf(fmaxf(fmaxf(fabsf(u[0]), fabsf(u[1])), fmaxf(fabsf(u[2]), fabsf(u[3]))), top);
+            }
+            // a power of two that brings the largest into 1 .. 2 (0 and what is not finite: 1)
+            int e = (int)(__float_as_uint(top) >> 23) - 127;
+            e = e > -120 && e < 120 ? e : 0;
+            f = __uint_as_float((uint32_t)(127 - e) << 23);
+            if (r == slice * a.rank)
+                a.back[(row0 + row) * a.slices + slice] = __uint_as_float((uint32_t)(127 + e) << 23);
+        }
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint16_t a0[2], a1[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const float y = v[2 * k + u] * f;
+                a0[u] = Mfma<T>::bits(y);
+                const float rest = y - Mfma<T>::value(a0[u]);
+                a1[u] = Mfma<T>::bits(rest == rest ? rest : 0.0f);  // (infinity has no rest)
+            }
+            hi[k] = (uint32_t)a0[0] | (uint32_t)a0[1] << 16;
+            lo[k] = (uint32_t)a1[0] | (uint32_t)a1[1] << 16;
+        }
+        const int64_t at = (row0 + row) * a.down + r;
+        *(uint4 *)(a.hi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *(uint4 *)(a.lo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
 }
 
-// 64 columns a wave, four waves side by side, the tile's tokens 16 at a time.  Columns are the matrix
-// instructions' rows, dealt out so that a lane ends up with 16 neighbouring ones of a token:
-// y is read and out written in vectors of 16 bytes.  B stays in registers over the tile.
-//
-// h enters the second product as the sum of two 16-bit numbers, which leaves 2^-16 of it (bf16) or
-// 2^-21 of its row's largest (fp16, after a power of two that brings the row into range), where
-// the rounding of a result in these types leaves 2^-8 and 2^-11.
+// out = y + h B^T: 16 CB columns a wave, four waves side by side in a slice, the tile's tokens 16 at a time,
+// with the tile's y under way before the rest.  Tokens are the matrix instructions' rows and columns their
+// columns, dealt out so that a lane ends up with CB neighbouring ones and 16 lanes with a run of a row:
+// y is read and out written in whole runs.  B stays in registers over the tile.  The tile's h
+// lies in LDS, turned as x in the first product.
 constexpr int kUpRows = 64;
 
-template <class T, class Y, int KS>
+// CB values of a row as they lie in memory, until they are needed as numbers.
+template <class Y, int CB> struct RawRow {
+    static constexpr int kBytes = CB * (int)sizeof(Y), kPiece = kBytes < 16 ? kBytes : 16;
+    struct alignas(kPiece) Piece { Y v[kPiece / sizeof(Y)]; } p[kBytes / kPiece];
+    __device__ inline void load(const Y *y)
+    {
+#pragma unroll
+        for (int i = 0; i < kBytes / kPiece; ++i)
+            p[i] = ((const Piece *)y)[i];
+    }
+    __device__ inline void get(float (&o)[CB]) const
+    {
+        constexpr int E = kPiece / sizeof(Y);
+#pragma unroll
+        for (int i = 0; i < CB; ++i)
+            o[i] = BlockType<Y>::get(p[i / E].v[i % E]);
+    }
+};
+
+template <class T, class Y, int KS, int CB>
 __global__ __launch_bounds__(256) void adapter_up_kernel(AdapterArgs a)
 {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int tile = blockIdx.x / a.col_tiles;
-    const int group = (int)(blockIdx.x % a.col_tiles) * 4 + wave;
-    int seq, n;
+    constexpr int kAhead = sizeof(Y) == 4 ? 2 : 4;  // blocks of 16 tokens under way together
+    constexpr int RU = KS == 1 ? 4 : (KS == 2 ? 8 : 16);  // pieces of 16 bytes of a row in LDS
+    __shared__ uint4 hs[2][kUpRows * RU];
+    __shared__ alignas(16) float back[kUpRows];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tile = blockIdx.x / a.col_tiles, part = blockIdx.x % a.col_tiles;
+    int n, id;
     int64_t row0;
-    if (!find_tile<kUpRows>(a, tile, seq, row0, n))
+    if (!find_tile<kUpRows>(a, tile, row0, n, id))
         return;
-    const int id = a.ids[seq];
-    const bool some = id >= 0 && id < a.adapters;
-    if (group >= a.groups || (!some && a.y == a.out))
+    const bool some = id >= 0;
+    if (!some && a.y == a.out)
         return;
     int slice = 0;
-    while (slice + 1 < a.slices && group >= a.first_group[slice + 1])
+    while (slice + 1 < a.slices && part >= a.first_tile[slice + 1])
         ++slice;
     const int m = lane & 15, q = lane >> 4;
-    const int col0 = a.first_col[slice] + (group - a.first_group[slice]) * 64;
+    const int col0 = a.first_col[slice] + ((part - a.first_tile[slice]) * 4 + wave) * 16 * CB;
     const int left = a.first_col[slice + 1] - col0;  // columns of the slice from here on
-    const bool mine = q * 16 < left;
-    uint4 w[4][KS];
+    const bool mine = m * CB < left;
+    // Where some row or column is missing, its loads repeat another: a load under a condition of its own
+    // waits for the one before.  Whole blocks, almost all of them, store without conditions.
+    const Y *y = (const Y *)a.y + row0 * a.ys + (left > 0 ? col0 : 0) + (mine ? m * CB : 0);
+    RawRow<Y, CB> v[kAhead][4];
+    auto load = [&](int t0) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = t0 + u * 16 + q * 4 + i;
+                v[u][i].load(y + (t < n ? t : n - 1) * a.ys);
+            }
+    };
+    load(0);
+    uint4 w[CB][KS];
     if (some) {
+        const T *b = (const T *)a.b + ((int64_t)id * a.cols_out + (left > 0 ? col0 : 0)) * a.rank;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int c = (m >> 2) * 16 + j * 4 + (m & 3);
-            const T *b = (const T *)a.b + ((int64_t)id * a.cols_out + col0 + c) * a.rank + q * 8;
+        for (int j = 0; j < CB; ++j)
 #pragma unroll
-            for (int s = 0; s < KS; ++s)
-                w[j][s] = load16(b + s * 32, c < left && s * 32 + q * 8 < a.rank);
+            for (int s = 0; s < KS; ++s) {
+                const bool in = mine && s * 32 + q * 8 < a.rank;
+                const uint4 got = *(const uint4 *)(b + (in ? (m * CB + j) * a.rank + s * 32 + q * 8 : 0));
+                const uint32_t keep = in ? ~0u : 0u;  // (a choice would become a branch around the load)
+                w[j][s] = make_uint4(got.x & keep, got.y & keep, got.z & keep, got.w & keep);
+            }
+        constexpr int kHere = kUpRows * KS * 4 / 256;
+        const int units = a.rank / 8;
+        uint4 h[2][kHere];
+#pragma unroll
+        for (int i = 0; i < kHere; ++i) {
+            const int at = threadIdx.x + i * 256, row = at / (KS * 4), u = at - row * (KS * 4);
+            const int64_t from =
+                (row0 + (row < n ? row : 0)) * a.down + slice * a.rank + (u < units ? u * 8 : 0);
+            h[0][i] = *(const uint4 *)(a.hi + from);
+            h[1][i] = *(const uint4 *)(a.lo + from);
         }
+#pragma unroll
+        for (int i = 0; i < kHere; ++i) {
+            const int at = threadIdx.x + i * 256, row = at / (KS * 4), u = at - row * (KS * 4);
+            const bool in = row < n && u < units;
+            const int to = row * RU + (u ^ (row / (16 / RU) % RU));
+            hs[0][to] = in ? h[0][i] : make_uint4(0, 0, 0, 0);
+            hs[1][to] = in ? h[1][i] : make_uint4(0, 0, 0, 0);
+        }
+        if (__is_same(T, _Float16) && threadIdx.x < kUpRows)
+            back[threadIdx.x] =
+                (int)threadIdx.x < n ? a.back[(row0 + threadIdx.x) * a.slices + slice] : 1.0f;
+        __syncthreads();
     }
-    const float scale = some && a.scale ? a.scale[id] : 1.0f;
-    const float *h = a.h + slice * a.rank + q * 8;
-    for (int t = 0; t < n; t += 16) {
-        const bool in = t + m < n;
-        const int64_t row = row0 + (in ? t + m : n - 1);
-        const Y *y = (const Y *)a.y + row * a.ys + col0 + q * 16;
-        float v[16];
-        if (mine)
-            load_n(y, v);
-        f32x4 acc[4];
+    if (left <= 0)
+        return;
+    const bool whole = left >= 16 * CB;
+    Y *out = (Y *)a.out + row0 * a.os + col0 + m * CB;
+    for (int t0 = 0; t0 < n; t0 += 16 * kAhead) {
+        if (t0 > 0)
+            load(t0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        float back = 1.0f;
-        if (some) {
-            float u[KS][8];
-            float top = 0.0f;
+        for (int u = 0; u < kAhead; ++u) {
+            f32x4 acc[CB];
 #pragma unroll
-            for (int s = 0; s < KS; ++s) {
+            for (int j = 0; j < CB; ++j)
+                acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            f32x4 f = {1.0f, 1.0f, 1.0f, 1.0f};
+            if (some) {
+                // (rows past the last one: zeros up to the tile's end)
+                const int row = t0 + u * 16 + m;
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    u[s][i] = 0.0f;
-                if (s * 32 + q * 8 < a.rank) {
-                    for (int p = 0; p < a.splits; ++p) {
-                        float f[8];
-                        load_n(h + (p * a.rows.tokens + row) * a.down + s * 32, f);
+                for (int s = 0; s < KS; ++s) {
+                    const int at = row * RU + ((s * 4 + q) ^ (row / (16 / RU) % RU));
+                    const uint4 hi = hs[0][at], lo = hs[1][at];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            u[s][i] += f[i];
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        u[s][i] *= scale;
-                        top = fmaxf(top, fabsf(u[s][i]));
+                    for (int j = 0; j < CB; ++j) {
+                        acc[j] = Mfma<T>::mul(lo, w[j][s], acc[j]);
+                        acc[j] = Mfma<T>::mul(hi, w[j][s], acc[j]);
                     }
                 }
+                if (__is_same(T, _Float16))
+                    f = *(const f32x4 *)&back[t0 + u * 16 + q * 4];
             }
-            if (sizeof(_Float16) == sizeof(T) && __is_same(T, _Float16)) {
-                top = fmaxf(top, __shfl_xor(top, 16));
-                top = fmaxf(top, __shfl_xor(top, 32));
-                // a power of two that brings the row's largest into 1 .. 2 (0 and what is not finite: 1)
-                const int e = (int)(__float_as_uint(top) >> 23) - 127;
-                const bool ok = e > -120 && e < 120;
-                const float f = __uint_as_float((uint32_t)(127 - (ok ? e : 0)) << 23);
-                back = __uint_as_float((uint32_t)(127 + (ok ? e : 0)) << 23);
+            // lane: token 4 q + i, columns CB m + j
+            float o[4][CB];
 #pragma unroll
-                for (int s = 0; s < KS; ++s)
+            for (int i = 0; i < 4; ++i) {
+                v[u][i].get(o[i]);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        u[s][i] *= f;
+                for (int j = 0; j < CB; ++j)
+                    o[i][j] = fmaf(acc[j][i], f[i], o[i][j]);
             }
-#pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint16_t a0[2], a1[2];
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float f = u[s][2 * i + k];
-                        a0[k] = Mfma<T>::bits(f);
-                        const float rest = f - Mfma<T>::value(a0[k]);
-                        a1[k] = Mfma<T>::bits(rest == rest ? rest : 0.0f);
-                    }
-                    hi[i] = (uint32_t)a0[0] | (uint32_t)a0[1] << 16;
-                    lo[i] = (uint32_t)a1[0] | (uint32_t)a1[1] << 16;
-                }
-                const uint4 hv = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                const uint4 lv = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    acc[j] = Mfma<T>::mul(w[j][s], lv, acc[j]);
-                    acc[j] = Mfma<T>::mul(w[j][s], hv, acc[j]);
-                }
-            }
-        }
-        if (mine && in) {
-            // lane: token m, columns 16 q + 4 j + i
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
+            const int t = t0 + u * 16 + q * 4;
+            if (whole && t0 + u * 16 + 16 <= n) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    v[4 * j + i] = fmaf(acc[j][i], back, v[4 * j + i]);
-            store_n((Y *)a.out + row * a.os + col0 + q * 16, v);
+                    store_n(out + (t + i) * a.os, o[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (mine && t + i < n)
+                        store_n(out + (t + i) * a.os, o[i]);
+            }
         }
     }
 }
 
-template <class T, int TM> hipError_t down_as(const AdapterArgs &a, hipStream_t st)
+template <class T, int TM, int W> hipError_t down_as(const AdapterArgs &a, hipStream_t st)
 {
-    const dim3 grid((unsigned)(adapter_tiles(a, 16 * TM) * a.splits));
+    const dim3 grid((unsigned)adapter_tiles(a, 16 * TM));
     const int nb = (a.down + 15) / 16;
 #define CFZ_DOWN_CASE(NB)                                                                          \
     if (nb <= NB) {                                                                                \
-        adapter_down_kernel<T, NB, TM><<<grid, 256, 0, st>>>(a);                                    \
+        adapter_down_kernel<T, NB, TM, W><<<grid, 64 * W, 0, st>>>(a);                              \
         return hipGetLastError();                                                                  \
     }
     CFZ_DOWN_CASE(1)
@@ -316,17 +482,17 @@ template <class T, class Y> hipError_t up_as(const AdapterArgs &a, hipStream_t s
 {
     const dim3 grid((unsigned)(adapter_tiles(a, kUpRows) * a.col_tiles));
     switch ((a.rank + 31) / 32) {
-    case 1: adapter_up_kernel<T, Y, 1><<<grid, 256, 0, st>>>(a); break;
-    case 2: adapter_up_kernel<T, Y, 2><<<grid, 256, 0, st>>>(a); break;
-    case 3: adapter_up_kernel<T, Y, 3><<<grid, 256, 0, st>>>(a); break;
-    default: adapter_up_kernel<T, Y, 4><<<grid, 256, 0, st>>>(a); break;
+    case 1: adapter_up_kernel<T, Y, 1, 8><<<grid, 256, 0, st>>>(a); break;
+    case 2: adapter_up_kernel<T, Y, 2, 8><<<grid, 256, 0, st>>>(a); break;
+    case 3: adapter_up_kernel<T, Y, 3, 4><<<grid, 256, 0, st>>>(a); break;
+    default: adapter_up_kernel<T, Y, 4, 4><<<grid, 256, 0, st>>>(a); break;
     }
     return hipGetLastError();
 }
 
 template <class T> hipError_t add_as(const AdapterArgs &a, bool f32, hipStream_t st)
 {
-    const hipError_t e = a.tall ? down_as<T, 2>(a, st) : down_as<T, 1>(a, st);
+    const hipError_t e = a.tall ? down_as<T, 2, 4>(a, st) : down_as<T, 1, 8>(a, st);
     if (e != hipSuccess)
         return e;
     return f32 ? up_as<T, float>(a, st) : up_as<T, T>(a, st);
@@ -338,20 +504,39 @@ int64_t adapter_tiles(const AdapterArgs &a, int rows) { return a.rows.tokens / r
 
 int64_t adapter_groups(const AdapterArgs &a)
 {
-    const int64_t down = adapter_tiles(a, a.tall ? 32 : 16) * a.splits;
+    const int64_t down = adapter_tiles(a, a.tall ? 32 : 16);
     const int64_t up = adapter_tiles(a, kUpRows) * a.col_tiles;
     return down > up ? down : up;
 }
 
-// Tokens of a tile, and into how many runs the columns of x are cut: enough work-groups to fill the
-// card twice, with no run shorter than two chunks a wave.
+// 32 tokens a tile of the first product read A half as often as 16; 16, and twice the waves, where
+// sequences are too short to fill them, or the sums of more than 128 adapter rows would not fit the registers.
+//
+// The second product's work-groups take 512 columns of a slice, or 256 where the rank is over 64 (what B
+// takes of the registers).
 void adapter_plan(AdapterArgs &a)
 {
-    a.tall = a.rows.tokens >= 16 * (int64_t)a.rows.batch * 2 && a.down <= 128;
-    const int64_t tiles = adapter_tiles(a, a.tall ? 32 : 16) + 1;  // (there may be none)
-    const int64_t want = (512 + tiles - 1) / tiles, most = a.cols_in / 512;
-    a.splits = (int)(want < most ? want : most);
-    a.splits = a.splits < 1 ? 1 : a.splits;
+    const int cols = a.rank <= 64 ? 512 : 256;
+    a.col_tiles = 0;
+    for (int i = 0; i < a.slices; ++i) {
+        a.first_tile[i] = a.col_tiles;
+        a.col_tiles += (a.first_col[i + 1] - a.first_col[i] + cols - 1) / cols;
+    }
+    a.tall = a.rows.tokens >= 32 * (int64_t)a.rows.batch && a.down <= 128;
+}
+
+int64_t adapter_pieces(const AdapterArgs &a)
+{
+    return (int64_t)((a.down + 15) / 16) * down_steps(a) * 64;
+}
+
+hipError_t launch_adapters_put(const AdapterArgs &a, const void *rows, int first, int count,
+                               hipStream_t st)
+{
+    const int64_t pieces = adapter_pieces(a) * count;
+    adapter_put_kernel<<<dim3((unsigned)((pieces + 255) / 256)), 256, 0, st>>>(
+        a, (const uint16_t *)rows, first, pieces);
+    return hipGetLastError();
 }
 
 hipError_t launch_adapters(const AdapterArgs &a, bool f16, bool y_f32, hipStream_t st)

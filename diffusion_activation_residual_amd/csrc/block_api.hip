@@ -97,15 +97,13 @@ cfz_status check_adapters(const cfz_adapters *w, int64_t tokens, int32_t batch, 
                     w->rank, w->slices);
     if (w->cols_in < 8 || w->cols_in > 1 << 20 || w->cols_in % 8 != 0)
         return fail(CFZ_ERR_SHAPE, "cols_in = %d (a multiple of 8, 8 .. 2^20)", w->cols_in);
-    int cols = 0, groups = 0;
+    int cols = 0;
     for (int i = 0; i < w->slices; ++i) {
         const int c = w->slice_cols[i];
         if (c < 16 || c > 1 << 20 || c % 16 != 0)
             return fail(CFZ_ERR_SHAPE, "slice_cols[%d] = %d (a multiple of 16, 16 .. 2^20)", i, c);
         a->first_col[i] = cols;
-        a->first_group[i] = groups;
         cols += c;
-        groups += (c + 63) / 64;
     }
     if (cols > 1 << 20)
         return fail(CFZ_ERR_SHAPE, "%d columns (at most 2^20)", cols);
@@ -122,8 +120,6 @@ cfz_status check_adapters(const cfz_adapters *w, int64_t tokens, int32_t batch, 
     a->down = w->slices * w->rank;
     a->cols_in = w->cols_in;
     a->cols_out = cols;
-    a->groups = groups;
-    a->col_tiles = (groups + 3) / 4;
     cfz::adapter_plan(*a);
     return CFZ_OK;
 }
@@ -132,7 +128,7 @@ size_t adapters_bytes(const cfz::AdapterArgs &a)
 {
     if (a.rows.tokens == 0 || a.rows.batch == 0)
         return 0;
-    return (size_t)a.splits * a.rows.tokens * a.down * 4;
+    return (size_t)a.rows.tokens * (a.down + a.slices) * 4;
 }
 
 }  // namespace
@@ -305,6 +301,8 @@ cfz_status cfz_rotate(int32_t count, const cfz_rotate_rows *tensors, cfz_kv8_dty
         a.rot = rotation->rot_dim;
         a.interleaved = rotation->interleaved != 0;
     }
+    a.log2lanes = head_dim == 32 ? 2 : (head_dim == 64 ? 3 : (head_dim == 128 ? 4 : 5));
+    const int heads = (cfz::kRotateUnits * 64) >> a.log2lanes;  // a wave's
     for (int i = 0; i < count; ++i) {
         const cfz_rotate_rows &t = tensors[i];
         if (t.heads < 1 || t.heads > 1024)
@@ -320,24 +318,50 @@ cfz_status cfz_rotate(int32_t count, const cfz_rotate_rows *tensors, cfz_kv8_dty
             return fail(CFZ_ERR_ALIGN, "tensor %d: x and out must be 16-byte aligned", i);
         if (t.x == t.out && t.x_stride != t.out_stride)
             return fail(CFZ_ERR_SHAPE, "in place, the strides must be the same");
-        a.t[i] = cfz::RotateRows{t.x,        t.out,        t.weight,
-                                 t.x_stride, t.out_stride, t.weight_dtype == CFZ_KV8_F32, a.heads};
-        a.heads += t.heads;
+        a.t[i] = cfz::RotateRows{t.x,      t.out, t.weight, t.x_stride, t.out_stride,
+                                 t.weight_dtype == CFZ_KV8_F32, t.heads, a.parts};
+        a.parts += (t.heads + heads - 1) / heads;
     }
     a.count = count;
     a.dim = head_dim;
-    a.log2lanes = head_dim == 32 ? 2 : (head_dim == 64 ? 3 : (head_dim == 128 ? 4 : 5));
     a.starts = starts;
     a.normed = normed != 0;
     a.eps = eps;
-    const int heads = (cfz::kRotateUnits * 64) >> a.log2lanes;  // a wave's
-    a.parts = (a.heads + heads - 1) / heads;
     if (tokens == 0)
         return CFZ_OK;
     if (cfz::rotate_groups(a) >= cfz::kBlockMaxGroups)
         return fail(CFZ_ERR_SHAPE, "the call needs %lld work-groups (limit 2^23)",
                     (long long)cfz::rotate_groups(a));
     return hip_status(cfz::launch_rotate(a, dtype, (hipStream_t)hip_stream), "rotation launch");
+}
+
+size_t cfz_adapters_a_bytes(const cfz_adapters *adapters)
+{
+    cfz::AdapterArgs a;
+    if (check_adapters(adapters, 0, 0, &a) != CFZ_OK)
+        return 0;
+    return (size_t)cfz::adapter_pieces(a) * 16 * a.adapters;
+}
+
+cfz_status cfz_adapters_put(const cfz_adapters *w, int32_t first, int32_t count, const void *rows,
+                            void *hip_stream)
+{
+    cfz::AdapterArgs a;
+    CFZ_TRY(check_adapters(w, 0, 0, &a));
+    if (first < 0 || count < 0 || (int64_t)first + count > a.adapters)
+        return fail(CFZ_ERR_SHAPE, "adapters %d .. %lld of %d", first, (long long)first + count - 1,
+                    a.adapters);
+    if (cfz::adapter_pieces(a) * count / 256 >= cfz::kBlockMaxGroups)
+        return fail(CFZ_ERR_SHAPE, "more than 2^31 pieces of 16 bytes: fewer adapters a call");
+    if (count == 0)
+        return CFZ_OK;
+    if (!w->a || !rows)
+        return fail(CFZ_ERR_NULL, "a and rows are required");
+    if (!aligned(w->a, 16) || !aligned(rows, 16))
+        return fail(CFZ_ERR_ALIGN, "a and rows must be 16-byte aligned");
+    a.a = w->a;
+    return hip_status(cfz::launch_adapters_put(a, rows, first, count, (hipStream_t)hip_stream),
+                      "adapter layout launch");
 }
 
 size_t cfz_adapters_workspace_bytes(const cfz_adapters *adapters, int64_t tokens, int32_t batch)
@@ -393,7 +417,9 @@ cfz_status cfz_adapters_add(const cfz_adapters *w, int64_t tokens, int32_t batch
     a.xs = x_stride;
     a.ys = y_stride;
     a.os = out_stride;
-    a.h = (float *)workspace;
+    a.hi = (uint16_t *)workspace;
+    a.lo = a.hi + tokens * a.down;
+    a.back = (float *)(a.lo + tokens * a.down);
     return hip_status(cfz::launch_adapters(a, w->dtype == CFZ_KV8_F16, y_dtype == CFZ_KV8_F32,
                                            (hipStream_t)hip_stream),
                       "adapter launch");

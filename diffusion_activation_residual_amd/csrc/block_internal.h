@@ -59,12 +59,12 @@ struct RotateRows {
     void *out;
     const void *w;
     int64_t xs, os;
-    int w_f32;
-    int first;  // heads of the tensors before it
+    int w_f32, heads;
+    int first;  // waves per token of the tensors before it
 };
 struct RotateArgs {
     RotateRows t[4];
-    int count, heads, dim, log2lanes;
+    int count, dim, log2lanes;
     BlockRows rows;
     const int32_t *starts;
     const float *cos, *sin;
@@ -87,18 +87,21 @@ struct AdapterArgs {
     int adapters, slices, rank, cols_in, cols_out;
     int down;            // adapter rows of the first product: slices * rank
     int first_col[5];    // of each slice, and the end
-    int first_group[4];  // of 64 columns
-    int groups, col_tiles;
+    int first_tile[4];   // a slice's column tiles of the second product
+    int col_tiles;
     const void *x, *y;
     void *out;
     int64_t xs, ys, os;
-    float *h;  // [splits][tokens][down]
-    int splits;
+    uint16_t *hi, *lo;  // [tokens][down]: scale x A^T as the sum of two numbers of the type
+    float *back;        // [tokens][slices]: what it was multiplied by, turned round (fp16)
     bool tall;  // 32 tokens a tile of the first product, else 16
 };
 void adapter_plan(AdapterArgs &a);
 int64_t adapter_tiles(const AdapterArgs &a, int rows);
 int64_t adapter_groups(const AdapterArgs &a);
+int64_t adapter_pieces(const AdapterArgs &a);  // of 16 bytes, of one adapter's A as it is laid out
+hipError_t launch_adapters_put(const AdapterArgs &a, const void *rows, int first, int count,
+                               hipStream_t st);
 hipError_t launch_adapters(const AdapterArgs &a, bool f16, bool y_f32, hipStream_t st);
 
 // ---- device helpers

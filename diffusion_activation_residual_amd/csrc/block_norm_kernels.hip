@@ -85,32 +85,25 @@ __global__ __launch_bounds__(kThreads) void residual_norm_kernel(ResidualArgs a)
         return;
     const X *x = (const X *)a.x + row * a.xs;
     const Y *y = (const Y *)a.y + row * a.ys;
-    float v[V][8];
-    // (rows of no item are not read: the loads wait for the item only where offsets are given)
+    // the rows are under way while their item is looked up
+    float v[V][8], u[V][8];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int at = (i * G + tid) * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[i][j] = u[i][j] = 0.0f;
+        if (at < a.cols) {
+            load_n(x + at, u[i]);
+            if (a.y)
+                load_n(y + at, v[i]);
+        }
+    }
     int64_t first;
     const int item = block_item(a.rows, row, &first);
     if (item < 0)
         return;
     if (a.y) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int at = (i * G + tid) * 8;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[i][j] = 0.0f;
-            if (at < a.cols)
-                load_n(y + at, v[i]);
-        }
-        float u[V][8];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int at = (i * G + tid) * 8;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                u[i][j] = 0.0f;
-            if (at < a.cols)
-                load_n(x + at, u[i]);
-        }
         normalise<Y, V, G>(v, a.after, a.cols, tid, red);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -126,14 +119,10 @@ __global__ __launch_bounds__(kThreads) void residual_norm_kernel(ResidualArgs a)
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int at = (i * G + tid) * 8;
+        for (int i = 0; i < V; ++i)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                v[i][j] = 0.0f;
-            if (at < a.cols)
-                load_n(x + at, v[i]);
-        }
+                v[i][j] = u[i][j];
     }
     if (a.r) {
 #pragma unroll

@@ -24,49 +24,56 @@ __global__ __launch_bounds__(kThreads) void rotation_table_kernel(TableArgs a)
 
 constexpr int kStay = 0, kPairs = 1, kHalves = 2;  // how heads turn
 
-// A wave takes kRotateUnits x 64 units of 8 dimensions of one token, the tensors' heads side by
-// side; a head's units lie on neighbouring lanes, so that its norm is a short sum across lanes.  A
-// unit holds whole pairs: 8 neighbours, or 4 of each half.  All of a thread's units have the same
+// A wave takes kRotateUnits x 64 units of 8 dimensions of one token in one tensor; a head's units lie
+// on neighbouring lanes, so that its norm is a short sum across lanes.  A unit holds whole pairs: 8
+// neighbours, or 4 of each half.  All of a thread's units have the same
 // place in their heads, so that its cosines and sines are loaded once.
 template <class T, int TURN>
 __global__ __launch_bounds__(kThreads) void rotate_kernel(RotateArgs a)
 {
     const int lane = threadIdx.x & 63;
-    const int64_t wave = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
-    const int64_t row = wave / a.parts;
-    if (row >= a.rows.tokens)
+    const uint32_t wave =
+        __builtin_amdgcn_readfirstlane(blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6));
+    const uint32_t row32 = wave / (uint32_t)a.parts;
+    if (row32 >= a.rows.tokens)
         return;
-    int64_t first;
-    const int seq = block_item(a.rows, row, &first);
-    if (seq < 0)
-        return;
+    const int64_t row = row32;
+    int part = (int)(wave - row32 * (uint32_t)a.parts), which = 0;
+    while (which + 1 < a.count && part >= a.t[which + 1].first)
+        ++which;
+    const RotateRows t = a.t[which];
     const int lanes = 1 << a.log2lanes;
     const int unit = lane & (lanes - 1);
-    const int head0 = (int)(wave % a.parts) * ((kRotateUnits * 64) >> a.log2lanes) +
-                      (lane >> a.log2lanes);
+    const int head0 = ((part - t.first) * (kRotateUnits * 64) + lane) >> a.log2lanes;
     const int half = a.rot / 2;
     const bool turn = TURN != kStay && unit * 8 < a.rot;
     const bool split = TURN == kHalves && turn;
     const int d0 = split ? 4 * unit : 8 * unit, d1 = split ? half + 4 * unit : 8 * unit + 4;
 
+    // the values are under way while the row's sequence and position are looked up
     float v[kRotateUnits][8];
-    int which[kRotateUnits];
+    const T *x = (const T *)t.x + row * t.xs;
 #pragma unroll
     for (int i = 0; i < kRotateUnits; ++i) {
         const int head = head0 + i * (64 >> a.log2lanes);
-        int t = 0;
-        while (t + 1 < a.count && head >= a.t[t + 1].first)
-            ++t;
-        which[i] = head < a.heads ? t : -1;
-        if (which[i] < 0)
+        if (head >= t.heads)
             continue;
-        const T *x = (const T *)a.t[t].x + row * a.t[t].xs + (head - a.t[t].first) * a.dim;
         if (split) {
-            load_n(x + d0, *(float(*)[4]) & v[i][0]);
-            load_n(x + d1, *(float(*)[4]) & v[i][4]);
+            load_n(x + head * a.dim + d0, *(float(*)[4]) & v[i][0]);
+            load_n(x + head * a.dim + d1, *(float(*)[4]) & v[i][4]);
         } else {
-            load_n(x + d0, v[i]);
+            load_n(x + head * a.dim + d0, v[i]);
         }
+    }
+    int64_t first;
+    const int seq = block_item(a.rows, row, &first);
+    if (seq < 0)
+        return;
+    float w[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
+    if (t.w) {
+        const BlockVec wv{t.w, 0, t.w_f32};
+        load_vec<T>(wv, d0, *(float(*)[4]) & w[0]);
+        load_vec<T>(wv, d1, *(float(*)[4]) & w[4]);
     }
     float co[4], si[4];
     if (turn) {
@@ -77,22 +84,15 @@ __global__ __launch_bounds__(kThreads) void rotate_kernel(RotateArgs a)
     }
 #pragma unroll
     for (int i = 0; i < kRotateUnits; ++i) {
-        // (the lanes of a head go together)
-        if (which[i] < 0)
+        const int head = head0 + i * (64 >> a.log2lanes);
+        if (head >= t.heads)  // (the lanes of a head go together)
             continue;
-        const RotateRows &t = a.t[which[i]];
         if (a.normed) {
             float q = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 q = fmaf(v[i][j], v[i][j], q);
             const float f = 1.0f / sqrtf(lanes_sum(q, lanes) / (float)a.dim + a.eps);
-            float w[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
-            if (t.w) {
-                const BlockVec wv{t.w, 0, t.w_f32};
-                load_vec<T>(wv, d0, *(float(*)[4]) & w[0]);
-                load_vec<T>(wv, d1, *(float(*)[4]) & w[4]);
-            }
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 v[i][j] *= f * w[j];
@@ -106,8 +106,7 @@ __global__ __launch_bounds__(kThreads) void rotate_kernel(RotateArgs a)
                 v[i][p1] = fmaf(y0, si[j], y1 * co[j]);
             }
         }
-        const int head = head0 + i * (64 >> a.log2lanes);
-        T *o = (T *)t.out + row * t.os + (head - t.first) * a.dim;
+        T *o = (T *)t.out + row * t.os + head * a.dim;
         if (split) {
             store_n(o + d0, *(float(*)[4]) & v[i][0]);
             store_n(o + d1, *(float(*)[4]) & v[i][4]);

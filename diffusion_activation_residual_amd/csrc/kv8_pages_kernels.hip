@@ -375,16 +375,20 @@ __global__ __launch_bounds__(kThreads) void kv8_copy_kernel(Kv8Cache to, Kv8Cach
             x = from.v + a * s.codes;
             y = to.v + b * s.codes;
         }
-        const int64_t at = (int64_t)piece * kPiece + threadIdx.x * 16;
-        uint4 q[kPiece / 16 / kThreads];
-#pragma unroll
-        for (int i = 0; i < kPiece / 16 / kThreads; ++i)
-            if (at + i * kThreads * 16 < bytes)
-                q[i] = *(const uint4 *)(x + at + i * kThreads * 16);
-#pragma unroll
-        for (int i = 0; i < kPiece / 16 / kThreads; ++i)
-            if (at + i * kThreads * 16 < bytes)
-                *(uint4 *)(y + at + i * kThreads * 16) = q[i];
+        const int64_t base = (int64_t)piece * kPiece;
+        const uint4 *px = (const uint4 *)(x + base) + threadIdx.x;
+        uint4 *py = (uint4 *)(y + base) + threadIdx.x;
+        static_assert(kPiece == 4 * 16 * kThreads, "a piece is four vectors a thread");
+        if (bytes - base >= kPiece) {
+            const uint4 q0 = px[0], q1 = px[kThreads], q2 = px[2 * kThreads], q3 = px[3 * kThreads];
+            py[0] = q0;
+            py[kThreads] = q1;
+            py[2 * kThreads] = q2;
+            py[3 * kThreads] = q3;
+        } else {
+            for (int i = 0; i * kThreads + threadIdx.x < (bytes - base) / 16; ++i)
+                py[i * kThreads] = px[i * kThreads];
+        }
     }
 }
 

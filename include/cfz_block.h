@@ -52,7 +52,7 @@ typedef struct {
  * cols: a multiple of 8, 8 .. 16384; row strides in elements, >= cols, multiples of 16
  * bytes.  0 <= tokens < 2^31, 1 <= batch <= 65535.
  * offsets: [batch + 1] int32, ascending: rows offsets[b] .. offsets[b + 1] - 1 belong to item b;
- * rows outside every item are neither read nor written.  NULL: batch equal runs (tokens a
+ * rows outside every item are left as they are in r and h.  NULL: batch equal runs (tokens a
  * multiple of batch).
  * r may be x, and h may be y, with the same stride; other overlaps are not allowed.
  * Errors: CFZ_ERR_NULL, CFZ_ERR_SHAPE, CFZ_ERR_UNSUPPORTED, CFZ_ERR_ALIGN, CFZ_ERR_HIP. */
@@ -135,7 +135,7 @@ typedef struct {
  * rotation NULL: the norm alone.  Without rotation->positions, row i of sequence b is at position
  * starts[b] + i (starts NULL: i).  Positions outside the table take its nearest row.
  * head_dim in {32, 64, 128, 256}, rot_dim a multiple of 8 up to it, heads 1 .. 1024 each.
- * offsets: [batch + 1] int32 as above, rows outside are neither read nor written; NULL: one
+ * offsets: [batch + 1] int32 as above, rows outside are left as they are in out; NULL: one
  * sequence (batch = 1).  0 <= tokens < 2^31, 1 <= batch <= 65535; 2^23 or more work-groups (of
  * four tokens x up to 2048 values) are refused.
  * Errors: as cfz_residual_norm. */
@@ -145,8 +145,10 @@ cfz_status cfz_rotate(int32_t count, const cfz_rotate_rows *tensors, cfz_kv8_dty
                       float eps, void *hip_stream);
 
 /* Low-rank adapters of one projection, to be added beside it for several requests at once.
- *   a: [adapters][slices * rank][cols_in], b: [adapters][cols_out][rank], both of `dtype` (BF16 or
- *   F16), scale: [adapters] fp32 or NULL (1).
+ *   a: [adapters][slices * rank][cols_in] of `dtype` (BF16 or F16), laid out by cfz_adapters_put:
+ *      for each adapter [ceil(slices * rank / 16)][4 ceil(cols_in / 128)][4][16][8], row 16 i + m's
+ *      column 32 k + 8 q + e at [i][k][q][m][e], zeros past either end; cfz_adapters_a_bytes bytes;
+ *   b: [adapters][cols_out][rank] of `dtype`, scale: [adapters] fp32 or NULL (1).
  * The projection's columns are dealt out to 1 .. 4 slices (query, key and value of one fused
  * projection) of slice_cols[i] columns each, multiples of 16, cols_out in all; slice i's columns
  * are met by adapter rows i * rank .. (i + 1) * rank - 1 of a.  rank: a multiple of 8, 8 .. 128,
@@ -159,10 +161,18 @@ typedef struct {
     int32_t cols_in;
     int32_t slice_cols[4];
     int32_t dtype;
-    const void *a;
+    void *a;
     const void *b;
     const float *scale;
 } cfz_adapters;
+
+/* Bytes of the laid-out a; 0 if the arguments are invalid. */
+size_t cfz_adapters_a_bytes(const cfz_adapters *adapters);
+/* Lays out the rows [count][slices * rank][cols_in] of adapters first .. first + count - 1 in
+ * adapters->a (b, scale are not looked at).  2^31 or more pieces of 16 bytes a call are refused.
+ * Errors: CFZ_ERR_NULL, CFZ_ERR_SHAPE, CFZ_ERR_UNSUPPORTED, CFZ_ERR_ALIGN, CFZ_ERR_HIP. */
+cfz_status cfz_adapters_put(const cfz_adapters *adapters, int32_t first, int32_t count,
+                            const void *rows, void *hip_stream);
 
 /* out = y + scale_a (x a^T) b^T for the token rows offsets[b] .. offsets[b + 1] - 1 of sequence b, with
  * adapter ids[b] (outside of 0 .. adapters - 1: none, out = y).  x: rows of `dtype`; y and out: rows

@@ -200,9 +200,25 @@ def test_adapter_refusals(kw, status):
                                 None) == NULL
 
 
+@pytest.mark.parametrize("first,count,a,rows,status", [
+    (-1, 1, A, A, SHAPE), (0, -1, A, A, SHAPE), (2, 1, A, A, SHAPE), (1 << 30, 1 << 30, A, A, SHAPE),
+    (0, 1, None, A, NULL), (0, 1, A, None, NULL), (0, 1, ODD, A, ALIGN), (0, 1, A, ODD, ALIGN),
+    (2, 0, None, None, cfz.CFZ_OK),
+])
+def test_adapter_layout_refusals(first, count, a, rows, status):
+    w = block.cfz_adapters(2, 1, 8, 64, (C.c_int32 * 4)(64), 0, a, None, None)
+    assert lib.cfz_adapters_put(C.byref(w), first, count, rows, None) == status
+    assert lib.cfz_adapters_put(None, 0, 0, None, None) == NULL
+    assert lib.cfz_adapters_a_bytes(C.byref(w)) == 2 * 16 * 128 * 2
+    w.cols_in, w.rank = 40, 24
+    assert lib.cfz_adapters_a_bytes(C.byref(w)) == 2 * 32 * 128 * 2
+    w.rank = 7
+    assert lib.cfz_adapters_a_bytes(C.byref(w)) == 0
+
+
 def test_adapter_workspaces():
-    """A row of all slices' low-rank values for each token; nothing for no tokens or sequences."""
-    assert adapters()[1] == 4 * 16 * 4
+    """A row of all slices' low-rank values and a number for each slice, for each token; nothing for no
+    tokens or sequences."""
+    assert adapters()[1] == 4 * (16 + 2) * 4
     assert adapters(tokens=0)[1] == adapters(batch=0)[1] == adapters(rank=7)[1] == 0
-    # few rows: the columns are cut into runs of at least 512
-    assert adapters(cols_in=4096, xs=4096)[1] == 8 * 4 * 16 * 4
+    assert adapters(cols_in=4096, xs=4096)[1] == 4 * (16 + 2) * 4

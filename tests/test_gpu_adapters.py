@@ -18,7 +18,9 @@ def make(g, count, cols_in, slices, rank, real, scaled=True):
     a = g(count, len(slices) * rank, cols_in, dtype=REAL[real], size=cols_in ** -0.5)
     b = g(count, sum(slices), rank, dtype=REAL[real], size=rank ** -0.5)
     scale = g(count) if scaled else None
-    return block.Adapters(a, b, scale, slices=slices)
+    w = block.Adapters(a, b, scale, slices=slices)
+    w.rows = a
+    return w
 
 
 def check(w, x, y, out, ids, offsets, real, before=None, max_rows=1 << 30):
@@ -28,10 +30,10 @@ def check(w, x, y, out, ids, offsets, real, before=None, max_rows=1 << 30):
         if lo >= hi:
             continue
         seen[lo:hi] = True
-        if not 0 <= n < w.a.shape[0]:
+        if not 0 <= n < w.count:
             assert torch.equal(out[lo:hi], y[lo:hi])
             continue
-        want, off = model.adapters_add(to64(x[lo:hi]), to64(y[lo:hi]), to64(w.a[n]), to64(w.b[n]),
+        want, off = model.adapters_add(to64(x[lo:hi]), to64(y[lo:hi]), to64(w.rows[n]), to64(w.b[n]),
                                        1.0 if w.scale is None else float(w.scale[n]), w.slices, real)
         close(out[lo:hi], want, off)
     if before is not None:
@@ -96,7 +98,7 @@ def test_many_sequences(batch):
     which = torch.tensor(np.repeat(ids, counts), device=DEV)
     low = torch.zeros(tokens, 32, dtype=torch.float64, device=DEV)
     for n in range(6):
-        h = (x.double() @ w.a[n].double().t().contiguous()) * w.scale[n].double()
+        h = (x.double() @ w.rows[n].double().t().contiguous()) * w.scale[n].double()
         low += torch.where((which == n)[:, None], h @ w.b[n].double().t().contiguous(), 0.0)
     want = y.double() + low
     # (rank 8, sizes of 1: far inside the model's bound at 2^-12)
@@ -151,13 +153,45 @@ def test_refusals():
         w.add(x, y, one, off, 4, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
     with pytest.raises(cfz.CfzError):
         w.add(x, y, one, off, -1)
-    with pytest.raises(ValueError):
-        block.Adapters(w.a, w.b, slices=3)
-    with pytest.raises(ValueError):
-        block.Adapters(w.a, w.b[:1])
+    for a, b, kw in ((w.rows, w.b, dict(slices=3)), (w.rows, w.b[:1], {}),
+                     (w.rows[:, :4], w.b, {}), (w.rows, w.b.half(), {}),
+                     (w.rows, w.b, dict(scale=y[0])), (w.rows[0], w.b, {})):
+        with pytest.raises(ValueError):
+            block.Adapters(a, b, **kw)
     with pytest.raises(cfz.CfzError):
-        v = block.Adapters(w.a[:, :4].contiguous(), w.b[:, :, :4].contiguous())
-        v.add(x, y, one, off, 4)
+        block.Adapters(w.rows[:, :4].contiguous(), w.b[:, :, :4].contiguous())
+    for args in ((1, w.rows), (-1, w.rows), (0, w.rows.half()), (0, w.rows, w.b[:1]),
+                 (0, w.rows, None, w.scale[:1])):
+        with pytest.raises(ValueError):
+            w.put(*args)
+
+
+@pytest.mark.parametrize("down,cols_in", [(8, 8), (24, 40), (16, 32), (72, 4104)])
+def test_layout_and_replacement(down, cols_in):
+    """Pieces of 16 rows x 32 columns, zeros past the ends; adapters replaced leave the others alone."""
+    g = Gen(down)
+    a = g(3, down, cols_in, dtype=torch.bfloat16)
+    w = block.Adapters(a, g(3, 64, down, dtype=torch.bfloat16), g(3))
+
+    def want(rows):
+        i, k = -(-down // 16), -(-cols_in // 128) * 4
+        full = torch.zeros(3, 16 * i, 32 * k, dtype=torch.bfloat16, device=DEV)
+        full[:, :down, :cols_in] = rows
+        return full.view(3, i, 16, k, 4, 8).permute(0, 1, 3, 4, 2, 5).contiguous()
+
+    def held():
+        return w.a.view(torch.bfloat16).view(want(a).shape)
+
+    assert torch.equal(held(), want(a))
+    new, b, scale = g(2, down, cols_in, dtype=torch.bfloat16), w.b[:2].clone() + 1, g(2)
+    before = w.b.clone(), w.scale.clone()
+    w.put(1, new, b, scale)
+    a[1:] = new
+    assert torch.equal(held(), want(a))
+    assert torch.equal(w.b[1:], b) and torch.equal(w.scale[1:], scale)
+    assert torch.equal(w.b[0], before[0][0]) and w.scale[0] == before[1][0]
+    w.put(0, a)
+    assert torch.equal(held(), want(a)) and torch.equal(w.b[1:], b)
 
 
 def test_streams_and_graphs():

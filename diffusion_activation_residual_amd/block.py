@@ -18,6 +18,7 @@ from typing import Optional
 import torch
 
 from . import cfz, kv8
+from .cfz import CFZ_ERR_NULL, CFZ_OK, CfzError
 from .kv8 import CFZ_KV8_F32, _REALS, _empty_on, _fit, _ints, _queue, cfz_kv8_rotation
 
 NORMS = {"none": 0, "rms": 1, "layer": 2}
@@ -94,6 +95,9 @@ def _as_stream(stream, device):
 
 def _matrix(t, shape, dtypes, device, what):
     """Row stride of a [rows, cols] tensor with dense rows."""
+    stride = t.stride()
+    if t.dtype in dtypes and t.device == device and t.shape == shape and stride[1] == 1:
+        return stride[0] if shape[0] > 1 else shape[1]
     if t.dtype not in dtypes:
         raise TypeError(f"{what}: {t.dtype}, expected one of {dtypes}")
     if t.device != device:
@@ -101,9 +105,9 @@ def _matrix(t, shape, dtypes, device, what):
     if t.shape != shape:
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     rows, cols = shape
-    if t.numel() and cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{what}: a row's values must lie side by side (strides {t.stride()})")
-    return t.stride(0) if rows > 1 else cols
+    if t.numel() and cols > 1:
+        raise ValueError(f"{what}: a row's values must lie side by side (strides {stride})")
+    return stride[0] if rows > 1 else cols
 
 
 def _vector(t, size, dtype, device, what):
@@ -127,8 +131,6 @@ class Norm:
 
 
 def _norm(norm, cols, dtype, device, what):
-    if norm is None:
-        return cfz_norm()
     if norm.kind not in NORMS:
         raise ValueError(f"{what}: kind = {norm.kind!r}, one of {sorted(NORMS)}")
     weight = bias = None
@@ -145,8 +147,6 @@ def _norm(norm, cols, dtype, device, what):
 
 def _items(t, batch, cols, dtype, device, what):
     """[batch, cols] rows (possibly apart, as chunks of one projection are), [1, cols] or [cols]."""
-    if t is None:
-        return cfz_item_rows()
     if t.dim() == 1:
         t = t[None]
     if t.dim() != 2 or t.shape[0] not in (1, batch):
@@ -170,45 +170,76 @@ def residual_norm(x, y=None, *, before=None, after=None, gate=None, gate_scale=1
     (int32 [batch + 1]) gives the items' rows; rows of no item are left alone (unset, where r and h
     are allocated here).  Without it the items have equally many rows.  ``out`` may be x and
     ``normed`` may be y: in place."""
+    a, device, out, normed = _residual(x, y, before, after, gate, gate_scale, scale, shift, offsets,
+                                       batch, dtype, out, normed, stream)
+    _queue(_lib.cfz_residual_norm, device, stream, C.byref(a))
+    return out, normed
+
+
+def check_residual_norm(x, y=None, *, out, normed, before=None, after=None, gate=None, gate_scale=1.0,
+                        scale=None, shift=None, offsets=None, batch=None, dtype=None):
+    """Raises where ``residual_norm`` would refuse these arguments (out and normed: given, or None where
+    the call would leave them out); queues nothing."""
+    a, *_ = _residual(x, y, before, after, gate, gate_scale, scale, shift, offsets, batch, dtype, out,
+                      normed, None)
+    if a.x % 16 if a.x else 0:
+        raise ValueError(f"x: {a.x:#x}, expected 16-byte alignment")
+    if out is not None and a.r == a.x and a.r_stride != a.x_stride:
+        raise ValueError("in place, the strides must be the same")
+    a.x = None  # (the last thing that the library asks for)
+    status = _lib.cfz_residual_norm(C.byref(a), None)
+    if status != (CFZ_OK if a.tokens == 0 else CFZ_ERR_NULL):
+        raise CfzError(status, "cfz_residual_norm")
+
+
+def _residual(x, y, before, after, gate, gate_scale, scale, shift, offsets, batch, dtype, out, normed,
+              stream):
+    """The call's arguments, checked as far as the library does not see them, and its results."""
     device = _device(x, "x")
     if x.dim() != 2 or x.dtype not in _REALS:
         raise ValueError(f"x: {x.dtype} {tuple(x.shape)}, expected bf16, fp16 or fp32 [tokens, cols]")
-    tokens, cols = x.shape
+    shape = tokens, cols = x.shape
     if dtype is None:
         dtype = x.dtype if y is None else y.dtype
     if dtype not in _REALS or (y is not None and y.dtype != dtype):
         raise TypeError(f"dtype = {dtype}: bf16, fp16 or fp32, and y's")
-    if batch is None:
+    if offsets is not None:
+        batch = offsets.numel() - 1
+    elif batch is None:
         batch = max([1] + [t.shape[0] for t in (gate, scale, shift) if t is not None and t.dim() == 2])
-        if offsets is not None:
-            batch = offsets.numel() - 1
     _fit(32, cols=cols, batch=batch)
     a = cfz_residual()
     a.tokens, a.cols, a.batch = tokens, cols, batch
     if offsets is not None:
         a.offsets = _ints(offsets, (batch + 1,), device, "offsets")
     a.x_dtype, a.y_dtype = _REALS[x.dtype], _REALS[dtype]
-    a.x, a.x_stride = x.data_ptr(), _matrix(x, x.shape, _REALS, device, "x")
+    a.x, a.x_stride = x.data_ptr(), _matrix(x, shape, _REALS, device, "x")
     if y is not None:
-        a.y, a.y_stride = y.data_ptr(), _matrix(y, x.shape, _REALS, device, "y")
+        a.y, a.y_stride = y.data_ptr(), _matrix(y, shape, _REALS, device, "y")
     a.gate_scale = gate_scale
-    a.gate = _items(gate, batch, cols, dtype, device, "gate")
-    a.scale = _items(scale, batch, cols, dtype, device, "scale")
-    a.shift = _items(shift, batch, cols, dtype, device, "shift")
-    a.after = _norm(after, cols, dtype, device, "after")
-    a.before = _norm(before, cols, dtype, device, "before")
-    if y is None and out is None:
+    if gate is not None:
+        a.gate = _items(gate, batch, cols, dtype, device, "gate")
+    if scale is not None:
+        a.scale = _items(scale, batch, cols, dtype, device, "scale")
+    if shift is not None:
+        a.shift = _items(shift, batch, cols, dtype, device, "shift")
+    if after is not None:
+        a.after = _norm(after, cols, dtype, device, "after")
+    if before is not None:
+        a.before = _norm(before, cols, dtype, device, "before")
+    if out is not None:
+        a.r, a.r_stride = out.data_ptr(), _matrix(out, shape, (x.dtype,), device, "out")
+    elif y is not None:
+        out = _empty_on(device, stream, shape, x.dtype)
+        a.r, a.r_stride = out.data_ptr(), cols
+    else:
         out = x  # (nothing changes: no copy is made)
-    elif out is None:
-        out = _empty_on(device, stream, (tokens, cols), x.dtype)
-    if y is not None or out is not x:
-        a.r, a.r_stride = out.data_ptr(), _matrix(out, x.shape, (x.dtype,), device, "out")
-    if before is not None or scale is not None or shift is not None or normed is not None:
-        if normed is None:
-            normed = _empty_on(device, stream, (tokens, cols), dtype)
-        a.h, a.h_stride = normed.data_ptr(), _matrix(normed, x.shape, (dtype,), device, "normed")
-    _queue(_lib.cfz_residual_norm, device, stream, C.byref(a))
-    return out, normed
+    if normed is not None:
+        a.h, a.h_stride = normed.data_ptr(), _matrix(normed, shape, (dtype,), device, "normed")
+    elif before is not None or scale is not None or shift is not None:
+        normed = _empty_on(device, stream, shape, dtype)
+        a.h, a.h_stride = normed.data_ptr(), cols
+    return a, device, out, normed
 
 
 def rotation_table(rot_dim, rows=None, positions=None, axis_dims=None, base=10000.0, scaling="none",

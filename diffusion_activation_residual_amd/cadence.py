@@ -10,7 +10,10 @@ launch's ramp-up and drain then overlap another launch's streaming.
 
 ``enqueue_layer_attention`` goes on to the algorithm's next line: what a device has received of
 every share's K and V is decoded, the shares are written into the layer's 8-bit cache, and the
-device's own queries attend over all of them.
+device's own queries attend over all of them, normed and turned on the way where the plan says so.
+
+``enqueue_layer_features`` is for strategies that exchange a layer's features instead: the step along the
+residual stream that makes them (gate, sum, norm, scale and shift) and their compression.
 
 Host logic only: every launch is a call of the C ABI through the binding."""
 import ctypes as C
@@ -20,7 +23,7 @@ from typing import Optional
 
 import torch
 
-from . import cfz, kv8
+from . import block, cfz, kv8
 
 
 @dataclass
@@ -45,10 +48,16 @@ class SharePlan:
     its own of the pages 0 .. pages - 1 of a pool), and the rotation of the keys.
 
     With ``count`` the queries attend in blocks of ``q_block`` over the ``count`` pages that
-    ``kv8.Cache.select`` picks for them, the ``first`` and ``last`` ones always among them."""
+    ``kv8.Cache.select`` picks for them, the ``first`` and ``last`` ones always among them.
+
+    With ``query_start`` the queries come as they were projected and are turned here, by the same
+    rotation as the keys: an item's query i is at position query_start + i (the start of the
+    device's own share).  With ``head_norm`` (an eps) their heads are normed before, with the weights that
+    the step names for each layer (``q_weights``)."""
 
     def __init__(self, batch, share_tokens, queries, page_tokens, rotation=None, q_block=128,
-                 count=None, first=0, last=0, scale=None, device="cuda"):
+                 count=None, first=0, last=0, scale=None, device="cuda", query_start=None,
+                 head_norm=None):
         share_tokens = list(share_tokens)
         if batch < 1 or not share_tokens or min(share_tokens) < 1 or queries < 1:
             raise ValueError(f"batch = {batch}, share_tokens = {share_tokens}, queries = {queries}: "
@@ -58,6 +67,12 @@ class SharePlan:
         if count is not None and (not 1 <= count <= 4096 or not 1 <= q_block < 1 << 31 or
                                   first < 0 or last < 0 or first + last > count):
             raise ValueError(f"count = {count}, q_block = {q_block}, first = {first}, last = {last}")
+        if query_start is not None and (rotation is None or rotation.positions is not None or
+                                        not 0 <= query_start < 1 << 31):
+            raise ValueError(f"query_start = {query_start}: needs a rotation that names no positions")
+        self.query_start, self.head_norm = query_start, head_norm
+        if head_norm is not None and not 0 <= head_norm < float("inf"):
+            raise ValueError(f"head_norm = {head_norm}: finite and not negative")
         self.batch, self.share_tokens, self.queries = batch, share_tokens, queries
         self.tokens = sum(share_tokens)
         self.page_tokens = page_tokens
@@ -75,6 +90,7 @@ class SharePlan:
         self.offsets = [ints([i * n for i in range(batch + 1)]) for n in share_tokens]
         self.lengths = ints([self.tokens] * batch)
         self.q_offsets = ints([i * queries for i in range(batch + 1)])
+        self.q_starts = None if query_start is None else ints([query_start] * batch)
 
     def _check_sizes(self, cache, q, keys):
         """Raises what the library refuses about these sizes."""
@@ -101,8 +117,18 @@ class SharePlan:
         cache.append(share.k, share.v, self.table, self.starts[index], self.offsets[index],
                      self.share_tokens[index], rotation=self.rotation, stream=stream)
 
-    def attend(self, cache, q, out=None, lse=None, stream=None):
+    def turn(self, q, weight=None, stream=None):
+        """The queries as they attend: their heads normed and turned as the plan says."""
+        if self.q_starts is None and self.head_norm is None:
+            return q
+        return block.rotate([q], None if self.q_starts is None else self.rotation, self.q_offsets,
+                            self.q_starts, weights=None if weight is None else [weight],
+                            normed=self.head_norm is not None,
+                            eps=0.0 if self.head_norm is None else self.head_norm, stream=stream)[0]
+
+    def attend(self, cache, q, out=None, lse=None, stream=None, q_weight=None):
         """The queries q [batch * queries, q_heads, head_dim] over all shares: (out, lse)."""
+        q = self.turn(q, q_weight, stream)
         blocks = None
         if self.count is not None:
             blocks = cache.select(q, self.table, self.lengths, self.q_offsets, self.queries,
@@ -133,17 +159,18 @@ def enqueue_layer_step(layers, senders, receivers, x, codes, scales, streams, xh
                                      None if xhat is None else [xhat[i] for i in c], stream=st)
 
 
-def enqueue_layer_attention(plan, layers, caches, q, out, streams):
+def enqueue_layer_attention(plan, layers, caches, q, out, streams, q_weights=None):
     """Enqueue one step of the attention over compressed shares: for layer l one grouped decode
     of the received payloads of layers[l] (a list of ``Share``, in the order of the plan's shares),
     their tokens into caches[l] (``kv8.Cache`` of at least ``plan.pages`` pages), and the
     attention of q[l] over all of them into out[l], on streams[l % len(streams)], ordered as in
     ``enqueue_layer_step``.  Works eagerly and under capture.  The layers must not share
-    caches, tensors or receivers.
+    caches, tensors or receivers.  q_weights: the weights [head_dim] of the layers' query norms, where the
+    plan has one (None, or None for a layer: ones).
 
     A step that does not fit is refused whole, before anything is queued: a decode moves its
     receivers' bases on, so that a step cannot be tried again after half of it."""
-    _check_step(plan, layers, caches, q, out, streams)
+    _check_step(plan, layers, caches, q, out, streams, q_weights)
     with _spread(streams):
         for l, shares in enumerate(layers):
             st = streams[l % len(streams)]
@@ -153,7 +180,66 @@ def enqueue_layer_attention(plan, layers, caches, q, out, streams):
             for i, s in enumerate(shares):
                 plan.write(caches[l], i, s, stream=st)
             # (the log-sum-exp is not wanted: its buffer lives as long as the work on st)
-            plan.attend(caches[l], q[l], out=out[l], stream=st)
+            plan.attend(caches[l], q[l], out=out[l], stream=st,
+                        **({} if q_weights is None else {"q_weight": q_weights[l]}))
+
+
+@dataclass
+class FeatureStep:
+    """One layer's step along the residual stream, as ``block.residual_norm`` takes it: the sum goes to
+    ``out`` (which may be x), the features to the tensor that the step names."""
+
+    x: torch.Tensor
+    y: torch.Tensor
+    out: torch.Tensor
+    before: Optional[block.Norm] = None
+    after: Optional[block.Norm] = None
+    gate: Optional[torch.Tensor] = None
+    gate_scale: float = 1.0
+    scale: Optional[torch.Tensor] = None
+    shift: Optional[torch.Tensor] = None
+    offsets: Optional[torch.Tensor] = None
+
+
+def enqueue_layer_features(steps, senders, features, codes, scales, streams):
+    """Enqueue one step of exchanged features: for layer l the step along the residual stream steps[l]
+    (``FeatureStep``), its features into features[l] (bf16 [tokens, cols], dense), and their
+    compression by senders[l] (a state handle) into codes[l] and scales[l], on
+    streams[l % len(streams)], ordered as in ``enqueue_layer_step``.  Works eagerly and under
+    capture.  The layers must not share tensors or senders.
+
+    A step that does not fit is refused whole, before anything is queued: a sum in place and a sender's
+    state cannot be taken back."""
+    if not len(steps) == len(senders) == len(features) == len(codes) == len(scales):
+        raise ValueError(f"{len(steps)} steps, {len(senders)} senders, {len(features)} features, "
+                         f"{len(codes)} codes and {len(scales)} scales")
+    if not streams:
+        raise ValueError("at least one stream")
+    if len(set(senders)) != len(senders):
+        raise ValueError("the same sender twice")
+    for l, s in enumerate(steps):
+        h = features[l]
+        if s.out is None or h is None or h.dtype != torch.bfloat16 or not h.is_contiguous():
+            raise ValueError(f"layer {l}: out and dense bf16 features are required")
+        if streams[l % len(streams)].device != s.x.device:
+            raise ValueError(f"layer {l}: stream on {streams[l % len(streams)].device}, x on "
+                             f"{s.x.device}")
+        block.check_residual_norm(s.x, s.y, normed=h, dtype=h.dtype, **_step_args(s))
+        if cfz.state_elements(senders[l]) not in (None, h.numel()):
+            raise ValueError(f"layer {l}: {h.numel()} features, the sender has "
+                             f"{cfz.state_elements(senders[l])}")
+        cfz.check_compress_group([senders[l]], [h], [codes[l]], [scales[l]])
+    with _spread(streams):
+        for l, s in enumerate(steps):
+            st = streams[l % len(streams)]
+            block.residual_norm(s.x, s.y, normed=features[l], dtype=features[l].dtype, stream=st,
+                                **_step_args(s))
+            cfz.cfz_compress_group([senders[l]], [features[l]], [codes[l]], [scales[l]], stream=st)
+
+
+def _step_args(s):
+    return dict(out=s.out, before=s.before, after=s.after, gate=s.gate, gate_scale=s.gate_scale,
+                scale=s.scale, shift=s.shift, offsets=s.offsets)
 
 
 def _payload(shares):
@@ -161,13 +247,16 @@ def _payload(shares):
             [c for s in shares for c in s.scales])
 
 
-def _check_step(plan, layers, caches, q, out, streams):
+def _check_step(plan, layers, caches, q, out, streams, q_weights=None):
     """Everything that a launch of the step would refuse."""
     if not streams:
         raise ValueError("at least one stream")
     if not len(layers) == len(caches) == len(q) == len(out):
         raise ValueError(f"{len(layers)} layers, {len(caches)} caches, {len(q)} queries and "
                          f"{len(out)} outputs")
+    if q_weights is not None and (plan.head_norm is None or len(q_weights) != len(q)):
+        raise ValueError(f"{len(q_weights)} q_weights for {len(q)} layers, head_norm = "
+                         f"{plan.head_norm}")
     alike = set()  # the plan's sizes are checked once for layers of the same sizes
     for l, (shares, cache) in enumerate(zip(layers, caches)):
         if len(shares) != len(plan.share_tokens):
@@ -198,6 +287,8 @@ def _check_step(plan, layers, caches, q, out, streams):
         _whole_rows(q[l], cache._queries(q[l]), l, "q")
         if out[l] is not None:
             _whole_rows(out[l], cache._outputs(q[l], out[l]), l, "out")
+        if q_weights is not None and q_weights[l] is not None:
+            block._vector(q_weights[l], cache.head_dim, q[l].dtype, cache.device, f"q_weights[{l}]")
         got = [s for s in shares if s.receivers is not None]
         if got:
             cfz.check_decompress_group(*_payload(got))

@@ -289,14 +289,35 @@ def cfz_compress_group(handles, xs, codes, scales, stream=None) -> None:
            "cfz_compress_group")
 
 
+def state_elements(handle):
+    """Elements of a state's tensor; None for a handle that this module did not make."""
+    return _sizes[handle][0] if handle in _sizes else None
+
+
+def check_compress_group(handles, xs, codes, scales) -> None:
+    """Raises where ``cfz_compress_group`` would refuse these arguments; queues nothing.  (Of handles
+    that this module did not make, only their presence and repetition are seen.)"""
+    if len(xs) != len(handles):
+        raise ValueError("all lists must have one entry per state")
+    for h, x in zip(handles, xs):
+        _check_payload(h, x=x)
+        if _bf16_ptr(x) % 16:
+            raise ValueError("x must be 16-byte aligned")
+    _check_group(handles, codes, scales, CFZ_SENDER, "sender")
+
+
 def check_decompress_group(handles, codes, scales) -> None:
     """Raises where ``cfz_decompress_group`` would refuse these arguments; queues nothing.  (Of handles
     that this module did not make, only their presence and repetition are seen.)"""
+    _check_group(handles, codes, scales, CFZ_RECEIVER, "receiver")
+
+
+def _check_group(handles, codes, scales, role, name):
     n = len(handles)
     if not (len(codes) == len(scales) == n):
         raise ValueError("all lists must have one entry per state")
     if len(set(handles)) != n or not all(handles):
-        raise ValueError("receivers: closed, or the same state twice")
+        raise ValueError(f"{name}s: closed, or the same state twice")
     codec = None
     for h, c, s in zip(handles, codes, scales):
         _check_payload(h, codes=c, scales=s)
@@ -305,10 +326,10 @@ def check_decompress_group(handles, codes, scales) -> None:
         mine = _codecs.get(h)
         if mine is None:
             continue
-        if mine[-1] != CFZ_RECEIVER:
-            raise ValueError("not a receiver state")
+        if mine[-1] != role:
+            raise ValueError(f"not a {name} state")
         if codec is not None and mine != codec:
-            raise ValueError("the receivers of a group must have one codec")
+            raise ValueError(f"the {name}s of a group must have one codec")
         codec = mine
 
 

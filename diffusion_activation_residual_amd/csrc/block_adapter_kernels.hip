@@ -313,12 +313,14 @@ constexpr int kUpRows = 64;
 // CB values of a row as they lie in memory, until they are needed as numbers.
 template <class Y, int CB> struct RawRow {
     static constexpr int kBytes = CB * (int)sizeof(Y), kPiece = kBytes < 16 ? kBytes : 16;
+    typedef uint32_t Words __attribute__((ext_vector_type(kPiece / 4)));
     struct alignas(kPiece) Piece { Y v[kPiece / sizeof(Y)]; } p[kBytes / kPiece];
+    // (read once and for the last time: not to take the place of x, A and out in the caches)
     __device__ inline void load(const Y *y)
     {
 #pragma unroll
         for (int i = 0; i < kBytes / kPiece; ++i)
-            p[i] = ((const Piece *)y)[i];
+            p[i] = __builtin_bit_cast(Piece, __builtin_nontemporal_load((const Words *)y + i));
     }
     __device__ inline void get(float (&o)[CB]) const
     {

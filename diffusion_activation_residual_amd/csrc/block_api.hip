@@ -157,24 +157,26 @@ cfz_status cfz_residual_norm(const cfz_residual *r, void *hip_stream)
     CFZ_TRY(check_stride(r->x_stride, r->cols, r->x_dtype, "x_stride"));
     if (r->y)
         CFZ_TRY(check_stride(r->y_stride, r->cols, call, "y_stride"));
-    else if (r->gate.data || r->after.kind != CFZ_NORM_NONE)
-        return fail(CFZ_ERR_NULL, "a gate and a norm of y need y");
     if (r->r)
         CFZ_TRY(check_stride(r->r_stride, r->cols, r->x_dtype, "r_stride"));
     if (r->h)
         CFZ_TRY(check_stride(r->h_stride, r->cols, call, "h_stride"));
     if (r->tokens == 0)
         return CFZ_OK;
-    if (!r->x || (!r->r && !r->h))
-        return fail(CFZ_ERR_NULL, "x and one of r and h are required");
     if (!aligned(r->x, 16) || !aligned(r->y, 16) || !aligned(r->r, 16) || !aligned(r->h, 16))
         return fail(CFZ_ERR_ALIGN, "x, y, r and h must be 16-byte aligned");
-    if ((r->r == r->x && r->r_stride != r->x_stride) ||
-        (r->y && r->h == r->y && r->h_stride != r->y_stride))
+    if ((r->r && r->r == r->x && r->r_stride != r->x_stride) ||
+        (r->h && r->h == r->y && r->h_stride != r->y_stride))
         return fail(CFZ_ERR_SHAPE, "in place, the strides must be the same");
-    if (r->cols > 4096 && r->tokens >= cfz::kBlockMaxGroups)
+    if (r->cols > 512 && r->tokens >= cfz::kBlockMaxGroups)
         return fail(CFZ_ERR_SHAPE, "the call needs %lld work-groups (limit 2^23)",
                     (long long)r->tokens);
+    if (!r->y && (r->gate.data || r->after.kind != CFZ_NORM_NONE))
+        return fail(CFZ_ERR_NULL, "a gate and a norm of y need y");
+    if (!r->r && !r->h)
+        return fail(CFZ_ERR_NULL, "one of r and h is required");
+    if (!r->x)
+        return fail(CFZ_ERR_NULL, "x is required");
     a.cols = r->cols;
     a.x = r->x, a.y = r->y, a.r = r->r, a.h = r->h;
     a.xs = r->x_stride, a.ys = r->y_stride, a.rs = r->r_stride, a.hs = r->h_stride;

@@ -183,19 +183,27 @@ __device__ inline int block_item(const BlockRows &rows, int64_t row, int64_t *fi
     return row >= a && row < e ? lo : -1;
 }
 
-// Sum over groups of `lanes` neighbouring lanes (a power of two), in every lane.
-__device__ inline float lanes_sum(float x, int lanes)
+// x plus another lane's x, by DPP.
+template <int CTRL> __device__ inline float plus_lane(float x)
 {
-    for (int d = 1; d < lanes; d <<= 1)
-        x += __shfl_xor(x, d);
-    return x;
+    const int o = __builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), CTRL, 0xf, 0xf, true);
+    return x + __uint_as_float((uint32_t)o);
 }
 
-__device__ inline float wave_sum(float x)
+// Sum over groups of `lanes` neighbouring lanes (4, 8, 16, 32 or 64), in every lane of the group:
+// neighbours, pairs, then the mirrored half of 8 and of 16 lanes, then across the rows of 16.
+__device__ inline float lanes_sum(float x, int lanes)
 {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1)
-        x += __shfl_xor(x, d);
+    x = plus_lane<0xb1>(x);  // quad_perm 1 0 3 2
+    x = plus_lane<0x4e>(x);  // quad_perm 2 3 0 1
+    if (lanes >= 8)
+        x = plus_lane<0x141>(x);  // row_half_mirror
+    if (lanes >= 16)
+        x = plus_lane<0x140>(x);  // row_mirror
+    if (lanes >= 32)
+        x += __shfl_xor(x, 16);
+    if (lanes >= 64)
+        x += __shfl_xor(x, 32);
     return x;
 }
 

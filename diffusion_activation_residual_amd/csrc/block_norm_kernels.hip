@@ -4,19 +4,21 @@
 namespace cfz {
 namespace {
 
-constexpr int kThreads = 256;
+// Threads of a work-group whose rows take G threads each: four rows of a wave, or one row.
+constexpr int group_threads(int g) { return g == 64 ? 256 : g; }
 
-// Sum over the threads that hold one row: a wave, or the work-group's four.
+// Sum over the threads that hold one row: a wave, two or four.
 template <int G> __device__ inline float row_sum(float x, float *red)
 {
-    x = wave_sum(x);
+    x = lanes_sum(x, 64);
     if (G == 64)
         return x;
+    const int wave = threadIdx.x >> 6;
     __syncthreads();  // (what was read from red before)
     if ((threadIdx.x & 63) == 0)
-        red[threadIdx.x >> 6] = x;
+        red[wave] = x;
     __syncthreads();
-    return (red[0] + red[1]) + (red[2] + red[3]);
+    return G == 128 ? red[0] + red[1] : (red[0] + red[1]) + (red[2] + red[3]);
 }
 
 // v becomes its norm, in two passes over registers: the mean first, so that nothing cancels in
@@ -48,7 +50,7 @@ __device__ inline void normalise(float (&v)[V][8], const BlockNormOf &n, int col
             }
         }
     }
-    const float f = 1.0f / sqrtf(row_sum<G>(q, red) * inv + n.eps);
+    const float f = rsqrtf(row_sum<G>(q, red) * inv + n.eps);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int at = (i * G + tid) * 8;
@@ -76,11 +78,11 @@ __device__ inline void normalise(float (&v)[V][8], const BlockNormOf &n, int col
 // A row stays in registers from its load to its stores: x and y are read once, r and h written once.
 // G threads hold a row, V vectors of 8 values each.
 template <class X, class Y, int V, int G>
-__global__ __launch_bounds__(kThreads) void residual_norm_kernel(ResidualArgs a)
+__global__ __launch_bounds__(group_threads(G)) void residual_norm_kernel(ResidualArgs a)
 {
     __shared__ float red[4];
-    const int tid = G == 64 ? threadIdx.x & 63 : threadIdx.x;
-    const int64_t row = G == 64 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+    const int tid = threadIdx.x % G;
+    const int64_t row = (int64_t)blockIdx.x * (group_threads(G) / G) + threadIdx.x / G;
     if (row >= a.rows.tokens)
         return;
     const X *x = (const X *)a.x + row * a.xs;
@@ -160,19 +162,16 @@ __global__ __launch_bounds__(kThreads) void residual_norm_kernel(ResidualArgs a)
 template <class X, class Y> hipError_t launch_as(const ResidualArgs &a, hipStream_t st)
 {
     const int64_t t = a.rows.tokens;
-    const bool wide = a.cols > 4096;
-    const int group = wide ? 256 : 64;
-    const int need = (a.cols / 8 + group - 1) / group;
-    const dim3 grid((unsigned)(wide ? t : (t + 3) / 4));
 #define CFZ_NORM_CASE(V, G)                                                                        \
-    if (group == G && need <= V) {                                                                 \
-        residual_norm_kernel<X, Y, V, G><<<grid, kThreads, 0, st>>>(a);                             \
+    if (a.cols <= 8 * V * G) {                                                                     \
+        const dim3 grid((unsigned)(G == 64 ? (t + 3) / 4 : t));                                     \
+        residual_norm_kernel<X, Y, V, G><<<grid, group_threads(G), 0, st>>>(a);                     \
         return hipGetLastError();                                                                  \
     }
     CFZ_NORM_CASE(1, 64)
-    CFZ_NORM_CASE(2, 64)
-    CFZ_NORM_CASE(4, 64)
-    CFZ_NORM_CASE(8, 64)
+    CFZ_NORM_CASE(1, 128)
+    CFZ_NORM_CASE(1, 256)
+    CFZ_NORM_CASE(2, 256)
     CFZ_NORM_CASE(4, 256)
     CFZ_NORM_CASE(8, 256)
 #undef CFZ_NORM_CASE

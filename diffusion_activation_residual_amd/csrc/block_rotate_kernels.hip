@@ -45,6 +45,7 @@ __global__ __launch_bounds__(kThreads) void rotate_kernel(RotateArgs a)
     const int lanes = 1 << a.log2lanes;
     const int unit = lane & (lanes - 1);
     const int head0 = ((part - t.first) * (kRotateUnits * 64) + lane) >> a.log2lanes;
+    const float inv = 1.0f / (float)a.dim;  // (a power of two)
     const int half = a.rot / 2;
     const bool turn = TURN != kStay && unit * 8 < a.rot;
     const bool split = TURN == kHalves && turn;
@@ -92,7 +93,7 @@ __global__ __launch_bounds__(kThreads) void rotate_kernel(RotateArgs a)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 q = fmaf(v[i][j], v[i][j], q);
-            const float f = 1.0f / sqrtf(lanes_sum(q, lanes) / (float)a.dim + a.eps);
+            const float f = rsqrtf(lanes_sum(q, lanes) * inv + a.eps);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 v[i][j] *= f * w[j];

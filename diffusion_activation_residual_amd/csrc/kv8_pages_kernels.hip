@@ -87,6 +87,7 @@ __global__ __launch_bounds__(kWide) void kv8_reserve_kernel(Kv8Pages p, Kv8Reser
 {
     __shared__ int found[kPieces * kWaves];
     __shared__ int sums[kWaves];
+    __shared__ int list[kWide];  // the first free pages; more of them go through memory
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     for (int b = tid; b < p.batch; b += kWide)
         r.source[b] = r.target[b] = -1;
@@ -104,12 +105,28 @@ __global__ __launch_bounds__(kWide) void kv8_reserve_kernel(Kv8Pages p, Kv8Reser
         const int page = p.table[(int64_t)row * p.width + e];
         return names_page(p, page) ? page : -1;
     };
-    bool any = false;
+    // the first free pages' counts are under way while the places are looked up
+    int ahead[kPieces];
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+        const int64_t page = u * kWide + tid;
+        ahead[u] = page < p.pages ? p.refs[page] : 1;
+    }
     int row, e;
     int64_t held;
+    // (a thread's first place is looked up once; few calls have more than one a thread)
+    const int mine = tid < r.places ? place(tid, row, e, held) : -2;
+    const int mine_refs = mine >= 0 ? p.refs[mine] : 0;
+    auto look = [&](int64_t q, int &refs) {
+        const int page = q == tid ? mine : place((int)q, row, e, held);
+        refs = q == tid ? mine_refs : (page >= 0 ? p.refs[page] : 0);
+        return page;
+    };
+    bool any = false;
     for (int64_t q = tid; q < r.places; q += kWide) {
-        const int page = place((int)q, row, e, held);
-        if (page >= 0 && p.refs[page] > 1) {
+        int refs;
+        const int page = look(q, refs);
+        if (refs > 1) {
             any = true;
             fresh_store(r.owner + page, INT_MAX);
             fresh_store(r.writers + page, 0);
@@ -117,8 +134,9 @@ __global__ __launch_bounds__(kWide) void kv8_reserve_kernel(Kv8Pages p, Kv8Reser
     }
     if (__syncthreads_or(any)) {
         for (int64_t q = tid; q < r.places; q += kWide) {
-            const int page = place((int)q, row, e, held);
-            if (page >= 0 && p.refs[page] > 1) {
+            int refs;
+            const int page = look(q, refs);
+            if (refs > 1) {
                 atomicMin(r.owner + page, (int)q);
                 atomicAdd(r.writers + page, 1);
             }
@@ -128,14 +146,16 @@ __global__ __launch_bounds__(kWide) void kv8_reserve_kernel(Kv8Pages p, Kv8Reser
 
     // ranks among the places that need a page
     int64_t total = 0;
+    int mine_rank = -1;
     for (int64_t base = 0; base < r.places; base += kWide) {
         const int64_t q = base + tid;
         bool need = false;
         if (q < r.places) {
-            const int page = place((int)q, row, e, held);
+            int refs;
+            const int page = look(q, refs);
             need = page == -1;
-            if (page >= 0 && p.refs[page] > 1)
-                need = !(p.refs[page] <= fresh_load(r.writers + page) &&
+            if (refs > 1)
+                need = !(refs <= fresh_load(r.writers + page) &&
                          fresh_load(r.owner + page) == (int)q);
         }
         const uint64_t votes = __ballot(need);
@@ -147,8 +167,11 @@ __global__ __launch_bounds__(kWide) void kv8_reserve_kernel(Kv8Pages p, Kv8Reser
             before += w < wave ? sums[w] : 0;
             total += sums[w];
         }
-        if (q < r.places)
-            r.rank[q] = need ? (int)(before + __popcll(votes & ((1ull << lane) - 1))) : -1;
+        const int rank = need ? (int)(before + __popcll(votes & ((1ull << lane) - 1))) : -1;
+        if (base == 0)
+            mine_rank = rank;
+        else if (q < r.places)
+            r.rank[q] = rank;
         __syncthreads();
     }
     if (total == 0) {
@@ -163,7 +186,7 @@ __global__ __launch_bounds__(kWide) void kv8_reserve_kernel(Kv8Pages p, Kv8Reser
 #pragma unroll
         for (int u = 0; u < kPieces; ++u) {
             const int64_t page = base + u * kWide + tid;
-            refs[u] = page < p.pages ? p.refs[page] : 1;
+            refs[u] = base == 0 ? ahead[u] : (page < p.pages ? p.refs[page] : 1);
         }
         uint64_t votes[kPieces];
 #pragma unroll
@@ -197,8 +220,13 @@ __global__ __launch_bounds__(kWide) void kv8_reserve_kernel(Kv8Pages p, Kv8Reser
                 before += at % 4 == j ? own : 0;
             }
             const int64_t rank = have + before + __popcll(votes[u] & ((1ull << lane) - 1));
-            if (refs[u] <= 0 && rank < total)
-                fresh_store(r.list + rank, (int)(base + u * kWide + tid));
+            if (refs[u] <= 0 && rank < total) {
+                const int page = (int)(base + u * kWide + tid);
+                if (rank < kWide)
+                    list[rank] = page;
+                else
+                    fresh_store(r.list + rank, page);
+            }
         }
         have += all;
         __syncthreads();
@@ -208,11 +236,11 @@ __global__ __launch_bounds__(kWide) void kv8_reserve_kernel(Kv8Pages p, Kv8Reser
     if (have < total)
         return;
     for (int64_t q = tid; q < r.places; q += kWide) {
-        const int rank = r.rank[q];
+        const int rank = q == tid ? mine_rank : r.rank[q];
         if (rank < 0)
             continue;
         const int old = place((int)q, row, e, held);
-        const int page = fresh_load(r.list + rank);
+        const int page = rank < kWide ? list[rank] : fresh_load(r.list + rank);
         p.table[(int64_t)row * p.width + e] = page;
         p.refs[page] = 1;
         if (old >= 0) {
@@ -257,39 +285,62 @@ __global__ __launch_bounds__(kThreads) void kv8_pack_count_kernel(Kv8Pages p, Kv
 }
 
 // With n pages in use, the free pages below n in ascending order meet the pages in use from n on in
-// descending order: both numbers follow from how many pages in use lie before a page.
+// descending order: both numbers follow from how many pages in use lie before a page.  One chunk
+// counts itself.
 __global__ __launch_bounds__(kThreads) void kv8_pack_lists_kernel(Kv8Pages p, Kv8Compact k, int chunks)
 {
+    constexpr int N = kKv8RefsChunk / kThreads;
+    static_assert(N * kThreads / 64 == 64, "a lane of a wave a vote");
     __shared__ int red[4];
+    __shared__ int found[64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    int all = 0, mine = 0;
-    for (int i = tid; i < chunks; i += kThreads) {
-        const int c = k.counts[i];
-        all += c;
-        mine += i < (int)blockIdx.x ? c : 0;
+    const int64_t base = (int64_t)blockIdx.x * kKv8RefsChunk;
+    int refs[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int64_t page = base + i * kThreads + tid;
+        refs[i] = page < p.pages ? p.refs[page] : 0;
     }
-    const int n = block_sum(all, red);
-    int before = block_sum(mine, red);
+    int n = 0, before = 0;
+    if (chunks > 1) {
+        int all = 0, mine = 0;
+        for (int i = tid; i < chunks; i += kThreads) {
+            const int c = k.counts[i];
+            all += c;
+            mine += i < (int)blockIdx.x ? c : 0;
+        }
+        n = block_sum(all, red);
+        before = block_sum(mine, red);
+    }
+    uint64_t votes[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        votes[i] = __ballot(refs[i] > 0);
+        if (lane == 0)
+            found[i * 4 + wave] = __popcll(votes[i]);
+    }
+    __syncthreads();
+    const int own = found[lane];
+    int incl = own;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(incl, d);
+        incl += lane >= d ? o : 0;
+    }
+    if (chunks == 1)
+        n = __shfl(incl, 63);
     if (blockIdx.x == 0 && tid == 0) {
         k.live[0] = n;
         if (n == 0)
             k.moves[0] = 0;
     }
-    const int64_t base = (int64_t)blockIdx.x * kKv8RefsChunk;
-    for (int i = 0; i < kKv8RefsChunk / kThreads; ++i) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
         const int64_t page = base + i * kThreads + tid;
-        const bool in = page < p.pages, used = in && p.refs[page] > 0;
-        const uint64_t votes = __ballot(used);
-        if (lane == 0)
-            red[wave] = __popcll(votes);
-        __syncthreads();
-        int rank = before + __popcll(votes & ((1ull << lane) - 1));
-        for (int w = 0; w < 4; ++w) {
-            rank += w < wave ? red[w] : 0;
-            before += red[w];
-        }
-        __syncthreads();
-        if (!in)
+        const bool used = refs[i] > 0;
+        const int rank = before + __shfl(incl - own, i * 4 + wave) +
+                         __popcll(votes[i] & ((1ull << lane) - 1));
+        if (page >= p.pages)
             continue;
         if (page < n) {
             if (!used)
@@ -444,7 +495,8 @@ int kv8_compact_chunks(const Kv8Pages &p)
 hipError_t launch_kv8_compact(const Kv8Pages &p, const Kv8Compact &k, hipStream_t st)
 {
     const int chunks = kv8_compact_chunks(p);
-    kv8_pack_count_kernel<<<dim3((unsigned)chunks), kThreads, 0, st>>>(p, k);
+    if (chunks > 1)
+        kv8_pack_count_kernel<<<dim3((unsigned)chunks), kThreads, 0, st>>>(p, k);
     kv8_pack_lists_kernel<<<dim3((unsigned)chunks), kThreads, 0, st>>>(p, k, chunks);
     const int64_t places = (int64_t)p.batch * p.width, moves = p.pages / 2;
     const int64_t n = ((places > moves ? places : moves) + kThreads - 1) / kThreads;  // (>= 1)

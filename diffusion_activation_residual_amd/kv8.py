@@ -514,8 +514,8 @@ class Pages:
         batch = self.table.shape[0]
         counts = _ints(counts, (batch,), self.device, "counts")
         need = _lib.cfz_kv8_reserve_workspace_bytes(self._ref, max_new)
-        source, target, missing = _empty_on(self.device, stream, 2 * batch + 1, torch.int32).split(
-            (batch, batch, 1))
+        source, target, missing = (_empty_on(self.device, stream, n, torch.int32)
+                                   for n in (batch, batch, 1))
         workspace, have = self._workspace(need, workspace, stream)
         _queue(_lib.cfz_kv8_reserve, self.device, stream, self._ref, counts, max_new,
                source.data_ptr(), target.data_ptr(), missing.data_ptr(), workspace, have)
@@ -527,8 +527,8 @@ class Pages:
         which are then 0 .. live - 1."""
         most = self.refs.numel() // 2
         need = _lib.cfz_kv8_compact_workspace_bytes(self._ref)
-        source, target, live, count = _empty_on(self.device, stream, 2 * most + 2,
-                                                torch.int32).split((most, most, 1, 1))
+        source, target, live, count = (_empty_on(self.device, stream, n, torch.int32)
+                                       for n in (most, most, 1, 1))
         workspace, have = self._workspace(need, workspace, stream)
         _queue(_lib.cfz_kv8_compact, self.device, stream, self._ref, source.data_ptr(),
                target.data_ptr(), live.data_ptr(), count.data_ptr(), workspace, have)

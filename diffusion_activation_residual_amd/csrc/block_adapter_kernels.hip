@@ -160,13 +160,14 @@ __global__ __launch_bounds__(64 * W) void adapter_down_kernel(AdapterArgs a)
     // groups of four steps g0 .. g1 - 1, from one in their midst on and round
     const int g0 = steps / 4 * wave / W, g1 = steps / 4 * (wave + 1) / W;
     int step = 0;  // the one under way farthest ahead
-    uint4 xv[4][TM], wv[2][NB];
+    constexpr int XS = TM == 4 ? 2 : 4;  // steps of x under way
+    uint4 xv[XS][TM], wv[2][NB];
     auto load_x = [&](int step, auto at) {
         const int k = step * 32;
         const bool in = k + piece * 8 < a.cols_in;
 #pragma unroll
         for (int t = 0; t < TM; ++t)
-            xv[decltype(at)::value][t] = *(const uint4 *)(x[t] + (in ? k : -piece * 8));
+            xv[decltype(at)::value % XS][t] = *(const uint4 *)(x[t] + (in ? k : -piece * 8));
     };
     auto load_a = [&](int step, auto at) {
         // (a block past the last one repeats it: its sums are not kept)
@@ -180,7 +181,7 @@ __global__ __launch_bounds__(64 * W) void adapter_down_kernel(AdapterArgs a)
         const uint32_t keep = step * 32 + piece * 8 < a.cols_in ? ~0u : 0u;
 #pragma unroll
         for (int t = 0; t < TM; ++t) {
-            const uint4 v = xv[decltype(xat)::value][t];
+            const uint4 v = xv[decltype(xat)::value % XS][t];
             put[t * 64] = make_uint4(v.x & keep, v.y & keep, v.z & keep, v.w & keep);
         }
         wave_sync();
@@ -203,22 +204,27 @@ __global__ __launch_bounds__(64 * W) void adapter_down_kernel(AdapterArgs a)
         step = (g0 + blockIdx.x % (g1 - g0)) * 4;
         load_x(step, i0);
         load_a(step, i0);
-        load_x(step + 1, i1);
-        load_x(step + 2, i2);
+        if constexpr (XS == 4) {
+            load_x(step + 1, i1);
+            load_x(step + 2, i2);
+        }
     }
     for (int g = g0; g < g1; ++g) {
         // (past the last group the loads repeat the first: no load is under a condition)
         const int next = step + 4 < g1 * 4 ? step + 4 : g0 * 4;
-        load_x(step + 3, i3);
+        if constexpr (XS == 4)
+            load_x(step + 3, i3);
+        else
+            load_x(step + 1, i1);
         load_a(step + 1, i1);
         multiply(step, i0, i0);
-        load_x(next, i0);
+        load_x(XS == 4 ? next : step + 2, i0);
         load_a(step + 2, i0);
         multiply(step + 1, i1, i1);
-        load_x(next + 1, i1);
+        load_x(XS == 4 ? next + 1 : step + 3, i1);
         load_a(step + 3, i1);
         multiply(step + 2, i2, i0);
-        load_x(next + 2, i2);
+        load_x(XS == 4 ? next + 2 : next, i2);
         load_a(next, i0);
         multiply(step + 3, i3, i1);
         step = next;
@@ -471,7 +477,9 @@ template <class T, int TM, int W> hipError_t down_as(const AdapterArgs &a, hipSt
     CFZ_DOWN_CASE(2)
     CFZ_DOWN_CASE(4)
     CFZ_DOWN_CASE(6)
-    CFZ_DOWN_CASE(8)
+    if constexpr (TM < 4) {
+        CFZ_DOWN_CASE(8)
+    }
     if constexpr (TM == 1) {
         CFZ_DOWN_CASE(12)
         CFZ_DOWN_CASE(16)
@@ -494,7 +502,9 @@ template <class T, class Y> hipError_t up_as(const AdapterArgs &a, hipStream_t s
 
 template <class T> hipError_t add_as(const AdapterArgs &a, bool f32, hipStream_t st)
 {
-    const hipError_t e = a.tall ? down_as<T, 2, 4>(a, st) : down_as<T, 1, 8>(a, st);
+    const hipError_t e = a.tall == 4   ? down_as<T, 4, 8>(a, st)
+                         : a.tall == 2 ? down_as<T, 2, 4>(a, st)
+                                       : down_as<T, 1, 8>(a, st);
     if (e != hipSuccess)
         return e;
     return f32 ? up_as<T, float>(a, st) : up_as<T, T>(a, st);
@@ -506,13 +516,15 @@ int64_t adapter_tiles(const AdapterArgs &a, int rows) { return a.rows.tokens / r
 
 int64_t adapter_groups(const AdapterArgs &a)
 {
-    const int64_t down = adapter_tiles(a, a.tall ? 32 : 16);
+    const int64_t down = adapter_tiles(a, 16 * a.tall);
     const int64_t up = adapter_tiles(a, kUpRows) * a.col_tiles;
     return down > up ? down : up;
 }
 
-// 32 tokens a tile of the first product read A half as often as 16; 16, and twice the waves, where
-// sequences are too short to fill them, or the sums of more than 128 adapter rows would not fit the registers.
+// The more tokens a tile of the first product has, the less often A is read: 64, where sequences fill such
+// tiles and half of the card's 256 units get one, and the sums of up to 96 adapter rows fit the registers
+// (2 x 4388 rows of 1920 at 96 adapter rows: 15.6 us, with 32 tokens 18.1; ragged prompts of 4096 columns at 64:
+// 32.8 and 37.7); else 32, up to 128 adapter rows; else 16.  Four waves a tile of 32, eight of the others.
 //
 // The second product's work-groups take 512 columns of a slice, or 256 where the rank is over 64 (what B
 // takes of the registers).
@@ -524,7 +536,11 @@ void adapter_plan(AdapterArgs &a)
         a.first_tile[i] = a.col_tiles;
         a.col_tiles += (a.first_col[i + 1] - a.first_col[i] + cols - 1) / cols;
     }
-    a.tall = a.rows.tokens >= 32 * (int64_t)a.rows.batch && a.down <= 128;
+    const int64_t t = a.rows.tokens, most = t / (a.rows.batch > 0 ? a.rows.batch : 1);
+    if (a.down <= 96 && most >= 64 && adapter_tiles(a, 64) >= 128)
+        a.tall = 4;
+    else
+        a.tall = a.down <= 128 && most >= 32 ? 2 : 1;
 }
 
 int64_t adapter_pieces(const AdapterArgs &a)

@@ -94,7 +94,7 @@ struct AdapterArgs {
     int64_t xs, ys, os;
     uint16_t *hi, *lo;  // [tokens][down]: scale x A^T as the sum of two numbers of the type
     float *back;        // [tokens][slices]: what it was multiplied by, turned round (fp16)
-    bool tall;  // 32 tokens a tile of the first product, else 16
+    int tall;  // 16 tokens times this a tile of the first product
 };
 void adapter_plan(AdapterArgs &a);
 int64_t adapter_tiles(const AdapterArgs &a, int rows);

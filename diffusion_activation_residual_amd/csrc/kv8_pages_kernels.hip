@@ -196,7 +196,8 @@ __global__ __launch_bounds__(kWide) void kv8_reserve_kernel(Kv8Pages p, Kv8Reser
                 found[u * kWaves + wave] = __popcll(votes[u]);
         }
         __syncthreads();
-        // running sums of the kPieces x kWaves counts, 4 a lane of every wave
+        // the counts become how many free pages lie before, 4 a lane of every wave (each for itself, the first
+        // writes them back)
         int c[4], sum = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -210,16 +211,17 @@ __global__ __launch_bounds__(kWide) void kv8_reserve_kernel(Kv8Pages p, Kv8Reser
             incl += lane >= d ? o : 0;
         }
         const int all = __shfl(incl, 63);
+        __syncthreads();
+        if (wave == 0) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                found[lane * 4 + j] = incl - sum + c[j];
+        }
+        __syncthreads();
 #pragma unroll
         for (int u = 0; u < kPieces; ++u) {
-            const int at = u * kWaves + wave;
-            int before = __shfl(incl - sum, at / 4);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int own = __shfl(c[j], at / 4);
-                before += at % 4 == j ? own : 0;
-            }
-            const int64_t rank = have + before + __popcll(votes[u] & ((1ull << lane) - 1));
+            const int64_t rank =
+                have + found[u * kWaves + wave] + __popcll(votes[u] & ((1ull << lane) - 1));
             if (refs[u] <= 0 && rank < total) {
                 const int page = (int)(base + u * kWide + tid);
                 if (rank < kWide)
@@ -287,37 +289,49 @@ __global__ __launch_bounds__(kThreads) void kv8_pack_count_kernel(Kv8Pages p, Kv
 // With n pages in use, the free pages below n in ascending order meet the pages in use from n on in
 // descending order: both numbers follow from how many pages in use lie before a page.  One chunk
 // counts itself.
-__global__ __launch_bounds__(kThreads) void kv8_pack_lists_kernel(Kv8Pages p, Kv8Compact k, int chunks)
+__global__ __launch_bounds__(kWide) void kv8_pack_lists_kernel(Kv8Pages p, Kv8Compact k, int chunks)
 {
-    constexpr int N = kKv8RefsChunk / kThreads;
-    static_assert(N * kThreads / 64 == 64, "a lane of a wave a vote");
-    __shared__ int red[4];
+    constexpr int N = kKv8RefsChunk / kWide;
+    static_assert(N * kWaves == 64, "a lane of a wave a vote");
+    __shared__ int red[2][kWaves];
     __shared__ int found[64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t base = (int64_t)blockIdx.x * kKv8RefsChunk;
     int refs[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const int64_t page = base + i * kThreads + tid;
+        const int64_t page = base + i * kWide + tid;
         refs[i] = page < p.pages ? p.refs[page] : 0;
     }
     int n = 0, before = 0;
     if (chunks > 1) {
         int all = 0, mine = 0;
-        for (int i = tid; i < chunks; i += kThreads) {
+        for (int i = tid; i < chunks; i += kWide) {
             const int c = k.counts[i];
             all += c;
             mine += i < (int)blockIdx.x ? c : 0;
         }
-        n = block_sum(all, red);
-        before = block_sum(mine, red);
+#pragma unroll
+        for (int d = 32; d >= 1; d >>= 1) {
+            all += __shfl_xor(all, d);
+            mine += __shfl_xor(mine, d);
+        }
+        if (lane == 0) {
+            red[0][wave] = all;
+            red[1][wave] = mine;
+        }
+        __syncthreads();
+        for (int w = 0; w < kWaves; ++w) {
+            n += red[0][w];
+            before += red[1][w];
+        }
     }
     uint64_t votes[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         votes[i] = __ballot(refs[i] > 0);
         if (lane == 0)
-            found[i * 4 + wave] = __popcll(votes[i]);
+            found[i * kWaves + wave] = __popcll(votes[i]);
     }
     __syncthreads();
     const int own = found[lane];
@@ -336,9 +350,9 @@ __global__ __launch_bounds__(kThreads) void kv8_pack_lists_kernel(Kv8Pages p, Kv
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const int64_t page = base + i * kThreads + tid;
+        const int64_t page = base + i * kWide + tid;
         const bool used = refs[i] > 0;
-        const int rank = before + __shfl(incl - own, i * 4 + wave) +
+        const int rank = before + __shfl(incl - own, i * kWaves + wave) +
                          __popcll(votes[i] & ((1ull << lane) - 1));
         if (page >= p.pages)
             continue;
@@ -497,7 +511,7 @@ hipError_t launch_kv8_compact(const Kv8Pages &p, const Kv8Compact &k, hipStream_
     const int chunks = kv8_compact_chunks(p);
     if (chunks > 1)
         kv8_pack_count_kernel<<<dim3((unsigned)chunks), kThreads, 0, st>>>(p, k);
-    kv8_pack_lists_kernel<<<dim3((unsigned)chunks), kThreads, 0, st>>>(p, k, chunks);
+    kv8_pack_lists_kernel<<<dim3((unsigned)chunks), kWide, 0, st>>>(p, k, chunks);
     const int64_t places = (int64_t)p.batch * p.width, moves = p.pages / 2;
     const int64_t n = ((places > moves ? places : moves) + kThreads - 1) / kThreads;  // (>= 1)
     kv8_pack_apply_kernel<<<dim3((unsigned)n), kThreads, 0, st>>>(p, k);

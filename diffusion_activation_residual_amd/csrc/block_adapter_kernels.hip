@@ -282,9 +282,9 @@ __global__ __launch_bounds__(64 * W) void adapter_down_kernel(AdapterArgs a)
                 const f32x4 u = *(const f32x4 *)&s.sum[row][k];
                 top = fmaxf(fmaxf(fmaxf(fabsf(u[0]), fabsf(u[1])), fmaxf(fabsf(u[2]), fabsf(u[3]))), top);
             }
-            // a power of two that brings the largest into 1 .. 2 (0 and what is not finite: 1)
+            // a power of two that brings the largest into 1 .. 4 (0 stays; what is not finite: 1)
             int e = (int)(__float_as_uint(top) >> 23) - 127;
-            e = e > -120 && e < 120 ? e : 0;
+            e = e > 127 ? 0 : (e > 126 ? 126 : (e < -126 ? -126 : e));
             f = __uint_as_float((uint32_t)(127 - e) << 23);
             if (r == slice * a.rank)
                 a.back[(row0 + row) * a.slices + slice] = __uint_as_float((uint32_t)(127 + e) << 23);

@@ -168,16 +168,16 @@ cfz_status cfz_residual_norm(const cfz_residual *r, void *hip_stream)
     if ((r->r && r->r == r->x && r->r_stride != r->x_stride) ||
         (r->h && r->h == r->y && r->h_stride != r->y_stride))
         return fail(CFZ_ERR_SHAPE, "in place, the strides must be the same");
-    if (r->cols > 512 && r->tokens >= cfz::kBlockMaxGroups)
+    a.cols = r->cols;
+    if (cfz::residual_groups(a) >= cfz::kBlockMaxGroups)
         return fail(CFZ_ERR_SHAPE, "the call needs %lld work-groups (limit 2^23)",
-                    (long long)r->tokens);
+                    (long long)cfz::residual_groups(a));
     if (!r->y && (r->gate.data || r->after.kind != CFZ_NORM_NONE))
         return fail(CFZ_ERR_NULL, "a gate and a norm of y need y");
     if (!r->r && !r->h)
         return fail(CFZ_ERR_NULL, "one of r and h is required");
     if (!r->x)
         return fail(CFZ_ERR_NULL, "x is required");
-    a.cols = r->cols;
     a.x = r->x, a.y = r->y, a.r = r->r, a.h = r->h;
     a.xs = r->x_stride, a.ys = r->y_stride, a.rs = r->r_stride, a.hs = r->h_stride;
     a.gate_scale = r->gate_scale;

@@ -41,6 +41,7 @@ struct ResidualArgs {
     BlockVec gate, scale, shift;
     BlockNormOf after, before;
 };
+int64_t residual_groups(const ResidualArgs &a);
 hipError_t launch_residual_norm(const ResidualArgs &a, int x_dtype, int y_dtype, hipStream_t st);
 
 struct TableArgs {

@@ -161,10 +161,9 @@ __global__ __launch_bounds__(group_threads(G)) void residual_norm_kernel(Residua
 
 template <class X, class Y> hipError_t launch_as(const ResidualArgs &a, hipStream_t st)
 {
-    const int64_t t = a.rows.tokens;
+    const dim3 grid((unsigned)residual_groups(a));
 #define CFZ_NORM_CASE(V, G)                                                                        \
     if (a.cols <= 8 * V * G) {                                                                     \
-        const dim3 grid((unsigned)(G == 64 ? (t + 3) / 4 : t));                                     \
         residual_norm_kernel<X, Y, V, G><<<grid, group_threads(G), 0, st>>>(a);                     \
         return hipGetLastError();                                                                  \
     }
@@ -179,6 +178,12 @@ template <class X, class Y> hipError_t launch_as(const ResidualArgs &a, hipStrea
 }
 
 }  // namespace
+
+// Four rows a work-group where a wave holds one (up to 512 columns), else one.
+int64_t residual_groups(const ResidualArgs &a)
+{
+    return a.cols <= 512 ? (a.rows.tokens + 3) / 4 : a.rows.tokens;
+}
 
 hipError_t launch_residual_norm(const ResidualArgs &a, int x_dtype, int y_dtype, hipStream_t st)
 {

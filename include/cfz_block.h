@@ -50,7 +50,8 @@ typedef struct {
  * sum is not stored; h NULL: no second norm (before is then not looked at).  x_dtype is
  * y_dtype or F32.  after and before may be of kind NONE.
  * cols: a multiple of 8, 8 .. 16384; row strides in elements, >= cols, multiples of 16
- * bytes.  0 <= tokens < 2^31, 1 <= batch <= 65535.
+ * bytes.  0 <= tokens < 2^31, 1 <= batch <= 65535; 2^23 or more work-groups (of a row, or of four up
+ * to 512 columns) are refused.
  * offsets: [batch + 1] int32, ascending: rows offsets[b] .. offsets[b + 1] - 1 belong to item b;
  * rows outside every item are left as they are in r and h.  NULL: batch equal runs (tokens a
  * multiple of batch).
@@ -136,8 +137,8 @@ typedef struct {
  * starts[b] + i (starts NULL: i).  Positions outside the table take its nearest row.
  * head_dim in {32, 64, 128, 256}, rot_dim a multiple of 8 up to it, heads 1 .. 1024 each.
  * offsets: [batch + 1] int32 as above, rows outside are left as they are in out; NULL: one
- * sequence (batch = 1).  0 <= tokens < 2^31, 1 <= batch <= 65535; 2^23 or more work-groups (of
- * four tokens x up to 2048 values) are refused.
+ * sequence (batch = 1).  0 <= tokens < 2^31, 1 <= batch <= 65535; 2^23 or more work-groups (of four
+ * runs of up to 2048 values of a token in a tensor) are refused.
  * Errors: as cfz_residual_norm. */
 cfz_status cfz_rotate(int32_t count, const cfz_rotate_rows *tensors, cfz_kv8_dtype dtype,
                       int32_t head_dim, int64_t tokens, int32_t batch, const int32_t *offsets,
@@ -180,7 +181,8 @@ cfz_status cfz_adapters_put(const cfz_adapters *adapters, int32_t first, int32_t
  * stride; other overlaps are not allowed.  Rows of no sequence, and rows past a sequence's first
  * max_rows, are neither read nor written.  The products accumulate in fp32; x a^T enters the second one as the sum of
  * two numbers of `dtype` (off by 2^-16 of itself for BF16, 2^-21 of its row's largest value for F16).
- * Results do not depend on the run.
+ * Results do not depend on the run.  2^23 or more work-groups (of 64 tokens x 512 columns of a slice, 256
+ * where the rank is over 64) are refused.
  * workspace: cfz_adapters_workspace_bytes(...) bytes, 256-byte aligned, overwritten; calls that may
  * run at the same time need one each.
  * Errors: CFZ_ERR_NULL, CFZ_ERR_SHAPE, CFZ_ERR_UNSUPPORTED, CFZ_ERR_ALIGN, CFZ_ERR_WORKSPACE,

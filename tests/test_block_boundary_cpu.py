@@ -90,7 +90,9 @@ def residual(**kw):
     (dict(r_stride=72), SHAPE), (dict(h_stride=72), SHAPE),
     (dict(cols=8192, tokens=1 << 23, x_stride=8192, y_stride=8192, r_stride=8192, h_stride=8192,
           gate=items(stride=0), scale=items(stride=0), shift=items(stride=0)), SHAPE),
+    (dict(tokens=1 << 25), SHAPE), (dict(tokens=(1 << 25) - 4, x=None), NULL),
     (dict(tokens=0, x=None, batch=5), cfz.CFZ_OK),
+    (dict(tokens=0, x=None, y=None, r=None, h=None, gate=items()), cfz.CFZ_OK),
 ])
 def test_norm_refusals(kw, status):
     assert residual(**kw) == status

@@ -125,6 +125,19 @@ def test_values_at_the_types_ends():
     assert torch.equal(w.add(x[:4], y[:4] + 3, ints([0]), ints([0, 4]), 4), y[:4] + 3)
 
 
+@pytest.mark.parametrize("real", ["bf16", "f16"])
+@pytest.mark.parametrize("power", [-100, -60, 60, 100])
+def test_scales_of_any_size(real, power):
+    """h far outside of fp16's range either way; rows that it leaves in fp32's range are right."""
+    g = Gen(power + 200)
+    w = make(g, 1, 64, [64], 8, real)
+    w.scale.fill_(2.0 ** power)
+    x, y = g(20, 64, dtype=REAL[real]), torch.zeros(20, 64, device=DEV)
+    out = w.add(x, y, ints([0]), ints([0, 20]), 20)
+    check(w, x, y, out, [0], [0, 20], real)
+    assert out.any() and out.isfinite().all()
+
+
 def test_nothing_to_add():
     g = Gen(9)
     w = make(g, 2, 64, [64], 8, "bf16")
@@ -214,3 +227,37 @@ def test_streams_and_graphs():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(kept, w.add(x, y, ids, off, 19))
+
+
+def test_rows_past_four_gigabytes():
+    from test_gpu_block import far_rows
+    g = Gen(31)
+    w = make(g, 2, 128, [64], 16, "bf16")
+    near, y = g(18, 128, dtype=torch.bfloat16), g(18, 64, dtype=torch.bfloat16)
+    x, z = far_rows(18, 128, torch.bfloat16), far_rows(18, 64, torch.bfloat16)
+    x.copy_(near)
+    z.copy_(y)
+    args = (ints([1, 0]), ints([0, 3, 18]), 18)
+    want = w.add(near, y, *args)
+    assert torch.equal(w.add(x, z, *args, out=z), want)
+
+
+def test_two_calls_at_once():
+    """On two streams, each with memory of its own, over and over; equal to one after the other."""
+    g = Gen(32)
+    w = make(g, 3, 1920, [640, 640], 32, "bf16")
+    jobs = []
+    for counts in ([700, 300], [64, 1, 500, 40]):
+        off = ints(np.concatenate([[0], np.cumsum(counts)]))
+        n = sum(counts)
+        jobs.append((g(n, 1920, dtype=torch.bfloat16), g(n, 1280, dtype=torch.bfloat16),
+                     ints(np.arange(len(counts)) % 3), off, max(counts)))
+    want = [w.add(*j) for j in jobs]
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(10):
+        got += [(i, w.add(*j, stream=s)) for i, (j, s) in enumerate(zip(jobs, streams))]
+    torch.cuda.synchronize()
+    assert all(torch.equal(t, want[i]) for i, t in got)

@@ -325,3 +325,25 @@ def test_streams_and_graphs():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(kept, step())), i
+
+
+def far_rows(rows, width, dtype, step=1 << 28):
+    """Rows so far apart that their elements pass 2^32."""
+    return torch.empty((rows - 1) * step + width, dtype=dtype, device=DEV).as_strided((rows, width),
+                                                                                      (step, 1))
+
+
+def test_rows_past_four_gigabytes():
+    g = Gen(30)
+    near, y = g(18, 256, dtype=torch.bfloat16), g(18, 256, dtype=torch.bfloat16)
+    x, h = far_rows(18, 256, torch.bfloat16), far_rows(18, 256, torch.bfloat16)
+    x.copy_(near)
+    before = block.Norm("rms", 1e-6)
+    want = block.residual_norm(near, y, before=before)
+    r, n = block.residual_norm(x, y, before=before, out=x, normed=h)
+    assert torch.equal(r, want[0]) and torch.equal(n, want[1])
+    x.copy_(near)
+    turn = kv8.Rotation(*table(20, 64))
+    (want,) = block.rotate([near.view(18, 4, 64)], turn)
+    (got,) = block.rotate([x.unflatten(1, (4, 64))], turn, outs=[h.unflatten(1, (4, 64))])
+    assert torch.equal(got, want)

@@ -117,9 +117,9 @@ __global__ __launch_bounds__(256) void adapter_put_kernel(AdapterArgs a, const u
 // steps of 32 at a time, and their sums are added in LDS, half of the waves at a time.  The matrix
 // instructions' rows are A's and their columns the tokens.  An operand's lanes are 16 different rows: read
 // so from rows in memory, each lane's 16 bytes are an access of their own, and the first-level cache gives
-// 16 bytes a clock.  So A is laid out once as the instructions take it, and of x four neighbouring
-// lanes read 64 bytes of a row, which the wave turns round in LDS, a row's four pieces shifted by its
-// number so that no bank is met twice.  Four steps of x and two of A are under way.  Tiles start their runs at
+// 16 bytes a clock.  So A is laid out once as the instructions take it, and of x eight neighbouring
+// lanes read 128 bytes of a row, which the wave turns round in LDS, a row's eight pieces shifted by its
+// number so that no bank is met twice.  Two or four steps are under way.  Tiles start their runs at
 // different places, so that rows a power of two apart are not all read from the same channels.
 //
 // h leaves as the sum of two 16-bit numbers, the operands of the second product: that leaves 2^-16 of it
@@ -131,7 +131,7 @@ __global__ __launch_bounds__(64 * W) void adapter_down_kernel(AdapterArgs a)
     constexpr int kBlocks = NB * TM, kHalf = W / 2;
     constexpr int kRow = NB * 16 + 4;  // of the sums in LDS
     __shared__ union {
-        uint4 turn[W][TM][64];
+        uint4 turn[W][TM][128];
         f32x4 part[kHalf][kBlocks][64];
         float sum[TM * 16][kRow];
     } s;
@@ -141,16 +141,19 @@ __global__ __launch_bounds__(64 * W) void adapter_down_kernel(AdapterArgs a)
     if (!find_tile<16 * TM>(a, blockIdx.x, row0, n, id) || id < 0)
         return;
     const int m = lane & 15, q = lane >> 4;
-    const int r = lane >> 2, piece = lane & 3;  // row of a block and its 16 bytes, as they are read
-    const T *x[TM];
+    const int r = lane >> 3, piece = lane & 7;  // of half a block: row and 16 bytes, as they are read
+    const T *x[TM][2];
 #pragma unroll
     for (int t = 0; t < TM; ++t)
-        // (rows past the tile's end repeat the last one: their sums are not kept)
-        x[t] = (const T *)a.x + (row0 + (t * 16 + r < n ? t * 16 + r : n - 1)) * a.xs + piece * 8;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            // (rows past the tile's end repeat the last one: their sums are not kept)
+            const int row = t * 16 + i * 8 + r;
+            x[t][i] = (const T *)a.x + (row0 + (row < n ? row : n - 1)) * a.xs + piece * 8;
+        }
     const int steps = down_steps(a), blocks = (a.down + 15) / 16;
     const uint4 *w = (const uint4 *)a.a + (int64_t)id * blocks * steps * 64;
-    uint4 *put = &s.turn[wave][0][r * 4 + (piece ^ ((r >> 2) & 3))];
-    const uint4 *get = &s.turn[wave][0][m * 4 + (q ^ ((m >> 2) & 3))];
+    uint4 *lds = s.turn[wave][0];
     f32x4 acc[TM][NB];
 #pragma unroll
     for (int t = 0; t < TM; ++t)
@@ -160,73 +163,88 @@ __global__ __launch_bounds__(64 * W) void adapter_down_kernel(AdapterArgs a)
     // groups of four steps g0 .. g1 - 1, from one in their midst on and round
     const int g0 = steps / 4 * wave / W, g1 = steps / 4 * (wave + 1) / W;
     int step = 0;  // the one under way farthest ahead
-    constexpr int XS = TM == 4 ? 2 : 4;  // steps of x under way
-    uint4 xv[XS][TM], wv[2][NB];
+    // pairs of steps of x and steps of A in registers, as many as they hold beside the sums
+    constexpr int XP = TM == 4 && NB > 4 ? 1 : 2, AS = NB > 4 ? 2 : 4;
+    uint4 xv[XP][TM][2], wv[AS][NB];
     auto load_x = [&](int step, auto at) {
         const int k = step * 32;
         const bool in = k + piece * 8 < a.cols_in;
 #pragma unroll
         for (int t = 0; t < TM; ++t)
-            xv[decltype(at)::value % XS][t] = *(const uint4 *)(x[t] + (in ? k : -piece * 8));
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                xv[decltype(at)::value % XP][t][i] = *(const uint4 *)(x[t][i] + (in ? k : -piece * 8));
     };
     auto load_a = [&](int step, auto at) {
         // (a block past the last one repeats it: its sums are not kept)
 #pragma unroll
         for (int j = 0; j < NB; ++j)
-            wv[decltype(at)::value][j] =
+            wv[decltype(at)::value % AS][j] =
                 (w + ((int64_t)(j < blocks ? j : blocks - 1) * steps + step) * 64)[lane];
     };
-    auto multiply = [&](int step, auto xat, auto wat) {
+    // (past the last group the loads repeat the first: no load is under a condition)
+    int next = 0;
+    auto ahead = [&](auto at) {
+        constexpr int I = decltype(at)::value;
+        return I < 4 ? step + I : next + I - 4;
+    };
+    auto put = [&](auto at) {
         // past the last column zeros
-        const uint32_t keep = step * 32 + piece * 8 < a.cols_in ? ~0u : 0u;
+        constexpr int I = decltype(at)::value;
+        const uint32_t keep = (step + 2 * I) * 32 + piece * 8 < a.cols_in ? ~0u : 0u;
 #pragma unroll
-        for (int t = 0; t < TM; ++t) {
-            const uint4 v = xv[decltype(xat)::value % XS][t];
-            put[t * 64] = make_uint4(v.x & keep, v.y & keep, v.z & keep, v.w & keep);
-        }
-        wave_sync();
+        for (int t = 0; t < TM; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint4 v = xv[I % XP][t][i];
+                const int row = i * 8 + r;
+                lds[t * 128 + row * 8 + (piece ^ (row >> 1))] =
+                    make_uint4(v.x & keep, v.y & keep, v.z & keep, v.w & keep);
+            }
+    };
+    auto multiply = [&](auto at) {
+        constexpr int I = decltype(at)::value;
+        constexpr std::integral_constant<int, I + AS - 1> ia{};
+        load_a(ahead(ia), ia);
         uint4 xo[TM];
 #pragma unroll
         for (int t = 0; t < TM; ++t)
-            xo[t] = get[t * 64];
+            xo[t] = lds[t * 128 + m * 8 + ((I % 2 * 4 + q) ^ (m >> 1))];
 #pragma unroll
         for (int j = 0; j < NB; ++j)
 #pragma unroll
             for (int t = 0; t < TM; ++t)
-                acc[t][j] = Mfma<T>::mul(wv[decltype(wat)::value][j], xo[t], acc[t][j]);
+                acc[t][j] = Mfma<T>::mul(wv[I % AS][j], xo[t], acc[t][j]);
+    };
+    auto pair = [&](auto at) {
+        constexpr int I = decltype(at)::value;
+        constexpr std::integral_constant<int, 2 * I> even{};
+        constexpr std::integral_constant<int, 2 * I + 1> odd{};
+        put(at);
+        wave_sync();
+        load_x(ahead(std::integral_constant<int, 2 * (I + XP)>()), std::integral_constant<int, I + XP>());
+        multiply(even);
+        multiply(odd);
         wave_sync();
     };
     constexpr std::integral_constant<int, 0> i0{};
     constexpr std::integral_constant<int, 1> i1{};
     constexpr std::integral_constant<int, 2> i2{};
-    constexpr std::integral_constant<int, 3> i3{};
     if (g0 < g1) {
         step = (g0 + blockIdx.x % (g1 - g0)) * 4;
         load_x(step, i0);
         load_a(step, i0);
-        if constexpr (XS == 4) {
-            load_x(step + 1, i1);
-            load_x(step + 2, i2);
+        if constexpr (XP == 2)
+            load_x(step + 2, i1);
+        if constexpr (AS == 4) {
+            load_a(step + 1, i1);
+            load_a(step + 2, i2);
         }
     }
     for (int g = g0; g < g1; ++g) {
-        // (past the last group the loads repeat the first: no load is under a condition)
-        const int next = step + 4 < g1 * 4 ? step + 4 : g0 * 4;
-        if constexpr (XS == 4)
-            load_x(step + 3, i3);
-        else
-            load_x(step + 1, i1);
-        load_a(step + 1, i1);
-        multiply(step, i0, i0);
-        load_x(XS == 4 ? next : step + 2, i0);
-        load_a(step + 2, i0);
-        multiply(step + 1, i1, i1);
-        load_x(XS == 4 ? next + 1 : step + 3, i1);
-        load_a(step + 3, i1);
-        multiply(step + 2, i2, i0);
-        load_x(XS == 4 ? next + 2 : next, i2);
-        load_a(next, i0);
-        multiply(step + 3, i3, i1);
+        next = step + 4 < g1 * 4 ? step + 4 : g0 * 4;
+        pair(i0);
+        pair(i1);
         step = next;
     }
     __syncthreads();
@@ -309,15 +327,17 @@ __global__ __launch_bounds__(64 * W) void adapter_down_kernel(AdapterArgs a)
     }
 }
 
-// out = y + h B^T: 16 CB columns a wave, four waves side by side in a slice, the tile's tokens 16 at a time,
+// out = y + h B^T: 64 columns a wave, four waves side by side in a slice, the tile's tokens 16 at a time,
 // with the tile's y under way before the rest.  Tokens are the matrix instructions' rows and columns their
-// columns, dealt out so that a lane ends up with CB neighbouring ones and 16 lanes with a run of a row:
+// columns, dealt out so that a lane ends up with four neighbouring ones and 16 lanes with a run of a row:
 // y is read and out written in whole runs.  B stays in registers over the tile.  The tile's h
 // lies in LDS, turned as x in the first product.
-constexpr int kUpRows = 64;
+// Four columns a lane: eight, in half as many work-groups, take 180 registers and 46 instead of 43 us for 2 x
+// 4388 rows of 5760 at rank 32, 49 instead of 45 for prompts of 4096 at rank 64.
+constexpr int kUpRows = 64, CB = 4, kUpCols = 4 * 16 * CB;
 
 // CB values of a row as they lie in memory, until they are needed as numbers.
-template <class Y, int CB> struct RawRow {
+template <class Y> struct RawRow {
     static constexpr int kBytes = CB * (int)sizeof(Y), kPiece = kBytes < 16 ? kBytes : 16;
     typedef uint32_t Words __attribute__((ext_vector_type(kPiece / 4)));
     struct alignas(kPiece) Piece { Y v[kPiece / sizeof(Y)]; } p[kBytes / kPiece];
@@ -337,10 +357,12 @@ template <class Y, int CB> struct RawRow {
     }
 };
 
-template <class T, class Y, int KS, int CB>
+template <class T, class Y, int KS>
 __global__ __launch_bounds__(256) void adapter_up_kernel(AdapterArgs a)
 {
-    constexpr int kAhead = sizeof(Y) == 4 ? 2 : 4;  // blocks of 16 tokens under way together
+    // blocks of 16 tokens under way together: rank 32 in 41.7 us with two and 42.9 with four, rank 64 in 46.7 and
+    // 44.6 (the sizes above)
+    constexpr int kAhead = sizeof(Y) == 4 || KS == 1 ? 2 : 4;
     constexpr int RU = KS == 1 ? 4 : (KS == 2 ? 8 : 16);  // pieces of 16 bytes of a row in LDS
     __shared__ uint4 hs[2][kUpRows * RU];
     __shared__ alignas(16) float back[kUpRows];
@@ -363,7 +385,7 @@ __global__ __launch_bounds__(256) void adapter_up_kernel(AdapterArgs a)
     // Where some row or column is missing, its loads repeat another: a load under a condition of its own
     // waits for the one before.  Whole blocks, almost all of them, store without conditions.
     const Y *y = (const Y *)a.y + row0 * a.ys + (left > 0 ? col0 : 0) + (mine ? m * CB : 0);
-    RawRow<Y, CB> v[kAhead][4];
+    RawRow<Y> v[kAhead][4];
     auto load = [&](int t0) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
@@ -492,10 +514,10 @@ template <class T, class Y> hipError_t up_as(const AdapterArgs &a, hipStream_t s
 {
     const dim3 grid((unsigned)(adapter_tiles(a, kUpRows) * a.col_tiles));
     switch ((a.rank + 31) / 32) {
-    case 1: adapter_up_kernel<T, Y, 1, 8><<<grid, 256, 0, st>>>(a); break;
-    case 2: adapter_up_kernel<T, Y, 2, 8><<<grid, 256, 0, st>>>(a); break;
-    case 3: adapter_up_kernel<T, Y, 3, 4><<<grid, 256, 0, st>>>(a); break;
-    default: adapter_up_kernel<T, Y, 4, 4><<<grid, 256, 0, st>>>(a); break;
+    case 1: adapter_up_kernel<T, Y, 1><<<grid, 256, 0, st>>>(a); break;
+    case 2: adapter_up_kernel<T, Y, 2><<<grid, 256, 0, st>>>(a); break;
+    case 3: adapter_up_kernel<T, Y, 3><<<grid, 256, 0, st>>>(a); break;
+    default: adapter_up_kernel<T, Y, 4><<<grid, 256, 0, st>>>(a); break;
     }
     return hipGetLastError();
 }
@@ -525,16 +547,12 @@ int64_t adapter_groups(const AdapterArgs &a)
 // tiles and half of the card's 256 units get one, and the sums of up to 96 adapter rows fit the registers
 // (2 x 4388 rows of 1920 at 96 adapter rows: 15.6 us, with 32 tokens 18.1; ragged prompts of 4096 columns at 64:
 // 32.8 and 37.7); else 32, up to 128 adapter rows; else 16.  Four waves a tile of 32, eight of the others.
-//
-// The second product's work-groups take 512 columns of a slice, or 256 where the rank is over 64 (what B
-// takes of the registers).
 void adapter_plan(AdapterArgs &a)
 {
-    const int cols = a.rank <= 64 ? 512 : 256;
     a.col_tiles = 0;
     for (int i = 0; i < a.slices; ++i) {
         a.first_tile[i] = a.col_tiles;
-        a.col_tiles += (a.first_col[i + 1] - a.first_col[i] + cols - 1) / cols;
+        a.col_tiles += (a.first_col[i + 1] - a.first_col[i] + kUpCols - 1) / kUpCols;
     }
     const int64_t t = a.rows.tokens, most = t / (a.rows.batch > 0 ? a.rows.batch : 1);
     if (a.down <= 96 && most >= 64 && adapter_tiles(a, 64) >= 128)

@@ -181,8 +181,8 @@ cfz_status cfz_adapters_put(const cfz_adapters *adapters, int32_t first, int32_t
  * stride; other overlaps are not allowed.  Rows of no sequence, and rows past a sequence's first
  * max_rows, are neither read nor written.  The products accumulate in fp32; x a^T enters the second one as the sum of
  * two numbers of `dtype` (off by 2^-16 of itself for BF16, 2^-21 of its row's largest value for F16).
- * Results do not depend on the run.  2^23 or more work-groups (of 64 tokens x 512 columns of a slice, 256
- * where the rank is over 64) are refused.
+ * Results do not depend on the run.  2^23 or more work-groups (of 64 tokens x 256 columns of a slice) are
+ * refused.
  * workspace: cfz_adapters_workspace_bytes(...) bytes, 256-byte aligned, overwritten; calls that may
  * run at the same time need one each.
  * Errors: CFZ_ERR_NULL, CFZ_ERR_SHAPE, CFZ_ERR_UNSUPPORTED, CFZ_ERR_ALIGN, CFZ_ERR_WORKSPACE,

@@ -19,7 +19,7 @@ import torch
 
 from . import cfz, kv8
 from .cfz import CFZ_ERR_NULL, CFZ_OK, CfzError
-from .kv8 import CFZ_KV8_F32, _REALS, _empty_on, _fit, _ints, _queue, cfz_kv8_rotation
+from .kv8 import _REALS, _empty_on, _fit, _ints, _queue, cfz_kv8_rotation
 
 NORMS = {"none": 0, "rms": 1, "layer": 2}
 SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3}
@@ -112,6 +112,8 @@ def _matrix(t, shape, dtypes, device, what):
 
 def _vector(t, size, dtype, device, what):
     """Address and type of a weight."""
+    if t.dtype == dtype and t.device == device and t.shape == (size,) and t.is_contiguous():
+        return t.data_ptr(), _REALS[dtype]
     if t.dtype != dtype and t.dtype != torch.float32:
         raise TypeError(f"{what}: {t.dtype}, expected {dtype} or fp32")
     if t.device != device or t.shape != (size,) or not t.is_contiguous():
@@ -207,7 +209,8 @@ def _residual(x, y, before, after, gate, gate_scale, scale, shift, offsets, batc
         batch = offsets.numel() - 1
     elif batch is None:
         batch = max([1] + [t.shape[0] for t in (gate, scale, shift) if t is not None and t.dim() == 2])
-    _fit(32, cols=cols, batch=batch)
+    if not (cols < 1 << 31 and -(1 << 31) <= batch < 1 << 31):
+        _fit(32, cols=cols, batch=batch)
     a = cfz_residual()
     a.tokens, a.cols, a.batch = tokens, cols, batch
     if offsets is not None:
@@ -329,11 +332,13 @@ def rotate(tensors, rotation, offsets=None, starts=None, weights=None, eps=1e-6,
                 raise ValueError(f"outs[{i}]: {out.dtype} {tuple(out.shape)}, expected {dtype} "
                                  f"{tuple(t.shape)}")
             out_stride = kv8._rows(out, heads, dim, device, f"outs[{i}]")
-        weight, kind = (None, CFZ_KV8_F32) if w is None else \
-            _vector(w, dim, dtype, device, f"weights[{i}]")
-        _fit(32, heads=heads)
-        args[i] = cfz_rotate_rows(t.data_ptr(), stride, out.data_ptr(), out_stride, heads, weight,
-                                  kind)
+        if heads >= 1 << 31:
+            _fit(32, heads=heads)
+        row = args[i]
+        row.x, row.x_stride, row.out, row.out_stride = t.data_ptr(), stride, out.data_ptr(), out_stride
+        row.heads = heads
+        if w is not None:
+            row.weight, row.weight_dtype = _vector(w, dim, dtype, device, f"weights[{i}]")
         results.append(out)
     _queue(_lib.cfz_rotate, device, stream, len(tensors), args, _REALS[dtype], dim, tokens, batch,
            None if offsets is None else _ints(offsets, (batch + 1,), device, "offsets"),
@@ -417,8 +422,9 @@ class Adapters:
         tokens, batch = x.shape[0], ids.numel()
         xs = _matrix(x, (tokens, self.cols_in), (self.dtype,), self.device, "x")
         ys = _matrix(y, (tokens, self.cols_out), (self.dtype, torch.float32), self.device, "y")
-        _fit(32, batch=batch)
-        _fit(64, max_rows=max_rows)
+        if not (batch < 1 << 31 and -(1 << 63) <= max_rows < 1 << 63):
+            _fit(32, batch=batch)
+            _fit(64, max_rows=max_rows)
         need = _lib.cfz_adapters_workspace_bytes(self._ref, tokens, batch)
         if out is None:
             out, os = _empty_on(self.device, stream, y.shape, y.dtype), self.cols_out
@@ -426,11 +432,12 @@ class Adapters:
             os = _matrix(out, y.shape, (y.dtype,), self.device, "out")
         if workspace is None:
             workspace = _empty_on(self.device, stream, need, torch.uint8)
-        elif workspace.device != self.device or not workspace.is_contiguous():
+        elif workspace.device == self.device and workspace.is_contiguous():
+            need = workspace.numel() * workspace.element_size()
+        else:
             raise ValueError("workspace: must be contiguous and on the adapters' device")
         _queue(_lib.cfz_adapters_add, self.device, stream, self._ref, tokens, batch,
                _ints(offsets, (batch + 1,), self.device, "offsets"),
                _ints(ids, (batch,), self.device, "ids"), max_rows, x.data_ptr(), xs, y.data_ptr(), ys,
-               out.data_ptr(), os, _REALS[y.dtype], workspace.data_ptr(),
-               workspace.numel() * workspace.element_size())
+               out.data_ptr(), os, _REALS[y.dtype], workspace.data_ptr(), need)
         return out

@@ -2,8 +2,11 @@
 //
 //   out = y + scale (x A^T) B^T   for each sequence's own A, B and scale
 //
-// Two launches: h = x A^T into the workspace, then out = y + scale h B^T.  Both are bound by the rows
-// that they read and write (x once, y and out once); the products are small beside them.  Row
+// Two launches: h = scale x A^T into the workspace, then out = y + h B^T.  Both are bound by the rows
+// that they read and write (x once, y and out once); the products are small beside them.  2 x 4388 rows of
+// 1920 to 3 x 1920 columns at rank 32, bf16: 15.1 + 42.8 us, 237 MB at 4.1 TB/s; 12,393 ragged rows of 4096 to
+// 4096 at rank 64, fp16: 29.3 + 44.2 us, 298 MB at 4.1 TB/s; 32 single tokens of 1024 to 3 x 1024 at rank 16:
+// 5.7 + 4.7 us, dependent reads.  Row
 // tiles never straddle sequences: sequence b's tiles are numbered from offsets[b] / R + b on, which
 // leaves room for a short tile at its end, so that a tile finds its sequence by a search and the
 // host needs no list.
@@ -117,7 +120,7 @@ __global__ __launch_bounds__(256) void adapter_put_kernel(AdapterArgs a, const u
 // steps of 32 at a time, and their sums are added in LDS, half of the waves at a time.  The matrix
 // instructions' rows are A's and their columns the tokens.  An operand's lanes are 16 different rows: read
 // so from rows in memory, each lane's 16 bytes are an access of their own, and the first-level cache gives
-// 16 bytes a clock.  So A is laid out once as the instructions take it, and of x eight neighbouring
+// 16 bytes a clock (31 us for the video shares).  So A is laid out once as the instructions take it, and of x eight neighbouring
 // lanes read 128 bytes of a row, which the wave turns round in LDS, a row's eight pieces shifted by its
 // number so that no bank is met twice.  Two or four steps are under way.  Tiles start their runs at
 // different places, so that rows a power of two apart are not all read from the same channels.
@@ -545,8 +548,8 @@ int64_t adapter_groups(const AdapterArgs &a)
 
 // The more tokens a tile of the first product has, the less often A is read: 64, where sequences fill such
 // tiles and half of the card's 256 units get one, and the sums of up to 96 adapter rows fit the registers
-// (2 x 4388 rows of 1920 at 96 adapter rows: 15.6 us, with 32 tokens 18.1; ragged prompts of 4096 columns at 64:
-// 32.8 and 37.7); else 32, up to 128 adapter rows; else 16.  Four waves a tile of 32, eight of the others.
+// (2 x 4388 rows of 1920 at 96 adapter rows: 15.1 us, with 32 tokens 16.8; ragged prompts of 4096 columns at 64:
+// 29.2 and 33.9); else 32, up to 128 adapter rows; else 16.  Four waves a tile of 32, eight of the others.
 void adapter_plan(AdapterArgs &a)
 {
     a.col_tiles = 0;

@@ -6,8 +6,9 @@
 // that they read and write (x once, y and out once); the products are small beside them.  2 x 4388 rows of
 // 1920 to 3 x 1920 columns at rank 32, bf16: 15.1 + 42.8 us, 237 MB at 4.1 TB/s; 12,393 ragged rows of 4096 to
 // 4096 at rank 64, fp16: 29.3 + 44.2 us, 298 MB at 4.1 TB/s; 32 single tokens of 1024 to 3 x 1024 at rank 16:
-// 5.7 + 4.7 us, dependent reads.  Row
-// tiles never straddle sequences: sequence b's tiles are numbered from offsets[b] / R + b on, which
+// 5.7 + 4.7 us, dependent reads.
+//
+// Row tiles never straddle sequences: sequence b's tiles are numbered from offsets[b] / R + b on, which
 // leaves room for a short tile at its end, so that a tile finds its sequence by a search and the
 // host needs no list.
 #include "block_internal.h"
@@ -120,10 +121,11 @@ __global__ __launch_bounds__(256) void adapter_put_kernel(AdapterArgs a, const u
 // steps of 32 at a time, and their sums are added in LDS, half of the waves at a time.  The matrix
 // instructions' rows are A's and their columns the tokens.  An operand's lanes are 16 different rows: read
 // so from rows in memory, each lane's 16 bytes are an access of their own, and the first-level cache gives
-// 16 bytes a clock (31 us for the video shares).  So A is laid out once as the instructions take it, and of x eight neighbouring
-// lanes read 128 bytes of a row, which the wave turns round in LDS, a row's eight pieces shifted by its
-// number so that no bank is met twice.  Two or four steps are under way.  Tiles start their runs at
-// different places, so that rows a power of two apart are not all read from the same channels.
+// 16 bytes a clock (31 us for the video shares).  So A is laid out once as the instructions take it, and of
+// x eight neighbouring lanes read 128 bytes of a row, which the wave turns round in LDS, a row's eight
+// pieces shifted by its number so that no bank is met twice (four lanes and 64 bytes: 34 instead of 29 us for
+// the prompts).  Two or four steps are under way.  Tiles start their runs at different places, so that rows a
+// power of two apart are not all read from the same channels at once.
 //
 // h leaves as the sum of two 16-bit numbers, the operands of the second product: that leaves 2^-16 of it
 // (bf16) or 2^-21 of its row's largest in a slice (fp16, after a power of two that brings the row into
@@ -165,7 +167,7 @@ __global__ __launch_bounds__(64 * W) void adapter_down_kernel(AdapterArgs a)
             acc[t][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     // groups of four steps g0 .. g1 - 1, from one in their midst on and round
     const int g0 = steps / 4 * wave / W, g1 = steps / 4 * (wave + 1) / W;
-    int step = 0;  // the one under way farthest ahead
+    int step = 0;  // the first one of the group
     // pairs of steps of x and steps of A in registers, as many as they hold beside the sums
     constexpr int XP = TM == 4 && NB > 4 ? 1 : 2, AS = NB > 4 ? 2 : 4;
     uint4 xv[XP][TM][2], wv[AS][NB];

@@ -26,6 +26,9 @@ __device__ inline void fresh_store(int32_t *p, int32_t x)
     __hip_atomic_store(p, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
+// A thread's stores and atomics are done.  (A work-group's barrier by itself does not wait for them.)
+__device__ inline void memory_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
 // A thread a place.  The exchange makes a row that is listed twice let go of its pages once.
 __global__ __launch_bounds__(kThreads) void kv8_free_kernel(Kv8Pages p, const int32_t *rows,
                                                             const int32_t *keep, int chunks)
@@ -134,6 +137,7 @@ __global__ __launch_bounds__(kWide) void kv8_reserve_kernel(Kv8Pages p, Kv8Reser
             fresh_store(r.writers + page, 0);
         }
     }
+    memory_done();
     if (__syncthreads_or(any)) {
         for (int64_t q = tid; q < r.places; q += kWide) {
             int refs;
@@ -144,6 +148,7 @@ __global__ __launch_bounds__(kWide) void kv8_reserve_kernel(Kv8Pages p, Kv8Reser
             }
         }
     }
+    memory_done();
     __syncthreads();
 
     // ranks among the places that need a page
@@ -233,6 +238,7 @@ __global__ __launch_bounds__(kWide) void kv8_reserve_kernel(Kv8Pages p, Kv8Reser
             }
         }
         have += all;
+        memory_done();
         __syncthreads();
     }
     if (tid == 0)

@@ -141,9 +141,13 @@ __global__ __launch_bounds__(64 * W) void adapter_down_kernel(AdapterArgs a)
         float sum[TM * 16][kRow];
     } s;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // adapter rows first .. first + down - 1 (whole slices, from a block of 16 on)
+    const int part = blockIdx.x % a.parts, tile = blockIdx.x / a.parts;
+    const int first = part * a.part_rows;
+    const int down = a.down - first < a.part_rows ? a.down - first : a.part_rows;
     int n, id;
     int64_t row0;
-    if (!find_tile<16 * TM>(a, blockIdx.x, row0, n, id) || id < 0)
+    if (!find_tile<16 * TM>(a, tile, row0, n, id) || id < 0)
         return;
     const int m = lane & 15, q = lane >> 4;
     const int r = lane >> 3, piece = lane & 7;  // of half a block: row and 16 bytes, as they are read
@@ -156,8 +160,9 @@ __global__ __launch_bounds__(64 * W) void adapter_down_kernel(AdapterArgs a)
             const int row = t * 16 + i * 8 + r;
             x[t][i] = (const T *)a.x + (row0 + (row < n ? row : n - 1)) * a.xs + piece * 8;
         }
-    const int steps = down_steps(a), blocks = (a.down + 15) / 16;
-    const uint4 *w = (const uint4 *)a.a + (int64_t)id * blocks * steps * 64;
+    const int steps = down_steps(a), blocks = (down + 15) / 16;
+    const uint4 *w =
+        (const uint4 *)a.a + ((int64_t)id * ((a.down + 15) / 16) + first / 16) * steps * 64;
     uint4 *lds = s.turn[wave][0];
     f32x4 acc[TM][NB];
 #pragma unroll
@@ -236,7 +241,7 @@ __global__ __launch_bounds__(64 * W) void adapter_down_kernel(AdapterArgs a)
     constexpr std::integral_constant<int, 1> i1{};
     constexpr std::integral_constant<int, 2> i2{};
     if (g0 < g1) {
-        step = (g0 + blockIdx.x % (g1 - g0)) * 4;
+        step = (g0 + tile % (g1 - g0)) * 4;
         load_x(step, i0);
         load_a(step, i0);
         if constexpr (XP == 2)
@@ -293,7 +298,7 @@ __global__ __launch_bounds__(64 * W) void adapter_down_kernel(AdapterArgs a)
             *(f32x4 *)&s.sum[b / NB * 16 + m][b % NB * 16 + q * 4] = sum[i];
     }
     __syncthreads();
-    const int units = a.down / 8;
+    const int units = down / 8;
     for (int i = threadIdx.x; i < n * units; i += 64 * W) {
         const int row = i / units, r = (i - row * units) * 8;
         const float *v = &s.sum[row][r];
@@ -310,7 +315,7 @@ __global__ __launch_bounds__(64 * W) void adapter_down_kernel(AdapterArgs a)
             e = e > 127 ? 0 : (e > 126 ? 126 : (e < -126 ? -126 : e));
             f = __uint_as_float((uint32_t)(127 - e) << 23);
             if (r == slice * a.rank)
-                a.back[(row0 + row) * a.slices + slice] = __uint_as_float((uint32_t)(127 + e) << 23);
+                a.back[(row0 + row) * a.slices + first / a.rank + slice] = __uint_as_float((uint32_t)(127 + e) << 23);
         }
         uint32_t hi[4], lo[4];
 #pragma unroll
@@ -326,7 +331,7 @@ __global__ __launch_bounds__(64 * W) void adapter_down_kernel(AdapterArgs a)
             hi[k] = (uint32_t)a0[0] | (uint32_t)a0[1] << 16;
             lo[k] = (uint32_t)a1[0] | (uint32_t)a1[1] << 16;
         }
-        const int64_t at = (row0 + row) * a.down + r;
+        const int64_t at = (row0 + row) * a.down + first + r;
         *(uint4 *)(a.hi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *(uint4 *)(a.lo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
@@ -493,8 +498,8 @@ __global__ __launch_bounds__(256) void adapter_up_kernel(AdapterArgs a)
 
 template <class T, int TM, int W> hipError_t down_as(const AdapterArgs &a, hipStream_t st)
 {
-    const dim3 grid((unsigned)adapter_tiles(a, 16 * TM));
-    const int nb = (a.down + 15) / 16;
+    const dim3 grid((unsigned)(adapter_tiles(a, 16 * TM) * a.parts));
+    const int nb = (a.part_rows + 15) / 16;
 #define CFZ_DOWN_CASE(NB)                                                                          \
     if (nb <= NB) {                                                                                \
         adapter_down_kernel<T, NB, TM, W><<<grid, 64 * W, 0, st>>>(a);                              \
@@ -543,7 +548,7 @@ int64_t adapter_tiles(const AdapterArgs &a, int rows) { return a.rows.tokens / r
 
 int64_t adapter_groups(const AdapterArgs &a)
 {
-    const int64_t down = adapter_tiles(a, 16 * a.tall);
+    const int64_t down = adapter_tiles(a, 16 * a.tall) * a.parts;
     const int64_t up = adapter_tiles(a, kUpRows) * a.col_tiles;
     return down > up ? down : up;
 }
@@ -551,7 +556,8 @@ int64_t adapter_groups(const AdapterArgs &a)
 // The more tokens a tile of the first product has, the less often A is read: 64, where sequences fill such
 // tiles and half of the card's 256 units get one, and the sums of up to 96 adapter rows fit the registers
 // (2 x 4388 rows of 1920 at 96 adapter rows: 15.1 us, with 32 tokens 16.8; ragged prompts of 4096 columns at 64:
-// 29.2 and 33.9); else 32, up to 128 adapter rows; else 16.  Four waves a tile of 32, eight of the others.
+// 29.2 and 33.9); else 32, up to 128 adapter rows; else 16.  Four waves a tile of 32, eight of the others.  More than 256 adapter rows are
+// two work-groups' a tile, two slices each.
 void adapter_plan(AdapterArgs &a)
 {
     a.col_tiles = 0;
@@ -559,11 +565,14 @@ void adapter_plan(AdapterArgs &a)
         a.first_tile[i] = a.col_tiles;
         a.col_tiles += (a.first_col[i + 1] - a.first_col[i] + kUpCols - 1) / kUpCols;
     }
+    // (two slices together end with a block of 16 rows, whatever their rank)
+    a.parts = a.down > 256 ? 2 : 1;
+    a.part_rows = a.parts == 2 ? 2 * a.rank : a.down;
     const int64_t t = a.rows.tokens, most = t / (a.rows.batch > 0 ? a.rows.batch : 1);
-    if (a.down <= 96 && most >= 64 && adapter_tiles(a, 64) >= 128)
+    if (a.part_rows <= 96 && most >= 64 && adapter_tiles(a, 64) >= 128)
         a.tall = 4;
     else
-        a.tall = a.down <= 128 && most >= 32 ? 2 : 1;
+        a.tall = a.part_rows <= 128 && most >= 32 ? 2 : 1;
 }
 
 int64_t adapter_pieces(const AdapterArgs &a)

@@ -92,9 +92,8 @@ cfz_status check_adapters(const cfz_adapters *w, int64_t tokens, int32_t batch, 
         return fail(CFZ_ERR_SHAPE, "adapters = %d (1 .. 2^20)", w->adapters);
     if (w->slices < 1 || w->slices > 4)
         return fail(CFZ_ERR_SHAPE, "slices = %d (1 .. 4)", w->slices);
-    if (w->rank < 8 || w->rank > 128 || w->rank % 8 != 0 || w->slices * w->rank > 256)
-        return fail(CFZ_ERR_SHAPE, "rank = %d with %d slices (a multiple of 8, 8 .. 128, 256 in all)",
-                    w->rank, w->slices);
+    if (w->rank < 8 || w->rank > 128 || w->rank % 8 != 0)
+        return fail(CFZ_ERR_SHAPE, "rank = %d (a multiple of 8, 8 .. 128)", w->rank);
     if (w->cols_in < 8 || w->cols_in > 1 << 20 || w->cols_in % 8 != 0)
         return fail(CFZ_ERR_SHAPE, "cols_in = %d (a multiple of 8, 8 .. 2^20)", w->cols_in);
     int cols = 0;

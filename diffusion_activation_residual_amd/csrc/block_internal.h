@@ -95,6 +95,7 @@ struct AdapterArgs {
     int64_t xs, ys, os;
     uint16_t *hi, *lo;  // [tokens][down]: scale x A^T as the sum of two numbers of the type
     float *back;        // [tokens][slices]: what it was multiplied by, turned round (fp16)
+    int parts, part_rows;  // work-groups a tile of the first product, adapter rows of each
     int tall;  // 16 tokens times this a tile of the first product
 };
 void adapter_plan(AdapterArgs &a);

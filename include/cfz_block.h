@@ -152,8 +152,8 @@ cfz_status cfz_rotate(int32_t count, const cfz_rotate_rows *tensors, cfz_kv8_dty
  *   b: [adapters][cols_out][rank] of `dtype`, scale: [adapters] fp32 or NULL (1).
  * The projection's columns are dealt out to 1 .. 4 slices (query, key and value of one fused
  * projection) of slice_cols[i] columns each, multiples of 16, cols_out in all; slice i's columns
- * are met by adapter rows i * rank .. (i + 1) * rank - 1 of a.  rank: a multiple of 8, 8 .. 128,
- * slices * rank at most 256 (lower ranks: zeros).  cols_in: a multiple of 8, 8 .. 2^20;
+ * are met by adapter rows i * rank .. (i + 1) * rank - 1 of a.  rank: a multiple of 8, 8 .. 128
+ * (lower ranks: zeros).  cols_in: a multiple of 8, 8 .. 2^20;
  * cols_out at most 2^20; 1 <= adapters <= 2^20. */
 typedef struct {
     int32_t adapters;

@@ -44,7 +44,8 @@ def check(w, x, y, out, ids, offsets, real, before=None, max_rows=1 << 30):
 @pytest.mark.parametrize("rank,slices,cols_in", [
     (8, [16], 8), (8, [48, 16, 16], 72), (16, [64], 64), (24, [80, 208], 520), (32, [256], 1024),
     (40, [1024, 128, 128], 512), (64, [512], 4096), (64, [64, 64, 64, 64], 136), (128, [320], 1928),
-    (128, [96, 160], 256), (104, [16, 1040], 640)])
+    (128, [96, 160], 256), (104, [16, 1040], 640), (88, [64, 32, 80], 264), (128, [32, 64, 16, 48], 192),
+    (72, [80, 16, 16, 16], 96), (120, [16, 48, 32], 136)])
 @pytest.mark.parametrize("tall", [False, True])
 def test_ranks_and_slices(real, rank, slices, cols_in, tall):
     """Every number of adapter rows, column groups that end inside a wave's, odd numbers of tokens: single

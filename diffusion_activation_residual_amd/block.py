@@ -282,9 +282,14 @@ def rotation_table(rot_dim, rows=None, positions=None, axis_dims=None, base=1000
         raise ValueError(f"rows = {rows}, rot_dim = {rot_dim}")
     angles = cfz_rotation_angles(rot_dim, len(axis_dims), (C.c_int32 * 4)(*axis_dims),
                                  SCALINGS[scaling], base, factor, trained, slow, fast, amplitude)
+    where = None if positions is None else positions.data_ptr()
+    # (the tables are the last thing that the library asks for: nothing is allocated for what it refuses)
+    status = _lib.cfz_rotation_table(C.byref(angles), rows, where, None, None, None)
+    if status != (CFZ_OK if rows == 0 else CFZ_ERR_NULL):
+        raise CfzError(status, "cfz_rotation_table")
     cos, sin = (_empty_on(device, stream, (rows, rot_dim // 2), torch.float32) for _ in range(2))
-    _queue(_lib.cfz_rotation_table, device, stream, C.byref(angles), rows,
-           None if positions is None else positions.data_ptr(), cos.data_ptr(), sin.data_ptr())
+    _queue(_lib.cfz_rotation_table, device, stream, C.byref(angles), rows, where, cos.data_ptr(),
+           sin.data_ptr())
     return kv8.Rotation(cos, sin, interleaved=interleaved)
 
 
@@ -292,7 +297,7 @@ def rotate(tensors, rotation, offsets=None, starts=None, weights=None, eps=1e-6,
            outs=None, stream=None):
     """Norm and rotation of each head of up to four tensors [tokens, heads, head_dim] (bf16, fp16 or
     fp32; views of one projection, say its queries and keys), in one launch: a list of results,
-    dense or written to ``outs`` (which may be the tensors themselves).
+    dense or written to ``outs`` (which may be the tensors themselves; None: allocated).
 
     A head becomes x / sqrt(mean(x ** 2) + eps) * weight where ``weights`` gives one weight
     [head_dim] (or None) for each tensor (``normed=True``: without weights), and is then turned by
@@ -324,10 +329,10 @@ def rotate(tensors, rotation, offsets=None, starts=None, weights=None, eps=1e-6,
                              f"heads, {dim}]")
         heads = t.shape[1]
         stride = kv8._rows(t, heads, dim, device, f"tensors[{i}]")
-        if outs is None:
+        out = None if outs is None else outs[i]
+        if out is None:
             out, out_stride = _empty_on(device, stream, (tokens, heads, dim), dtype), heads * dim
         else:
-            out = outs[i]
             if out.dtype != dtype or out.shape != t.shape:
                 raise ValueError(f"outs[{i}]: {out.dtype} {tuple(out.shape)}, expected {dtype} "
                                  f"{tuple(t.shape)}")

@@ -222,12 +222,6 @@ cfz_status cfz_rotation_table(const cfz_rotation_angles *g, int64_t rows, const 
         return fail(CFZ_ERR_NULL, "more than one axis needs positions");
     if (!aligned(positions, 4))
         return fail(CFZ_ERR_ALIGN, "positions must be 4-byte aligned");
-    if (rows == 0)
-        return CFZ_OK;
-    if (!cos || !sin)
-        return fail(CFZ_ERR_NULL, "cos and sin are required");
-    if (!aligned(cos, 16) || !aligned(sin, 16))
-        return fail(CFZ_ERR_ALIGN, "cos and sin must be 16-byte aligned");
     cfz::TableArgs a;
     memset(&a, 0, sizeof a);
     int at = 0;
@@ -250,6 +244,12 @@ cfz_status cfz_rotation_table(const cfz_rotation_angles *g, int64_t rows, const 
             a.axis[at] = (uint8_t)j;
         }
     }
+    if (rows == 0)
+        return CFZ_OK;
+    if (!cos || !sin)
+        return fail(CFZ_ERR_NULL, "cos and sin are required");
+    if (!aligned(cos, 16) || !aligned(sin, 16))
+        return fail(CFZ_ERR_ALIGN, "cos and sin must be 16-byte aligned");
     a.pairs = pairs;
     a.axes = g->axes;
     a.rows = rows;

@@ -24,7 +24,8 @@ extern "C" {
  *   RMS:   v / sqrt(mean(v^2) + eps) * weight
  *   LAYER: (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) * weight + bias
  * weight and bias: [cols] of `dtype`, or NULL (1 and 0; a bias goes with LAYER only).  eps is
- * finite and >= 0. */
+ * finite and >= 0.  Squares are summed in fp32: values past 2^63 / sqrt(cols) may overflow it, and a
+ * row that is 0 (or all of one value, LAYER) with eps = 0 is 0 / 0. */
 typedef enum { CFZ_NORM_NONE = 0, CFZ_NORM_RMS = 1, CFZ_NORM_LAYER = 2 } cfz_norm_kind;
 typedef struct {
     int32_t kind;

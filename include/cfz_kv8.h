@@ -197,7 +197,9 @@ size_t cfz_kv8_select_workspace_bytes(const cfz_kv8_cache *cache, const cfz_kv8_
  * them: each call's page moves are then done in every layer's cache (cfz_kv8_copy).  A place that
  * names no page of 0 .. pages - 1 counts as -1; lengths count as clamped to
  * [0, table_width * page_tokens].  Limits as in cfz_kv8_cache and cfz_kv8_batch, batch >= 1.
- * The results of every call are the same whatever the order in which its parts run. */
+ * The results of every call are the same whatever the order in which its parts run; calls that
+ * change the same table run one after the other (on one stream, or ordered by the caller), and
+ * so do a change and the attention that reads the table. */
 typedef struct {
     int64_t pages;
     int32_t batch;

@@ -266,6 +266,9 @@ def test_rotate_head_counts_and_in_place(heads):
     q2, k2 = q.clone(), k.clone()
     block.rotate([q2, k2], turn, outs=[q2, k2])
     assert torch.equal(q2, a) and torch.equal(k2, b)
+    q3, k3 = q.clone(), k.clone()
+    got = block.rotate([q3, k3], turn, outs=[q3, None])
+    assert got[0] is q3 and torch.equal(q3, a) and torch.equal(got[1], b) and torch.equal(k3, k)
 
 
 def test_rotate_norm_alone_and_no_rows():
@@ -347,3 +350,42 @@ def test_rows_past_four_gigabytes():
     (want,) = block.rotate([near.view(18, 4, 64)], turn)
     (got,) = block.rotate([x.unflatten(1, (4, 64))], turn, outs=[h.unflatten(1, (4, 64))])
     assert torch.equal(got, want)
+
+
+def test_refusals_of_the_binding():
+    g = Gen(40)
+    x, y = g(6, 64, dtype=torch.bfloat16), g(6, 64, dtype=torch.bfloat16)
+    norm = block.Norm("rms", 1e-6)
+    bad_norm = [dict(y=y.half()), dict(y=y[:, :32]), dict(y=y[:5]), dict(y=y.t().contiguous().t()),
+                dict(y=y.cpu()), dict(out=x.float()), dict(out=x[:5]), dict(normed=y.float()),
+                dict(offsets=ints([0, 6]).long()), dict(offsets=ints([0, 6]).cpu()),
+                dict(gate=y[:4]), dict(gate=y[0].half()), dict(gate=y[0, :32]),
+                dict(scale=y[:2].t().contiguous().t()), dict(before=block.Norm("batch")),
+                dict(before=block.Norm("rms", 1e-6, y[0].half())),
+                dict(before=block.Norm("rms", 1e-6, y[0, :32])),
+                dict(before=block.Norm("layer", 1e-6, y[0], y[0].float())),
+                dict(before=block.Norm("rms", 1e-6, None, y[0])), dict(gate_scale=float("nan")),
+                dict(dtype=torch.float64)]
+    for kw in bad_norm:
+        with pytest.raises((ValueError, TypeError, cfz.CfzError)):
+            block.residual_norm(x, **{"y": y, "before": norm, **kw})
+    for args in ((x.double(),), (x[0],), (x.cpu(),), (x,)):
+        with pytest.raises((ValueError, TypeError, cfz.CfzError)):
+            block.residual_norm(*args)
+    for kw in (dict(rows=None), dict(rows=-1), dict(positions=ints([1, 2]).long()),
+               dict(positions=ints([[1, 2]])), dict(rows=3, positions=ints([1, 2])),
+               dict(axis_dims=[4, 4]), dict(axis_dims=[8] * 5), dict(scaling="no"),
+               dict(device="cpu"), dict(scaling="parts"), dict(rows=1 << 40)):
+        with pytest.raises((ValueError, TypeError, cfz.CfzError)):
+            block.rotation_table(64, **{"rows": 4, "device": DEV, **kw})
+    q, turn = g(6, 2, 64), block.rotation_table(64, rows=8, device=DEV)
+    for args, kw in ((([],), {}), (([q] * 5,), {}), (([q, q.half()],), {}), (([q, q[:5]],), {}),
+                     (([q[0]],), {}), (([q.cpu()],), {}), (([q.transpose(1, 2)],), {}),
+                     (([q],), dict(offsets=ints([0, 6]).long())), (([q],), dict(starts=ints([0, 1]))),
+                     (([q],), dict(weights=[None, None])), (([q],), dict(weights=[q[0, 0].half()])),
+                     (([q],), dict(weights=[q[0, 0, :32]])), (([q],), dict(outs=[q.half()])),
+                     (([q],), dict(outs=[q[:, :1]])), (([q],), dict(outs=[])),
+                     (([q],), dict(normed=False, weights=[q[0, 0]])),
+                     (([q],), dict(rotation=None)), (([q[..., :48].contiguous()],), {})):
+        with pytest.raises((ValueError, TypeError, cfz.CfzError)):
+            block.rotate(*args, **{"rotation": turn, **kw})

@@ -357,3 +357,24 @@ def test_captured_step_replays():
             if s >= 0:
                 assert torch.equal(cache.k[s], cache.k[t]) and torch.equal(cache.k_mean[s],
                                                                           cache.k_mean[t])
+
+
+def test_refusals_of_the_binding():
+    p, _ = empty(8, 2, 4)
+    rows = ints([0])
+    for call in (lambda: p.free(rows.long()), lambda: p.free(rows.cpu()), lambda: p.free(rows[None]),
+                 lambda: p.free(rows, ints([1, 2])), lambda: p.fork(rows, ints([0, 1])),
+                 lambda: p.fork(rows.long(), rows), lambda: p.reserve(ints([1]), 1),
+                 lambda: p.reserve(ints([1, 1]), -1), lambda: p.reserve(ints([1, 1]), 1 << 64),
+                 lambda: p.reserve(ints([1, 1]), 1, workspace=torch.empty(8, device=DEV)),
+                 lambda: p.compact(workspace=torch.empty(4, device=DEV)),
+                 lambda: p.compact(workspace=torch.empty(4096)),
+                 lambda: kv8.Pages(p.table.cpu(), p.lengths, p.refs, 32),
+                 lambda: kv8.Pages(p.table[0], p.lengths, p.refs, 32),
+                 lambda: kv8.Pages(p.table, p.lengths[:1], p.refs, 32),
+                 lambda: kv8.Pages(p.table, p.lengths, p.refs.long(), 32),
+                 lambda: kv8.Pages(p.table.t(), p.lengths, p.refs, 32),
+                 lambda: kv8.Pages(p.table, p.lengths, p.refs, 48).free(rows)):
+        with pytest.raises((ValueError, TypeError, cfz.CfzError)):
+            call()
+    assert (p.table == -1).all() and not p.lengths.any() and not p.refs.any()

@@ -4,14 +4,14 @@
 namespace cfz {
 namespace {
 
-// Threads of a work-group whose rows take G threads each: four rows of a wave, or one row.
-constexpr int group_threads(int g) { return g == 64 ? 256 : g; }
+// Threads of a work-group whose rows take G threads each: 256 / G rows of up to a wave, or one row.
+constexpr int group_threads(int g) { return g <= 64 ? 256 : g; }
 
-// Sum over the threads that hold one row: a wave, two or four.
+// Sum over the threads that hold one row: part of a wave, or up to four.
 template <int G> __device__ inline float row_sum(float x, float *red)
 {
-    x = lanes_sum(x, 64);
-    if (G == 64)
+    x = lanes_sum(x, G < 64 ? G : 64);
+    if (G <= 64)
         return x;
     const int wave = threadIdx.x >> 6;
     __syncthreads();  // (what was read from red before)
@@ -79,17 +79,20 @@ __device__ inline void normalise(float (&v)[V][8], const BlockNormOf &n, int col
 // G threads hold a row, V vectors of 8 values each.  Bound by the bytes: 2 x 4388 rows of 1920, bf16, with
 // gate, scale and shift in 27.1 us (135 MB, 5.0 TB/s); 12,393 rows of 4096 between an fp32 stream and fp16 with a norm on
 // either side in 115 us (609 MB, 5.3 TB/s).  Few values a thread and short work-groups keep more rows under way
-// than a wave a row did (30.9 and 143 us with 4 and 8 vectors a lane).  32 rows of 1024: 3.7 us.
+// than a wave a row did (30.9 and 143 us with 4 and 8 vectors a lane), and narrow rows share a wave (131,072 rows of
+// 256: 41.5 us, 65 with half of the lanes idle).  32 rows of 1024: 3.7 us.
 template <class X, class Y, int V, int G>
 __global__ __launch_bounds__(group_threads(G)) void residual_norm_kernel(ResidualArgs a)
 {
     __shared__ float red[4];
     const int tid = threadIdx.x % G;
     const int64_t row = (int64_t)blockIdx.x * (group_threads(G) / G) + threadIdx.x / G;
-    if (row >= a.rows.tokens)
+    if (G >= 64 && row >= a.rows.tokens)
         return;
-    const X *x = (const X *)a.x + row * a.xs;
-    const Y *y = (const Y *)a.y + row * a.ys;
+    // (a wave of several rows goes on together until their items are known: past the end, the last row)
+    const int64_t near = row < a.rows.tokens ? row : a.rows.tokens - 1;
+    const X *x = (const X *)a.x + near * a.xs;
+    const Y *y = (const Y *)a.y + near * a.ys;
     // the rows are under way while their item is looked up
     float v[V][8], u[V][8];
 #pragma unroll
@@ -105,8 +108,18 @@ __global__ __launch_bounds__(group_threads(G)) void residual_norm_kernel(Residua
         }
     }
     int64_t first;
-    const int item = block_item(a.rows, row, &first);
-    if (item < 0)
+    int item = -1;
+    if (G >= 64 || !a.rows.off) {
+        item = block_item(a.rows, near, &first);
+    } else {
+        const int64_t front = (int64_t)blockIdx.x * (256 / G) + (threadIdx.x >> 6) * (64 / G);
+        for (int i = 0; i < 64 / G; ++i) {
+            const int64_t r = front + i < a.rows.tokens ? front + i : a.rows.tokens - 1;
+            const int found = block_item(a.rows, r, &first);
+            item = (int)(threadIdx.x & 63) / G == i ? found : item;
+        }
+    }
+    if (row >= a.rows.tokens || item < 0)
         return;
     if (a.y) {
         normalise<Y, V, G>(v, a.after, a.cols, tid, red);
@@ -170,6 +183,9 @@ template <class X, class Y> hipError_t launch_as(const ResidualArgs &a, hipStrea
         residual_norm_kernel<X, Y, V, G><<<grid, group_threads(G), 0, st>>>(a);                     \
         return hipGetLastError();                                                                  \
     }
+    CFZ_NORM_CASE(1, 8)
+    CFZ_NORM_CASE(1, 16)
+    CFZ_NORM_CASE(1, 32)
     CFZ_NORM_CASE(1, 64)
     CFZ_NORM_CASE(1, 128)
     CFZ_NORM_CASE(1, 256)
@@ -182,10 +198,11 @@ template <class X, class Y> hipError_t launch_as(const ResidualArgs &a, hipStrea
 
 }  // namespace
 
-// Four rows a work-group where a wave holds one (up to 512 columns), else one.
+// Eight lanes a row and up: 32 rows a work-group of up to 64 columns, 16 to 4 of up to 128 to 512, else one.
 int64_t residual_groups(const ResidualArgs &a)
 {
-    return a.cols <= 512 ? (a.rows.tokens + 3) / 4 : a.rows.tokens;
+    const int rows = a.cols <= 64 ? 32 : (a.cols <= 128 ? 16 : (a.cols <= 256 ? 8 : (a.cols <= 512 ? 4 : 1)));
+    return (a.rows.tokens + rows - 1) / rows;
 }
 
 hipError_t launch_residual_norm(const ResidualArgs &a, int x_dtype, int y_dtype, hipStream_t st)

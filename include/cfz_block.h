@@ -51,8 +51,8 @@ typedef struct {
  * sum is not stored; h NULL: no second norm (before is then not looked at).  x_dtype is
  * y_dtype or F32.  after and before may be of kind NONE.
  * cols: a multiple of 8, 8 .. 16384; row strides in elements, >= cols, multiples of 16
- * bytes.  0 <= tokens < 2^31, 1 <= batch <= 65535; 2^23 or more work-groups (of a row, or of four up
- * to 512 columns) are refused.
+ * bytes.  0 <= tokens < 2^31, 1 <= batch <= 65535; 2^23 or more work-groups (of a row, or of 4 to 32
+ * rows of up to 512 to 64 columns) are refused.
  * offsets: [batch + 1] int32, ascending: rows offsets[b] .. offsets[b + 1] - 1 belong to item b;
  * rows outside every item are left as they are in r and h.  NULL: batch equal runs (tokens a
  * multiple of batch).

@@ -70,6 +70,10 @@ def residual(**kw):
     return lib.cfz_residual_norm(C.byref(a), None)
 
 
+WIDE = dict(cols=512, x_stride=512, y_stride=512, r_stride=512, h_stride=512, gate=items(stride=0),
+            scale=items(stride=0), shift=items(stride=0))
+
+
 @pytest.mark.parametrize("kw,status", [
     (dict(x_dtype=3), UNSUP), (dict(y_dtype=-1), UNSUP), (dict(x_dtype=1), UNSUP),
     (dict(x_dtype=0, y_dtype=2), UNSUP), (dict(cols=0), SHAPE), (dict(cols=12), SHAPE),
@@ -90,7 +94,8 @@ def residual(**kw):
     (dict(r_stride=72), SHAPE), (dict(h_stride=72), SHAPE),
     (dict(cols=8192, tokens=1 << 23, x_stride=8192, y_stride=8192, r_stride=8192, h_stride=8192,
           gate=items(stride=0), scale=items(stride=0), shift=items(stride=0)), SHAPE),
-    (dict(tokens=1 << 25), SHAPE), (dict(tokens=(1 << 25) - 4, x=None), NULL),
+    (dict(tokens=1 << 28), SHAPE), (dict(tokens=(1 << 28) - 32, x=None), NULL),
+    (dict(WIDE, tokens=1 << 25), SHAPE), (dict(WIDE, tokens=(1 << 25) - 4, x=None), NULL),
     (dict(tokens=0, x=None, batch=5), cfz.CFZ_OK),
     (dict(tokens=0, x=None, y=None, r=None, h=None, gate=items()), cfz.CFZ_OK),
 ])

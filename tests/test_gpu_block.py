@@ -77,7 +77,7 @@ def check_norm(offsets, tokens, x, y, r, h, kw, untouched=None):
             assert (to64(t)[~seen] == untouched).all()
 
 
-@pytest.mark.parametrize("cols", [8, 64, 512, 520, 1024, 1920, 4096, 4104, 8200, 16384])
+@pytest.mark.parametrize("cols", [8, 64, 72, 128, 200, 256, 264, 512, 520, 1024, 1920, 4096, 4104, 8200, 16384])
 @pytest.mark.parametrize("xt,yt", [("bf16", "bf16"), ("f32", "f16"), ("f32", "f32")])
 @pytest.mark.parametrize("kind", ["rms", "layer"])
 def test_norm_widths(cols, xt, yt, kind):
@@ -96,12 +96,13 @@ def test_norm_widths(cols, xt, yt, kind):
 
 @pytest.mark.parametrize("xt,yt", [("bf16", "bf16"), ("f16", "f16"), ("f32", "f32"),
                                    ("f32", "bf16"), ("f32", "f16")])
-@pytest.mark.parametrize("f32", [False, True])
-def test_norm_items_gaps_and_strides(xt, yt, f32):
+@pytest.mark.parametrize("cols,f32", [(136, False), (136, True), (40, False), (72, True),
+                                      (264, False), (528, True)])
+def test_norm_items_gaps_and_strides(xt, yt, cols, f32):
     """Ragged items (one empty, one of one row, rows before, between nothing and behind), rows that
     lie apart, chunks of one conditioning projection."""
     g = Gen(3)
-    offsets, tokens, cols, yt = [2, 2, 9, 10, 31], 35, 136, REAL[yt]
+    offsets, tokens, yt = [2, 2, 9, 10, 31], 35, REAL[yt]
     vt = torch.float32 if f32 else yt
     x = g(tokens, 2 * cols, dtype=REAL[xt])[:, cols:]
     y = g(tokens, cols + 24, dtype=yt)[:, :cols]
@@ -173,6 +174,15 @@ def test_norm_extreme_rows():
     x[4, 7], x[5, 3], x[6, 2] = float("nan"), float("inf"), -float("inf")
     x[7] = torch.linspace(1000, 1000.5, cols)
     good = [0, 1, 2, 3, 7]
+    narrow = x[:, ::16].contiguous()
+    narrow[4, 7], narrow[5, 3], narrow[6, 2] = float("nan"), float("inf"), -float("inf")
+    for kind in ("rms", "layer"):
+        # (rows side by side in a wave: neighbours stay apart)
+        kw = dict(before=block.Norm(kind, 1e-6))
+        _, h = block.residual_norm(narrow, **kw)
+        for i in good:
+            check_norm([0, 1], 1, narrow[i:i + 1], None, None, h[i:i + 1], kw)
+        assert h[4].isnan().all() and not h[5].isfinite().all() and not h[6].isfinite().all()
     for kind in ("rms", "layer"):
         kw = dict(before=block.Norm(kind, 1e-6))
         _, h = block.residual_norm(x, **kw)

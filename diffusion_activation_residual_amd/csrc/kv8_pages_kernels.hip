@@ -84,7 +84,7 @@ __global__ __launch_bounds__(kThreads) void kv8_fork_kernel(Kv8Pages p, int coun
 // One work-group: which places need a page is a matter of a few thousand integers and of steps that
 // wait for each other, which costs less in one launch than spread over the card and several.  The
 // free pages are looked for from the front, kScan pages at a time, until there are enough.  96 rows, one token
-// each, 32 of them forked: 8.3 us, most of it reads that wait for each other (length, table, count,
+// each, 32 of them forked: 8.7 us, most of it reads that wait for each other (length, table, count,
 // holders); a scan step of 64 KB more for every 16,384 pages in use before the free ones.
 constexpr int kWide = 1024, kWaves = kWide / 64, kPieces = 16, kScan = kWide * kPieces;
 

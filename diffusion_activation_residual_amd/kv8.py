@@ -120,6 +120,18 @@ def _empty_on(device, stream, shape, dtype):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _workspace_on(device, stream, nbytes, workspace):
+    """The caller's workspace, or one from torch's allocator (None: no bytes), and its size.  The tensor has
+    to be held until the call is queued: from then on the stream's order keeps its memory."""
+    if workspace is not None:
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace: must be contiguous and on {device}")
+        return workspace, workspace.numel() * workspace.element_size()
+    if nbytes == 0:
+        return None, 0
+    return _empty_on(device, stream, nbytes, torch.uint8), nbytes
+
+
 def _queue(call, device, stream, *args):
     """The library's call on `stream` (a stream, its handle, or None: the current one)."""
     index = device.index
@@ -272,17 +284,6 @@ class Cache:
         if st != CFZ_OK:
             raise CfzError(st, call.__name__)
 
-    def _workspace(self, nbytes, workspace, stream):
-        """The caller's workspace, or one from torch's allocator that stays in use until the
-        work queued on `stream` is done."""
-        if workspace is not None:
-            if workspace.device != self.device or not workspace.is_contiguous():
-                raise ValueError("workspace: must be contiguous and on the cache's device")
-            return workspace, workspace.numel() * workspace.element_size()
-        if nbytes == 0:
-            return None, 0
-        return self._empty(stream, nbytes, torch.uint8), nbytes
-
     def _new_rows(self, k, v):
         """Row strides of new keys and values."""
         ks = _rows(k, self.kv_heads, self.head_dim, self.device, "k")
@@ -375,7 +376,7 @@ class Cache:
             lists = C.byref(self._lists(blocks, batch, max_q, q_block))
         need = _lib.cfz_kv8_attend_workspace_bytes(self._ref, C.byref(batch), heads,
                                                    max_kv, lists)
-        workspace, have = self._workspace(need, workspace, stream)
+        workspace, have = _workspace_on(self.device, stream, need, workspace)
         ostride = heads * self.head_dim
         if out is None:
             out = self._empty(stream, (tokens, heads, self.head_dim), q.dtype)
@@ -413,7 +414,7 @@ class Cache:
         lists = self._lists(blocks, batch, max_q, q_block, count)
         need = _lib.cfz_kv8_select_workspace_bytes(self._ref, C.byref(batch), max_kv,
                                                    C.byref(lists))
-        workspace, have = self._workspace(need, workspace, stream)
+        workspace, have = _workspace_on(self.device, stream, need, workspace)
         self._call(_lib.cfz_kv8_select, stream, self._ref, C.byref(batch), _REALS[q.dtype],
                    q.data_ptr(), stride, q.shape[1], bool(causal), max_kv, first, last,
                    C.byref(lists), None if workspace is None else workspace.data_ptr(), have)
@@ -516,9 +517,10 @@ class Pages:
         need = _lib.cfz_kv8_reserve_workspace_bytes(self._ref, max_new)
         source, target, missing = (_empty_on(self.device, stream, n, torch.int32)
                                    for n in (batch, batch, 1))
-        workspace, have = self._workspace(need, workspace, stream)
+        workspace, have = _workspace_on(self.device, stream, need, workspace)
         _queue(_lib.cfz_kv8_reserve, self.device, stream, self._ref, counts, max_new,
-               source.data_ptr(), target.data_ptr(), missing.data_ptr(), workspace, have)
+               source.data_ptr(), target.data_ptr(), missing.data_ptr(),
+               None if workspace is None else workspace.data_ptr(), have)
         return Moves(source, target), missing
 
     def compact(self, workspace=None, stream=None):
@@ -529,14 +531,8 @@ class Pages:
         need = _lib.cfz_kv8_compact_workspace_bytes(self._ref)
         source, target, live, count = (_empty_on(self.device, stream, n, torch.int32)
                                        for n in (most, most, 1, 1))
-        workspace, have = self._workspace(need, workspace, stream)
+        workspace, have = _workspace_on(self.device, stream, need, workspace)
         _queue(_lib.cfz_kv8_compact, self.device, stream, self._ref, source.data_ptr(),
-               target.data_ptr(), live.data_ptr(), count.data_ptr(), workspace, have)
+               target.data_ptr(), live.data_ptr(), count.data_ptr(),
+               None if workspace is None else workspace.data_ptr(), have)
         return Moves(source, target, count), live
-
-    def _workspace(self, need, workspace, stream):
-        if workspace is None:
-            workspace = _empty_on(self.device, stream, need, torch.uint8)
-        elif workspace.device != self.device or not workspace.is_contiguous():
-            raise ValueError("workspace: must be contiguous and on the table's device")
-        return workspace.data_ptr(), workspace.numel() * workspace.element_size()

@@ -368,6 +368,8 @@ class Adapters:
             raise ValueError(f"a: {a.dtype} {tuple(a.shape)}, b: {tuple(b.shape)}, expected bf16 or "
                              "fp16 [adapters, slices * rank, cols_in] and [adapters, cols_out, rank]")
         count, cols_out, rank = b.shape
+        if a.shape[0] != count:
+            raise ValueError(f"a has {a.shape[0]} adapters, b {count}")
         if isinstance(slices, int):
             if slices < 1 or cols_out % slices:
                 raise ValueError(f"slices = {slices} of {cols_out} columns")

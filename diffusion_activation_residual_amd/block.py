@@ -415,7 +415,7 @@ class Adapters:
         _queue(_lib.cfz_adapters_put, self.device, stream, self._ref, first, n, a.data_ptr())
         for held, new in ((self.b, b), (self.scale, scale)):
             if new is not None:
-                with torch.cuda.stream(_as_stream(stream, self.device)):
+                with torch.cuda.stream(_as_stream(stream, self.device)), torch.inference_mode():
                     held[first:first + n].copy_(new)
 
     def add(self, x, y, ids, offsets, max_rows, out=None, workspace=None, stream=None):

@@ -19,7 +19,7 @@ import torch
 
 from . import cfz, kv8
 from .cfz import CFZ_ERR_NULL, CFZ_OK, CfzError
-from .kv8 import _REALS, _empty_on, _fit, _ints, _queue, cfz_kv8_rotation
+from .kv8 import _REALS, _empty_on, _fit, _held, _ints, _queue, cfz_kv8_rotation
 
 NORMS = {"none": 0, "rms": 1, "layer": 2}
 SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3}
@@ -360,7 +360,10 @@ class Adapters:
     rank: a multiple of 8 up to 128; adapters of a lower one are filled up with zeros.
 
     a is copied into the layout that the kernels read; b and scale are used as they are.  ``put``
-    replaces adapters in place (a pool that requests bring theirs to)."""
+    replaces adapters in place (a pool that requests bring theirs to).  The calls know all three by their
+    addresses: another tensor in their place is refused (ValueError)."""
+
+    a, b, scale = map(_held, ("a", "b", "scale"))
 
     def __init__(self, a, b, scale=None, slices=1, stream=None):
         self.device = _device(a, "a")

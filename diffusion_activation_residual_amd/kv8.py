@@ -110,6 +110,21 @@ def _ints(t, shape, device, what):
     return t.data_ptr()
 
 
+def _held(name):
+    """An attribute whose tensor the library knows by its address: changed in place, never replaced."""
+    key = "_" + name
+
+    def get(self):
+        return getattr(self, key)
+
+    def put(self, t):
+        if self.__dict__.setdefault(key, t) is not t:
+            raise ValueError(f"{name}: the calls know this tensor by its address; change it in place "
+                             "(+=, copy_), or make a new object around another one")
+
+    return property(get, put)
+
+
 def _empty_on(device, stream, shape, dtype):
     """Memory that belongs to the work queued on `stream` (None: the current one)."""
     if stream is None:
@@ -193,8 +208,13 @@ class Cache:
     current one the caller orders the tensors' other uses, as for every call of the library.
     Nothing is recorded for autograd: results carry no gradient, whatever the inputs require.
 
+    The calls know the cache's tensors by their addresses: they may be changed in place, and another tensor
+    in their place is refused (ValueError; ``Cache.over`` makes a cache around other ones).
+
     int8 is the finer of the two where a head's channels are of one size.  Channels many times
     larger than the others leave the others only a few of its steps: e4m3 is meant for such tensors."""
+
+    k, v, k_scale, v_scale, k_mean = map(_held, ("k", "v", "k_scale", "v_scale", "k_mean"))
 
     def __init__(self, pages, kv_heads, head_dim, page_tokens=64, fmt="int8", pooled=True,
                  device="cuda"):
@@ -459,7 +479,10 @@ class Pages:
         cache.append(k, v, pages.table, pages.lengths, offsets, max_new)
         pages.lengths += counts
 
-    Every call is queued like those of ``Cache``; nothing is read by the host."""
+    Every call is queued like those of ``Cache``; nothing is read by the host.  The calls know the three
+    tensors by their addresses: another tensor in their place is refused (ValueError)."""
+
+    table, lengths, refs = map(_held, ("table", "lengths", "refs"))
 
     def __init__(self, table, lengths, refs, page_tokens):
         if not table.is_cuda:

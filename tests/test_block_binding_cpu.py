@@ -53,3 +53,16 @@ def test_adapters_made_in_inference_mode_are_replaced_outside_of_it(log):
         w = block.Adapters(rows(2, 8, 64), rows(2, 32, 8), rows(2, dtype=torch.float32))
     w.put(0, rows(1, 8, 64), torch.ones(1, 32, 8, dtype=BF), torch.ones(1))
     assert (w.b[0] == 1).all() and w.scale.tolist() == [1, 0]
+
+
+def test_factors_that_are_known_by_their_address_stay(log):
+    w = block.Adapters(rows(2, 8, 64), rows(2, 32, 8), rows(2, dtype=torch.float32))
+    plain = block.Adapters(rows(2, 8, 64), rows(2, 32, 8))
+    for held, name in ((w, "a"), (w, "b"), (w, "scale"), (plain, "scale")):
+        t = getattr(held, name)
+        with pytest.raises(ValueError, match=name):
+            setattr(held, name, torch.zeros(2) if t is None else t.clone())
+        assert getattr(held, name) is t
+    w.scale += 1
+    w.b *= 2
+    assert w.scale.tolist() == [1, 1] and w.desc.scale == w.scale.data_ptr()

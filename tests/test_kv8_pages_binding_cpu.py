@@ -7,6 +7,7 @@ import pytest
 import torch
 
 from diffusion_activation_residual_amd import kv8
+from test_kv8_cadence_cpu import cache
 
 CPU = torch.device("cpu")
 
@@ -47,3 +48,31 @@ def test_what_a_call_allocates_is_held_until_it_is_queued(call, monkeypatch):
     monkeypatch.setattr(kv8, "_queue", queue)
     call(table())
     assert len(queued) == 1 and len(queued[0]) >= 4
+
+
+@pytest.mark.parametrize("make,names", [
+    (table, ("table", "lengths", "refs")), (cache, ("k", "v", "k_scale", "v_scale", "k_mean")),
+    (lambda: cache(pooled=False), ("k", "k_mean"))])
+def test_tensors_that_are_known_by_their_address_stay(make, names):
+    held = make()
+    for name in names:
+        t = getattr(held, name)
+        for other in (torch.zeros(3) if t is None else t.clone(), None if t is not None else t):
+            if other is t:
+                continue
+            with pytest.raises(ValueError, match=name):
+                setattr(held, name, other)
+            assert getattr(held, name) is t
+        if t is None:
+            continue
+        at, want = t.data_ptr(), t.clone() + 1
+        setattr(held, name, t.add_(1))  # as ``held.name += 1`` does
+        assert getattr(held, name).data_ptr() == at and torch.equal(getattr(held, name), want)
+
+
+def test_lengths_go_on_in_place():
+    p = table()
+    with pytest.raises(ValueError, match="lengths"):
+        p.lengths = p.lengths + ints(3, 4)
+    p.lengths += ints(3, 4)
+    assert p.lengths.tolist() == [3, 4] and p.desc.lengths == p.lengths.data_ptr()

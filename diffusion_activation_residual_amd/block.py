@@ -304,6 +304,29 @@ def rotate(tensors, rotation, offsets=None, starts=None, weights=None, eps=1e-6,
     ``rotation`` (None: the norm alone).  Row i of sequence b (rows offsets[b] .. offsets[b + 1] - 1;
     no offsets: all rows are one sequence) is at position starts[b] + i, where ``rotation`` names no
     positions.  Keys turned here are appended to a cache without a rotation."""
+    args, device, results = _rotate(tensors, rotation, offsets, starts, weights, eps, normed, outs, stream)
+    _queue(_lib.cfz_rotate, device, stream, *args)
+    return results
+
+
+def check_rotate(tensors, rotation, offsets=None, starts=None, weights=None, eps=1e-6, normed=None):
+    """Raises where ``rotate`` would refuse these arguments (its results allocated by itself); queues
+    and allocates nothing."""
+    args, *_ = _rotate(tensors, rotation, offsets, starts, weights, eps, normed, None, None, False)
+    rows, tokens = args[1], args[4]
+    if rotation is None and not args[-2]:
+        raise CfzError(CFZ_ERR_NULL, "cfz_rotate")
+    for i, row in enumerate(rows):
+        if row.x % 16 if row.x else 0:
+            raise ValueError(f"tensors[{i}]: {row.x:#x}, expected 16-byte alignment")
+        row.x = None  # (with the results the last thing that the library asks for)
+    status = _lib.cfz_rotate(*args, None)
+    if status != (CFZ_OK if tokens == 0 else CFZ_ERR_NULL):
+        raise CfzError(status, "cfz_rotate")
+
+
+def _rotate(tensors, rotation, offsets, starts, weights, eps, normed, outs, stream, allocate=True):
+    """The call's arguments, checked as far as the library does not see them, and its results."""
     tensors = list(tensors)
     if not 1 <= len(tensors) <= 4:
         raise ValueError(f"{len(tensors)} tensors: one to four")
@@ -329,9 +352,10 @@ def rotate(tensors, rotation, offsets=None, starts=None, weights=None, eps=1e-6,
                              f"heads, {dim}]")
         heads = t.shape[1]
         stride = kv8._rows(t, heads, dim, device, f"tensors[{i}]")
-        out = None if outs is None else outs[i]
+        out, out_stride = None if outs is None else outs[i], heads * dim
         if out is None:
-            out, out_stride = _empty_on(device, stream, (tokens, heads, dim), dtype), heads * dim
+            if allocate:
+                out = _empty_on(device, stream, (tokens, heads, dim), dtype)
         else:
             if out.dtype != dtype or out.shape != t.shape:
                 raise ValueError(f"outs[{i}]: {out.dtype} {tuple(out.shape)}, expected {dtype} "
@@ -340,16 +364,16 @@ def rotate(tensors, rotation, offsets=None, starts=None, weights=None, eps=1e-6,
         if heads >= 1 << 31:
             _fit(32, heads=heads)
         row = args[i]
-        row.x, row.x_stride, row.out, row.out_stride = t.data_ptr(), stride, out.data_ptr(), out_stride
+        row.x, row.x_stride, row.out_stride = t.data_ptr(), stride, out_stride
+        row.out = None if out is None else out.data_ptr()
         row.heads = heads
         if w is not None:
             row.weight, row.weight_dtype = _vector(w, dim, dtype, device, f"weights[{i}]")
         results.append(out)
-    _queue(_lib.cfz_rotate, device, stream, len(tensors), args, _REALS[dtype], dim, tokens, batch,
-           None if offsets is None else _ints(offsets, (batch + 1,), device, "offsets"),
-           None if starts is None else _ints(starts, (batch,), device, "starts"),
-           kv8._rotation(rotation, tokens, device), bool(normed), eps)
-    return results
+    return (len(tensors), args, _REALS[dtype], dim, tokens, batch,
+            None if offsets is None else _ints(offsets, (batch + 1,), device, "offsets"),
+            None if starts is None else _ints(starts, (batch,), device, "starts"),
+            kv8._rotation(rotation, tokens, device), bool(normed), eps), device, results
 
 
 class Adapters:

@@ -92,8 +92,10 @@ class SharePlan:
         self.q_offsets = ints([i * queries for i in range(batch + 1)])
         self.q_starts = None if query_start is None else ints([query_start] * batch)
 
-    def _check_sizes(self, cache, q, keys):
+    def _check_sizes(self, cache, q, keys, weight=None):
         """Raises what the library refuses about these sizes."""
+        if self.q_starts is not None or self.head_norm is not None:
+            block.check_rotate(**self._turning(q, weight))
         for i, k in enumerate(keys):
             batch = cache._batch(self.table, self.starts[i], self.offsets[i], len(k),
                                  self.share_tokens[i])
@@ -121,10 +123,13 @@ class SharePlan:
         """The queries as they attend: their heads normed and turned as the plan says."""
         if self.q_starts is None and self.head_norm is None:
             return q
-        return block.rotate([q], None if self.q_starts is None else self.rotation, self.q_offsets,
-                            self.q_starts, weights=None if weight is None else [weight],
-                            normed=self.head_norm is not None,
-                            eps=0.0 if self.head_norm is None else self.head_norm, stream=stream)[0]
+        return block.rotate(**self._turning(q, weight), stream=stream)[0]
+
+    def _turning(self, q, weight):
+        return dict(tensors=[q], rotation=None if self.q_starts is None else self.rotation,
+                    offsets=self.q_offsets, starts=self.q_starts,
+                    weights=None if weight is None else [weight], normed=self.head_norm is not None,
+                    eps=0.0 if self.head_norm is None else self.head_norm)
 
     def attend(self, cache, q, out=None, lse=None, stream=None, q_weight=None):
         """The queries q [batch * queries, q_heads, head_dim] over all shares: (out, lse)."""
@@ -287,15 +292,17 @@ def _check_step(plan, layers, caches, q, out, streams, q_weights=None):
         _whole_rows(q[l], cache._queries(q[l]), l, "q")
         if out[l] is not None:
             _whole_rows(out[l], cache._outputs(q[l], out[l]), l, "out")
-        if q_weights is not None and q_weights[l] is not None:
-            block._vector(q_weights[l], cache.head_dim, q[l].dtype, cache.device, f"q_weights[{l}]")
+        weight = None if q_weights is None else q_weights[l]
+        if weight is not None:
+            block._vector(weight, cache.head_dim, q[l].dtype, cache.device, f"q_weights[{l}]")
         got = [s for s in shares if s.receivers is not None]
         if got:
             cfz.check_decompress_group(*_payload(got))
         sizes = (cache.kv_heads, cache.head_dim, cache.device, q[l].shape[1], q[l].dtype,
-                 tuple(s.k.dtype for s in shares))
+                 tuple(s.k.dtype for s in shares),
+                 None if weight is None else (weight.dtype, weight.data_ptr() % 16))
         if sizes not in alike:
-            plan._check_sizes(cache, q[l], [s.k for s in shares])
+            plan._check_sizes(cache, q[l], [s.k for s in shares], weight)
             alike.add(sizes)
 
 

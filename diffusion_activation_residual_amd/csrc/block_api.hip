@@ -313,11 +313,9 @@ cfz_status cfz_rotate(int32_t count, const cfz_rotate_rows *tensors, cfz_kv8_dty
         if (t.weight && !normed)
             return fail(CFZ_ERR_UNSUPPORTED, "tensor %d: a weight without a norm", i);
         CFZ_TRY(check_vec(t.weight, t.weight_dtype, dtype, "weight"));
-        if (tokens > 0 && (!t.x || !t.out))
-            return fail(CFZ_ERR_NULL, "tensor %d: x and out are required", i);
         if (!aligned(t.x, 16) || !aligned(t.out, 16))
             return fail(CFZ_ERR_ALIGN, "tensor %d: x and out must be 16-byte aligned", i);
-        if (t.x == t.out && t.x_stride != t.out_stride)
+        if (t.x && t.x == t.out && t.x_stride != t.out_stride)
             return fail(CFZ_ERR_SHAPE, "in place, the strides must be the same");
         a.t[i] = cfz::RotateRows{t.x,      t.out, t.weight, t.x_stride, t.out_stride,
                                  t.weight_dtype == CFZ_KV8_F32, t.heads, a.parts};
@@ -333,6 +331,9 @@ cfz_status cfz_rotate(int32_t count, const cfz_rotate_rows *tensors, cfz_kv8_dty
     if (cfz::rotate_groups(a) >= cfz::kBlockMaxGroups)
         return fail(CFZ_ERR_SHAPE, "the call needs %lld work-groups (limit 2^23)",
                     (long long)cfz::rotate_groups(a));
+    for (int i = 0; i < count; ++i)
+        if (!a.t[i].x || !a.t[i].out)
+            return fail(CFZ_ERR_NULL, "tensor %d: x and out are required", i);
     return hip_status(cfz::launch_rotate(a, dtype, (hipStream_t)hip_stream), "rotation launch");
 }
 

@@ -188,9 +188,10 @@ def check_residual_norm(x, y=None, *, out, normed, before=None, after=None, gate
         raise ValueError(f"x: {a.x:#x}, expected 16-byte alignment")
     if out is not None and a.r == a.x and a.r_stride != a.x_stride:
         raise ValueError("in place, the strides must be the same")
-    a.x = None  # (the last thing that the library asks for)
+    a.x = None  # (the last thing that the library asks for, after these two)
+    missing = not (a.r or a.h) or not a.y and (a.gate.data or a.after.kind)
     status = _lib.cfz_residual_norm(C.byref(a), None)
-    if status != (CFZ_OK if a.tokens == 0 else CFZ_ERR_NULL):
+    if status != (CFZ_OK if a.tokens == 0 else CFZ_ERR_NULL) or (missing and a.tokens):
         raise CfzError(status, "cfz_residual_norm")
 
 
@@ -314,14 +315,13 @@ def check_rotate(tensors, rotation, offsets=None, starts=None, weights=None, eps
     and allocates nothing."""
     args, *_ = _rotate(tensors, rotation, offsets, starts, weights, eps, normed, None, None, False)
     rows, tokens = args[1], args[4]
-    if rotation is None and not args[-2]:
-        raise CfzError(CFZ_ERR_NULL, "cfz_rotate")
+    nothing = rotation is None and not args[-2]  # (asked for before)
     for i, row in enumerate(rows):
         if row.x % 16 if row.x else 0:
             raise ValueError(f"tensors[{i}]: {row.x:#x}, expected 16-byte alignment")
         row.x = None  # (with the results the last thing that the library asks for)
     status = _lib.cfz_rotate(*args, None)
-    if status != (CFZ_OK if tokens == 0 else CFZ_ERR_NULL):
+    if nothing or status != (CFZ_OK if tokens == 0 else CFZ_ERR_NULL):
         raise CfzError(status, "cfz_rotate")
 
 

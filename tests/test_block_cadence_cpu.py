@@ -71,3 +71,56 @@ def test_work_groups_past_the_rotation_limit_are_refused_before_any_work(monkeyp
         cadence.enqueue_layer_attention(plan, [[cadence.Share(wide[0], wide[0])]], [c], [wide[1]],
                                         [wide[1]], [Stream(log)])
     assert log == []
+
+
+def features(log, monkeypatch, **second):
+    """Two layers; `second` replaces parts of the second one's step."""
+    monkeypatch.setattr(block, "residual_norm", lambda *a, **k: log.append("norm"))
+    monkeypatch.setattr(cfz, "cfz_compress_group", lambda *a, **k: log.append("compress"))
+    monkeypatch.setattr(cfz, "_bf16_ptr", lambda t: t.data_ptr())
+    monkeypatch.setattr(cfz, "_ptr", lambda t: t.data_ptr())
+
+    def wide():
+        return torch.zeros((4, 64), dtype=torch.bfloat16)
+
+    steps = []
+    for change in ({}, second):
+        x = wide()
+        steps.append(cadence.FeatureStep(**{**dict(x=x, y=wide(), out=x), **change}))
+    codes = [torch.zeros(512, dtype=torch.uint8) for _ in steps]
+    scales = [torch.zeros(32) for _ in steps]
+    cadence.enqueue_layer_features(steps, [10, 20], [wide() for _ in steps], codes, scales, [Stream(log)])
+
+
+NORM = dict(after=block.Norm("rms"))
+GATE = dict(gate=torch.zeros(64, dtype=torch.bfloat16))
+
+
+@pytest.mark.parametrize("kw", [{}, GATE, NORM, dict(y=None), dict(y=None, before=block.Norm("layer")),
+                                dict(y=None, after=block.Norm("none"))])
+def test_features_that_fit(kw, monkeypatch):
+    log = []
+    features(log, monkeypatch, **kw)
+    assert log == ["norm", "compress"] * 2
+
+
+@pytest.mark.parametrize("kw", [GATE, NORM])
+def test_a_gate_without_a_block_output_is_refused_before_any_work(kw, monkeypatch):
+    """The library's answer to that is the one by which the check knows that only x is left out."""
+    log = []
+    with pytest.raises((ValueError, cfz.CfzError)):
+        features(log, monkeypatch, y=None, **kw)
+    assert log == []
+
+
+def test_a_check_without_any_result():
+    x = torch.zeros((4, 64), dtype=torch.bfloat16)
+    with pytest.raises(cfz.CfzError, match="r and h"):
+        block.check_residual_norm(x, None, out=None, normed=None)
+
+
+@pytest.mark.parametrize("tokens", [0, 4])
+def test_a_check_of_neither_norm_nor_rotation(tokens):
+    with pytest.raises(cfz.CfzError, match="neither"):
+        block.check_rotate([rows(tokens)], None)
+    block.check_rotate([rows(tokens)], None, normed=True)

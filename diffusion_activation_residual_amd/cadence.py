@@ -121,6 +121,8 @@ class SharePlan:
 
     def turn(self, q, weight=None, stream=None):
         """The queries as they attend: their heads normed and turned as the plan says."""
+        if weight is not None and self.head_norm is None:
+            raise ValueError("a weight of the queries' heads: the plan has no head_norm")
         if self.q_starts is None and self.head_norm is None:
             return q
         return block.rotate(**self._turning(q, weight), stream=stream)[0]

@@ -124,3 +124,16 @@ def test_a_check_of_neither_norm_nor_rotation(tokens):
     with pytest.raises(cfz.CfzError, match="neither"):
         block.check_rotate([rows(tokens)], None)
     block.check_rotate([rows(tokens)], None, normed=True)
+
+
+@pytest.mark.parametrize("kw", [{}, dict(rotation=rotation(), query_start=0)])
+def test_a_weight_of_queries_that_are_not_normed_is_refused(kw, monkeypatch):
+    log = []
+    monkeypatch.setattr(kv8.Cache, "attend", lambda *a, **k: log.append("attend"))
+    monkeypatch.setattr(block, "rotate", lambda *a, **k: [log.append("rotate")])
+    plan = cadence.SharePlan(BATCH, TOKENS, QUERIES, PAGE, device="cpu", **kw)
+    with pytest.raises(ValueError, match="head_norm"):
+        plan.attend(cache(), rows(NQ, 4), q_weight=ones())
+    assert log == []
+    plan.attend(cache(), rows(NQ, 4))
+    assert log == ["rotate"] * bool(kw) + ["attend"]

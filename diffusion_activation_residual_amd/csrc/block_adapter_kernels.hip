@@ -358,6 +358,12 @@ template <class Y> struct RawRow {
         for (int i = 0; i < kBytes / kPiece; ++i)
             p[i] = __builtin_bit_cast(Piece, __builtin_nontemporal_load((const Words *)y + i));
     }
+    __device__ inline void store(Y *o) const
+    {
+#pragma unroll
+        for (int i = 0; i < kBytes / kPiece; ++i)
+            ((Words *)o)[i] = __builtin_bit_cast(Words, p[i]);
+    }
     __device__ inline void get(float (&o)[CB]) const
     {
         constexpr int E = kPiece / sizeof(Y);
@@ -451,27 +457,33 @@ __global__ __launch_bounds__(256) void adapter_up_kernel(AdapterArgs a)
             load(t0);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
+            const int t = t0 + u * 16 + q * 4;
+            if (!some) {  // y as it is, to the last bit
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (mine && t + i < n)
+                        v[u][i].store(out + (t + i) * a.os);
+                continue;
+            }
             f32x4 acc[CB];
 #pragma unroll
             for (int j = 0; j < CB; ++j)
                 acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             f32x4 f = {1.0f, 1.0f, 1.0f, 1.0f};
-            if (some) {
-                // (rows past the last one: zeros up to the tile's end)
-                const int row = t0 + u * 16 + m;
+            // (rows past the last one: zeros up to the tile's end)
+            const int row = t0 + u * 16 + m;
 #pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    const int at = row * RU + ((s * 4 + q) ^ (row / (16 / RU) % RU));
-                    const uint4 hi = hs[0][at], lo = hs[1][at];
+            for (int s = 0; s < KS; ++s) {
+                const int at = row * RU + ((s * 4 + q) ^ (row / (16 / RU) % RU));
+                const uint4 hi = hs[0][at], lo = hs[1][at];
 #pragma unroll
-                    for (int j = 0; j < CB; ++j) {
-                        acc[j] = Mfma<T>::mul(lo, w[j][s], acc[j]);
-                        acc[j] = Mfma<T>::mul(hi, w[j][s], acc[j]);
-                    }
+                for (int j = 0; j < CB; ++j) {
+                    acc[j] = Mfma<T>::mul(lo, w[j][s], acc[j]);
+                    acc[j] = Mfma<T>::mul(hi, w[j][s], acc[j]);
                 }
-                if (__is_same(T, _Float16))
-                    f = *(const f32x4 *)&back[t0 + u * 16 + q * 4];
             }
+            if (__is_same(T, _Float16))
+                f = *(const f32x4 *)&back[t0 + u * 16 + q * 4];
             // lane: token 4 q + i, columns CB m + j
             float o[4][CB];
 #pragma unroll
@@ -481,7 +493,6 @@ __global__ __launch_bounds__(256) void adapter_up_kernel(AdapterArgs a)
                 for (int j = 0; j < CB; ++j)
                     o[i][j] = fmaf(acc[j][i], f[i], o[i][j]);
             }
-            const int t = t0 + u * 16 + q * 4;
             if (whole && t0 + u * 16 + 16 <= n) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)

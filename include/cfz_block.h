@@ -177,7 +177,7 @@ cfz_status cfz_adapters_put(const cfz_adapters *adapters, int32_t first, int32_t
                             const void *rows, void *hip_stream);
 
 /* out = y + scale_a (x a^T) b^T for the token rows offsets[b] .. offsets[b + 1] - 1 of sequence b, with
- * adapter ids[b] (outside of 0 .. adapters - 1: none, out = y).  x: rows of `dtype`; y and out: rows
+ * adapter ids[b] (outside of 0 .. adapters - 1: none, out = y, every bit).  x: rows of `dtype`; y and out: rows
  * of y_dtype (dtype or F32); row strides in elements, multiples of 16 bytes.  out may be y with the same
  * stride; other overlaps are not allowed.  Rows of no sequence, and rows past a sequence's first
  * max_rows, are neither read nor written.  The products accumulate in fp32; x a^T enters the second one as the sum of

@@ -305,28 +305,29 @@ def rotate(tensors, rotation, offsets=None, starts=None, weights=None, eps=1e-6,
     ``rotation`` (None: the norm alone).  Row i of sequence b (rows offsets[b] .. offsets[b + 1] - 1;
     no offsets: all rows are one sequence) is at position starts[b] + i, where ``rotation`` names no
     positions.  Keys turned here are appended to a cache without a rotation."""
-    args, device, results = _rotate(tensors, rotation, offsets, starts, weights, eps, normed, outs, stream)
-    _queue(_lib.cfz_rotate, device, stream, *args)
-    return results
+    return _rotate(_queue, tensors, rotation, offsets, starts, weights, eps, normed, outs, stream)
 
 
 def check_rotate(tensors, rotation, offsets=None, starts=None, weights=None, eps=1e-6, normed=None):
     """Raises where ``rotate`` would refuse these arguments (its results allocated by itself); queues
     and allocates nothing."""
-    args, *_ = _rotate(tensors, rotation, offsets, starts, weights, eps, normed, None, None, False)
-    rows, tokens = args[1], args[4]
-    nothing = rotation is None and not args[-2]  # (asked for before)
+    _rotate(_ask, tensors, rotation, offsets, starts, weights, eps, normed, None, None)
+
+
+def _ask(call, device, stream, count, rows, *args):
+    """A rotation that is only checked: its tensors are left out, the last thing that the library asks for."""
     for i, row in enumerate(rows):
         if row.x % 16 if row.x else 0:
             raise ValueError(f"tensors[{i}]: {row.x:#x}, expected 16-byte alignment")
-        row.x = None  # (with the results the last thing that the library asks for)
-    status = _lib.cfz_rotate(*args, None)
+        row.x = None
+    tokens, rotation, normed = args[2], args[6], args[7]
+    nothing = rotation is None and not normed  # (asked for before)
+    status = call(count, rows, *args, None)
     if nothing or status != (CFZ_OK if tokens == 0 else CFZ_ERR_NULL):
-        raise CfzError(status, "cfz_rotate")
+        raise CfzError(status, call.__name__)
 
 
-def _rotate(tensors, rotation, offsets, starts, weights, eps, normed, outs, stream, allocate=True):
-    """The call's arguments, checked as far as the library does not see them, and its results."""
+def _rotate(queue, tensors, rotation, offsets, starts, weights, eps, normed, outs, stream):
     tensors = list(tensors)
     if not 1 <= len(tensors) <= 4:
         raise ValueError(f"{len(tensors)} tensors: one to four")
@@ -354,7 +355,7 @@ def _rotate(tensors, rotation, offsets, starts, weights, eps, normed, outs, stre
         stride = kv8._rows(t, heads, dim, device, f"tensors[{i}]")
         out, out_stride = None if outs is None else outs[i], heads * dim
         if out is None:
-            if allocate:
+            if queue is not _ask:
                 out = _empty_on(device, stream, (tokens, heads, dim), dtype)
         else:
             if out.dtype != dtype or out.shape != t.shape:
@@ -370,10 +371,11 @@ def _rotate(tensors, rotation, offsets, starts, weights, eps, normed, outs, stre
         if w is not None:
             row.weight, row.weight_dtype = _vector(w, dim, dtype, device, f"weights[{i}]")
         results.append(out)
-    return (len(tensors), args, _REALS[dtype], dim, tokens, batch,
-            None if offsets is None else _ints(offsets, (batch + 1,), device, "offsets"),
-            None if starts is None else _ints(starts, (batch,), device, "starts"),
-            kv8._rotation(rotation, tokens, device), bool(normed), eps), device, results
+    queue(_lib.cfz_rotate, device, stream, len(tensors), args, _REALS[dtype], dim, tokens, batch,
+          None if offsets is None else _ints(offsets, (batch + 1,), device, "offsets"),
+          None if starts is None else _ints(starts, (batch,), device, "starts"),
+          kv8._rotation(rotation, tokens, device), bool(normed), eps)
+    return results
 
 
 class Adapters:

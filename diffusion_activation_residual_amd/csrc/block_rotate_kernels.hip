@@ -60,8 +60,12 @@ __global__ __launch_bounds__(kThreads) void rotate_kernel(RotateArgs a)
 #pragma unroll
     for (int i = 0; i < kRotateUnits; ++i) {
         const int head = head0 + i * (64 >> a.log2lanes);
-        if (head >= t.heads)
+        if (head >= t.heads) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[i][j] = 0.0f;
             continue;
+        }
         if (split) {
             load_n(x + head * a.dim + d0, *(float(*)[4]) & v[i][0]);
             load_n(x + head * a.dim + d1, *(float(*)[4]) & v[i][4]);
@@ -86,21 +90,50 @@ __global__ __launch_bounds__(kThreads) void rotate_kernel(RotateArgs a)
         load_n(a.cos + pos * half + 4 * unit, co);
         load_n(a.sin + pos * half + 4 * unit, si);
     }
+    if (a.normed) {
+        // all units' sums side by side (heads past the last one hold zeros)
+        float square[kRotateUnits];
+        bool far = false;
 #pragma unroll
-    for (int i = 0; i < kRotateUnits; ++i) {
-        const int head = head0 + i * (64 >> a.log2lanes);
-        if (head >= t.heads)  // (the lanes of a head go together)
-            continue;
-        if (a.normed) {
+        for (int i = 0; i < kRotateUnits; ++i) {
             float q = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 q = fmaf(v[i][j], v[i][j], q);
-            const float f = rsqrtf(lanes_sum(q, lanes) * inv + a.eps);
+            square[i] = lanes_sum(q, lanes) * inv + a.eps;
+            far |= !norm_in_range(square[i]);
+        }
+        if (far) {  // (the same for all lanes of a head)
+#pragma unroll
+            for (int i = 0; i < kRotateUnits; ++i) {
+                if (norm_in_range(square[i]))
+                    continue;
+                float top = 0.0f, q = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    top = fmaxf(top, fabsf(v[i][j]));
+                const float shrink = norm_shrink(lanes_max(top, lanes), a.eps);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    v[i][j] *= shrink;
+                    q = fmaf(v[i][j], v[i][j], q);
+                }
+                square[i] = lanes_sum(q, lanes) * inv + a.eps * shrink * shrink;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kRotateUnits; ++i) {
+            const float f = rsqrtf(square[i]);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 v[i][j] *= f * w[j];
         }
+    }
+#pragma unroll
+    for (int i = 0; i < kRotateUnits; ++i) {
+        const int head = head0 + i * (64 >> a.log2lanes);
+        if (head >= t.heads)
+            continue;
         if (turn) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {

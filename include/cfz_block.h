@@ -24,8 +24,9 @@ extern "C" {
  *   RMS:   v / sqrt(mean(v^2) + eps) * weight
  *   LAYER: (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) * weight + bias
  * weight and bias: [cols] of `dtype`, or NULL (1 and 0; a bias goes with LAYER only).  eps is
- * finite and >= 0.  Squares are summed in fp32: values past 2^63 / sqrt(cols) may overflow it, and a
- * row that is 0 (or all of one value, LAYER) with eps = 0 is 0 / 0. */
+ * finite and >= 0.  Rows whose squares vanish in fp32 or leave its range are scaled by a power of two
+ * before they are squared; what may overflow is a LAYER norm's sum of values past 2^127 / cols.  A row
+ * that is 0 (or all of one value, LAYER) with eps = 0 is 0 / 0. */
 typedef enum { CFZ_NORM_NONE = 0, CFZ_NORM_RMS = 1, CFZ_NORM_LAYER = 2 } cfz_norm_kind;
 typedef struct {
     int32_t kind;
@@ -134,6 +135,8 @@ typedef struct {
 /* Norm and rotation of each head, for up to 4 tensors (queries and keys) of the same tokens:
  *   v = x / sqrt(mean(x^2) + eps) * weight over a head (if `normed`, else v = x),
  * and the first rot_dim dimensions of v turned in pairs as cfz_kv8_append turns keys.
+ * Heads whose squares vanish in fp32 or leave its range are scaled by a power of two before they are
+ * squared; a head that is 0 with eps = 0 is 0 / 0.
  * rotation NULL: the norm alone.  Without rotation->positions, row i of sequence b is at position
  * starts[b] + i (starts NULL: i).  Positions outside the table take its nearest row.
  * head_dim in {32, 64, 128, 256}, rot_dim a multiple of 8 up to it, heads 1 .. 1024 each.

@@ -180,6 +180,32 @@ cfz_status check_compact(const cfz::Kv8Pages &p)
     return check_groups((double)p.batch * p.width / 256 + 1);
 }
 
+cfz_status reserve(const cfz_kv8_pages *pages, const int32_t *counts, int64_t max_new,
+                   int32_t *source, int32_t *target, int32_t *missing, int32_t *left_out,
+                   void *workspace, size_t ws_bytes, void *hip_stream)
+{
+    cfz::Kv8Pages p;
+    cfz::Kv8Reserve r;
+    CFZ_TRY(check_table(pages, &p));
+    CFZ_TRY(check_reserve(p, max_new, &r));
+    CFZ_TRY(check_table_pointers(p));
+    if (!counts || !source || !target || !missing)
+        return fail(CFZ_ERR_NULL, "counts, source, target and missing are required");
+    if (!aligned(counts, 4) || !aligned(source, 4) || !aligned(target, 4) || !aligned(missing, 4))
+        return fail(CFZ_ERR_ALIGN, "counts, source, target and missing must be 4-byte aligned");
+    CFZ_TRY(check_workspace(workspace, ws_bytes, (size_t)cfz::kv8_reserve_ints(p, r) * 4));
+    r.counts = counts;
+    r.source = source;
+    r.target = target;
+    r.missing = missing;
+    r.left_out = left_out;
+    r.rank = (int32_t *)workspace;
+    r.list = r.rank + r.places;
+    r.owner = r.list + r.fresh;
+    r.writers = r.owner + p.pages;
+    return hip_status(cfz::launch_kv8_reserve(p, r, (hipStream_t)hip_stream), "reserve launch");
+}
+
 size_t compact_ints(const cfz::Kv8Pages &p) { return (size_t)cfz::kv8_compact_chunks(p) + p.pages; }
 
 }  // namespace
@@ -417,25 +443,21 @@ cfz_status cfz_kv8_reserve(const cfz_kv8_pages *pages, const int32_t *counts, in
                            int32_t *source, int32_t *target, int32_t *missing, void *workspace,
                            size_t ws_bytes, void *hip_stream)
 {
-    cfz::Kv8Pages p;
-    cfz::Kv8Reserve r;
-    CFZ_TRY(check_table(pages, &p));
-    CFZ_TRY(check_reserve(p, max_new, &r));
-    CFZ_TRY(check_table_pointers(p));
-    if (!counts || !source || !target || !missing)
-        return fail(CFZ_ERR_NULL, "counts, source, target and missing are required");
-    if (!aligned(counts, 4) || !aligned(source, 4) || !aligned(target, 4) || !aligned(missing, 4))
-        return fail(CFZ_ERR_ALIGN, "counts, source, target and missing must be 4-byte aligned");
-    CFZ_TRY(check_workspace(workspace, ws_bytes, (size_t)cfz::kv8_reserve_ints(p, r) * 4));
-    r.counts = counts;
-    r.source = source;
-    r.target = target;
-    r.missing = missing;
-    r.rank = (int32_t *)workspace;
-    r.list = r.rank + r.places;
-    r.owner = r.list + r.fresh;
-    r.writers = r.owner + p.pages;
-    return hip_status(cfz::launch_kv8_reserve(p, r, (hipStream_t)hip_stream), "reserve launch");
+    return reserve(pages, counts, max_new, source, target, missing, nullptr, workspace, ws_bytes,
+                   hip_stream);
+}
+
+cfz_status cfz_kv8_reserve_rows(const cfz_kv8_pages *pages, const int32_t *counts, int64_t max_new,
+                                int32_t *source, int32_t *target, int32_t *missing,
+                                int32_t *left_out, void *workspace, size_t ws_bytes,
+                                void *hip_stream)
+{
+    if (!left_out)
+        return fail(CFZ_ERR_NULL, "left_out is required");
+    if (!aligned(left_out, 4))
+        return fail(CFZ_ERR_ALIGN, "left_out must be 4-byte aligned");
+    return reserve(pages, counts, max_new, source, target, missing, left_out, workspace, ws_bytes,
+                   hip_stream);
 }
 
 size_t cfz_kv8_compact_workspace_bytes(const cfz_kv8_pages *pages)

@@ -108,6 +108,7 @@ struct Kv8Reserve {
     int64_t places, fresh;
     int32_t *rank, *list, *owner, *writers;
     int32_t *source, *target, *missing;
+    int32_t *left_out;  // null: not wanted
 };
 Kv8Reserve kv8_reserve_plan(const Kv8Pages &p, int64_t max_new);
 int64_t kv8_reserve_ints(const Kv8Pages &p, const Kv8Reserve &r);

@@ -94,8 +94,15 @@ __global__ __launch_bounds__(kWide) void kv8_reserve_kernel(Kv8Pages p, Kv8Reser
     __shared__ int sums[kWaves];
     __shared__ int list[kWide];  // the first free pages; more of them go through memory
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    for (int b = tid; b < p.batch; b += kWide)
+    for (int b = tid; b < p.batch; b += kWide) {
         r.source[b] = r.target[b] = -1;
+        if (r.left_out) {
+            const int64_t room = ((int64_t)p.width << p.log2page) - held_tokens(p, b);
+            const int64_t want = r.counts[b] < 0 ? 0 : r.counts[b];
+            const int64_t most = r.max_new < room ? r.max_new : room;
+            r.left_out[b] = (int)(want > most ? want - most : 0);
+        }
+    }
 
     // a place: its row, its place in the row, and the page it names (-1: none, -2: not written)
     const uint32_t span = (uint32_t)r.span;

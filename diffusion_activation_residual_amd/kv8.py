@@ -68,6 +68,7 @@ _SIGNATURES = {
     "cfz_kv8_free": ([_pages, _i32, _p, _p, _p], _i32),
     "cfz_kv8_fork": ([_pages, _i32, _p, _p, _p], _i32),
     "cfz_kv8_reserve": ([_pages, _p, _i64, _p, _p, _p, _p, _sz, _p], _i32),
+    "cfz_kv8_reserve_rows": ([_pages, _p, _i64, _p, _p, _p, _p, _p, _sz, _p], _i32),
     "cfz_kv8_reserve_workspace_bytes": ([_pages, _i64], _sz),
     "cfz_kv8_compact": ([_pages, _p, _p, _p, _p, _p, _sz, _p], _i32),
     "cfz_kv8_compact_workspace_bytes": ([_pages], _sz),
@@ -460,11 +461,13 @@ class Cache:
 @dataclass
 class Moves:
     """Pages to be copied (``Cache.copy``): ``source`` and ``target`` int32, -1 where there is nothing
-    to do; ``count`` int32 [1], how many of them are meant (None: all)."""
+    to do; ``count`` int32 [1], how many of them are meant (None: all).  ``left_out`` int32 [batch] (of
+    ``Pages.reserve``): how many of a row's new tokens have no place."""
 
     source: torch.Tensor
     target: torch.Tensor
     count: Optional[torch.Tensor] = None
+    left_out: Optional[torch.Tensor] = None
 
 
 class Pages:
@@ -477,7 +480,7 @@ class Pages:
         moves, missing = pages.reserve(counts, max_new)  # pages for counts[b] more tokens a row
         cache.copy(moves)                                # shared pages about to be written
         cache.append(k, v, pages.table, pages.lengths, offsets, max_new)
-        pages.lengths += counts
+        pages.lengths += counts - moves.left_out         # (rows that are full take no more)
 
     Every call is queued like those of ``Cache``; nothing is read by the host.  The calls know the three
     tensors by their addresses: another tensor in their place is refused (ValueError)."""
@@ -533,18 +536,20 @@ class Pages:
         """Pages for counts[b] (int32 [batch], at most ``max_new``) more tokens behind each row's
         length, and pages of its own where it would write into one that other rows hold too:
         (moves, missing).  ``moves`` [batch] are to be copied in every cache before the tokens are appended.
-        ``missing`` (int32 [1]) is 0, or how many more free pages it takes: then nothing has changed."""
+        ``missing`` (int32 [1]) is 0, or how many more free pages it takes: then nothing has changed.
+        ``moves.left_out`` [batch] says how many of a row's counts[b] tokens have no place: those past ``max_new``
+        or past the table's end, which ``Cache.append`` drops."""
         _fit(64, max_new=max_new)
         batch = self.table.shape[0]
         counts = _ints(counts, (batch,), self.device, "counts")
         need = _lib.cfz_kv8_reserve_workspace_bytes(self._ref, max_new)
-        source, target, missing = (_empty_on(self.device, stream, n, torch.int32)
-                                   for n in (batch, batch, 1))
+        out = _empty_on(self.device, stream, 3 * batch + 1, torch.int32)
+        source, target, left_out, missing = out.split([batch, batch, batch, 1])
         workspace, have = _workspace_on(self.device, stream, need, workspace)
-        _queue(_lib.cfz_kv8_reserve, self.device, stream, self._ref, counts, max_new,
-               source.data_ptr(), target.data_ptr(), missing.data_ptr(),
+        _queue(_lib.cfz_kv8_reserve_rows, self.device, stream, self._ref, counts, max_new,
+               source.data_ptr(), target.data_ptr(), missing.data_ptr(), left_out.data_ptr(),
                None if workspace is None else workspace.data_ptr(), have)
-        return Moves(source, target), missing
+        return Moves(source, target, left_out=left_out), missing
 
     def compact(self, workspace=None, stream=None):
         """Moves the pages in use to the front of the pool, the highest to the lowest free one:

@@ -233,7 +233,8 @@ cfz_status cfz_kv8_fork(const cfz_kv8_pages *pages, int32_t count, const int32_t
  * up, to the places row by row.  Where such a place already holds tokens of its row (lengths[b] inside a
  * page), source[b] and target[b] (int32 [batch] each) get the old and the new page, whose contents the
  * caller then copies (cfz_kv8_copy); otherwise they are -1.  Lengths stay as they are, so
- * calling twice gives out nothing twice.  Places past the table's end are left out.
+ * calling twice gives out nothing twice.  Places past the table's end are left out
+ * (cfz_kv8_reserve_rows says how many tokens that costs).
  * missing[0] gets 0 -- or, where there are not enough free pages, how many more it takes: then nothing
  * is given out.
  * workspace: cfz_kv8_reserve_workspace_bytes(...) bytes, 256-byte aligned, overwritten.
@@ -241,6 +242,13 @@ cfz_status cfz_kv8_fork(const cfz_kv8_pages *pages, int32_t count, const int32_t
 cfz_status cfz_kv8_reserve(const cfz_kv8_pages *pages, const int32_t *counts, int64_t max_new,
                            int32_t *source, int32_t *target, int32_t *missing, void *workspace,
                            size_t ws_bytes, void *hip_stream);
+/* cfz_kv8_reserve that also says which rows are full: left_out[b] (int32 [batch]) gets how many of the
+ * counts[b] tokens have no place, those past max_new or past the table's end, whatever missing[0] is.
+ * The caller's lengths go on by counts[b] - left_out[b] (counts below 0 as 0): cfz_kv8_append drops the others. */
+cfz_status cfz_kv8_reserve_rows(const cfz_kv8_pages *pages, const int32_t *counts, int64_t max_new,
+                                int32_t *source, int32_t *target, int32_t *missing,
+                                int32_t *left_out, void *workspace, size_t ws_bytes,
+                                void *hip_stream);
 /* 0 if none is needed or the arguments are invalid. */
 size_t cfz_kv8_reserve_workspace_bytes(const cfz_kv8_pages *pages, int64_t max_new);
 

@@ -45,6 +45,11 @@ class Pages:
                 self.table[c][e] = page
             self.lengths[c] = n
 
+    def left_out(self, counts, max_new):
+        """How many tokens of each row a reserve call has no place for."""
+        return [max(0, n) - min(max(0, n), max_new, self.width * self.page - self.held(b))
+                for b, n in enumerate(counts)]
+
     def reserve(self, counts, max_new):
         batch = len(self.table)
         source, target = [-1] * batch, [-1] * batch

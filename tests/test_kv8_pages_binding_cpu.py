@@ -6,8 +6,10 @@ import weakref
 import pytest
 import torch
 
-from diffusion_activation_residual_amd import kv8
+from diffusion_activation_residual_amd import cfz, kv8
+from test_kv8_boundary_cpu import A
 from test_kv8_cadence_cpu import cache
+from test_kv8_pages_boundary_cpu import pages
 
 CPU = torch.device("cpu")
 
@@ -47,7 +49,7 @@ def test_what_a_call_allocates_is_held_until_it_is_queued(call, monkeypatch):
     monkeypatch.setattr(kv8, "_empty_on", empty)
     monkeypatch.setattr(kv8, "_queue", queue)
     call(table())
-    assert len(queued) == 1 and len(queued[0]) >= 4
+    assert len(queued) == 1 and len(queued[0]) >= 2
 
 
 @pytest.mark.parametrize("make,names", [
@@ -76,3 +78,13 @@ def test_lengths_go_on_in_place():
         p.lengths = p.lengths + ints(3, 4)
     p.lengths += ints(3, 4)
     assert p.lengths.tolist() == [3, 4] and p.desc.lengths == p.lengths.data_ptr()
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(left_out=None), cfz.CFZ_ERR_NULL), (dict(left_out=A + 2), cfz.CFZ_ERR_ALIGN),
+    (dict(counts=None), cfz.CFZ_ERR_NULL), (dict(source=None), cfz.CFZ_ERR_NULL),
+    (dict(max_new=-1), cfz.CFZ_ERR_SHAPE), (dict(ws=None), cfz.CFZ_ERR_WORKSPACE)])
+def test_refusals_of_reserve_rows(change, status):
+    kw = dict(counts=A, max_new=64, source=A, target=A, missing=A, left_out=A, ws=A)
+    kw.update(change)
+    assert kv8._lib.cfz_kv8_reserve_rows(C.byref(pages()), *kw.values(), 1 << 20, None) == status

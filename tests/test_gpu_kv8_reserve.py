@@ -54,3 +54,56 @@ def test_left_out_of_many_rows(seed):
     m.lengths = [int(n) for n in rng.integers(-3, 110, 2500)]
     p.lengths.copy_(ints(m.lengths))
     reserve(p, m, rng.integers(-2, 60, 2500), int(rng.integers(0, 80)))
+
+
+def crowded(pages, free, batch, width, rng, page=32):
+    """Rows that hold every page but the free ones, in any order; the last rows are empty."""
+    used = np.setdiff1d(np.arange(pages), free)
+    table = np.full((batch, width), -1)
+    table.reshape(-1)[:len(used)] = rng.permutation(used)
+    refs = np.zeros(pages, int)
+    refs[used] = 1
+    return both(table, (table >= 0).sum(1) * page, refs, page)
+
+
+@pytest.mark.parametrize("need", [1, 1023, 1024, 1025, 2049, 3000])
+def test_free_pages_behind_many_in_use(need):
+    """Free pages on either side of every 16,384 looked at, and more of them than the chip keeps."""
+    rng = np.random.default_rng(need)
+    around = np.concatenate([np.arange(k - 3, k + 3) for k in (16384, 32768, 49152)])
+    free = np.concatenate([[5], around, np.sort(rng.choice(np.arange(49200, 56000), need, False))])
+    p, m = crowded(56000, free, 900, 70, rng)
+    assert m.lengths[805:] == [0] * 95
+    counts = np.zeros(900, int)
+    pages = need + 5  # (some of the last ones stay free)
+    for row in range(810, 900):
+        counts[row] = 32 * min(pages, 70) - int(rng.integers(0, 32) if pages > 1 else 0)
+        pages -= min(pages, 70)
+    assert pages == 0
+    _, lack = reserve(p, m, counts, 70 * 32)
+    assert lack == 0
+    # what is left is not enough: nothing changes, after looking through all of them
+    again = np.zeros(900, int)
+    again[805:810] = 70 * 32
+    _, lack = reserve(p, m, again, 70 * 32)
+    assert lack == 5 * 70 - (len(free) - need - 5)
+
+
+def test_many_copies_of_shared_pages():
+    """More than 1024 rows about to write into pages that others hold; the new pages come through memory."""
+    rng = np.random.default_rng(7)
+    p, m = crowded(20000, np.arange(100, 20000, 5), 6000, 4, rng)
+    lengths = [max(0, n - int(k)) for n, k in zip(m.lengths, rng.integers(1, 32, 6000))]
+    m.lengths = lengths
+    p.lengths.copy_(ints(lengths))
+    first = next(i for i in range(6000) if m.table[i][0] < 0)
+    children = np.arange(first, 6000)
+    parents = rng.integers(0, 900, len(children))
+    p.fork(ints(parents), ints(children))
+    m.fork(list(map(int, parents)), list(map(int, children)))
+    check(p, m)
+    moves, lack = reserve(p, m, np.ones(6000, int), 1)
+    assert lack == 0 and (moves.source >= 0).sum() > 1024
+    p.free(ints(children))
+    m.free(list(map(int, children)))
+    check(p, m)

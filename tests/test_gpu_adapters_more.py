@@ -36,3 +36,54 @@ def test_rows_without_an_adapter_keep_every_bit(real, wide, slices):
     held = y.clone()
     w.add(x, held, ints(ids), ints(off), 70, out=held)
     assert torch.equal(held.view(like), out.view(like))
+
+
+def ragged(tokens, batch, rng):
+    """Lengths of tokens in all, one sequence empty, ends off the tiles' borders."""
+    cuts = np.sort(rng.choice(np.arange(1, tokens), batch - 2, False))
+    return [int(n) for n in np.concatenate([[0], cuts, cuts[-1:], [tokens]])]
+
+
+def run(seed, tokens, batch, cols_in, slices, rank, real, wide=False):
+    rng, g = np.random.default_rng([seed, tokens, cols_in]), Gen(seed)
+    w = make(g, 4, cols_in, slices, rank, real)
+    off = ragged(tokens, batch, rng)
+    ids = [int(i) for i in rng.integers(-1, 5, batch)]
+    ids[0] = 2
+    x = g(tokens, cols_in, dtype=REAL[real])
+    y = g(tokens, sum(slices), dtype=torch.float32 if wide else REAL[real])
+    out = w.add(x, y, ints(ids), ints(off), tokens)
+    check(w, x, y, out, ids, off, real)
+
+
+@pytest.mark.parametrize("real", ["bf16", "f16"])
+@pytest.mark.parametrize("slices,rank", [([16], 8), ([16, 32, 16], 8), ([32], 24), ([16, 48], 24),
+                                         ([64], 64), ([16, 16], 40), ([16, 32, 16], 32), ([16], 96),
+                                         ([16, 16, 16, 16], 24)])
+@pytest.mark.parametrize("cols_in", [8, 136, 1000, 1928])
+def test_tiles_of_64_tokens(real, slices, rank, cols_in):
+    """Sequences long enough for 128 tiles of 64 tokens, up to 96 adapter rows; columns that leave waves
+    without any, and that end inside a step."""
+    run(rank, 8300, 5, cols_in, slices, rank, real)
+
+
+@pytest.mark.parametrize("real", ["bf16", "f16"])
+@pytest.mark.parametrize("tokens,batch,slices,rank", [
+    (8063, 3, [16], 32), (8064, 3, [16], 32), (7999, 3, [16], 32),  # 128 tiles, 129, and 127
+    (4095, 64, [16], 32), (4096, 64, [16], 32),                     # 63 and 64 tokens a sequence
+    (8300, 3, [16, 16], 48), (8300, 3, [16], 104), (8300, 3, [16], 128), (8300, 3, [16, 16], 72),
+    (500, 16, [16], 64), (512, 16, [16], 64), (300, 3, [16, 16], 64), (300, 3, [16, 16, 16], 48)])
+def test_either_side_of_the_tiles_thresholds(real, tokens, batch, slices, rank):
+    run(tokens, tokens, batch, 264, slices, rank, real, wide=real == "bf16")
+
+
+@pytest.mark.parametrize("real", ["bf16", "f16"])
+def test_a_prompt_beside_single_tokens(real):
+    g = Gen(51)
+    w = make(g, 3, 520, [32, 16], 16, real)
+    counts = [1] * 40 + [700] + [1] * 30
+    off = [int(n) for n in np.concatenate([[0], np.cumsum(counts)])]
+    ids = [i % 5 - 1 for i in range(len(counts))]
+    ids[40] = 1
+    x, y = g(off[-1], 520, dtype=REAL[real]), g(off[-1], 48, dtype=REAL[real])
+    check(w, x, y, w.add(x, y, ints(ids), ints(off), 700), ids, off, real)

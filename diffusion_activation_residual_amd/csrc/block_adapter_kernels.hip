@@ -564,10 +564,12 @@ int64_t adapter_groups(const AdapterArgs &a)
     return down > up ? down : up;
 }
 
-// The more tokens a tile of the first product has, the less often A is read: 64, where sequences fill such
-// tiles and half of the card's 256 units get one, and the sums of up to 96 adapter rows fit the registers
+// The more tokens a tile of the first product has, the less often A is read: 64, where sequences have as many on
+// the average, half of the card's 256 units get a whole tile and the sums of up to 96 adapter rows fit the registers
 // (2 x 4388 rows of 1920 at 96 adapter rows: 15.1 us, with 32 tokens 16.8; ragged prompts of 4096 columns at 64:
-// 29.2 and 33.9); else 32, up to 128 adapter rows; else 16.  Four waves a tile of 32, eight of the others.  More than 256 adapter rows are
+// 29.2 and 33.9; but 64 sequences of 64 tokens, 64 tiles: 15.5 and 11.6); else 32, up to 128 adapter rows; else 16
+// (1000 tokens beside 63 single ones: 8.8 us, with 32 tokens a tile 11.6; 4000 beside 200: 14.2, 15.0, with 64 23.3;
+// 8000 beside 300: 23.6, 22.9, 25.9).  Four waves a tile of 32, eight of the others.  More than 256 adapter rows are
 // two work-groups' a tile, two slices each.
 void adapter_plan(AdapterArgs &a)
 {
@@ -579,11 +581,11 @@ void adapter_plan(AdapterArgs &a)
     // (two slices together end with a block of 16 rows, whatever their rank)
     a.parts = a.down > 256 ? 2 : 1;
     a.part_rows = a.parts == 2 ? 2 * a.rank : a.down;
-    const int64_t t = a.rows.tokens, most = t / (a.rows.batch > 0 ? a.rows.batch : 1);
-    if (a.part_rows <= 96 && most >= 64 && adapter_tiles(a, 64) >= 128)
+    const int64_t t = a.rows.tokens, mean = t / (a.rows.batch > 0 ? a.rows.batch : 1);
+    if (a.part_rows <= 96 && mean >= 64 && t / 64 >= 128)
         a.tall = 4;
     else
-        a.tall = a.part_rows <= 128 && most >= 32 ? 2 : 1;
+        a.tall = a.part_rows <= 128 && mean >= 32 ? 2 : 1;
 }
 
 int64_t adapter_pieces(const AdapterArgs &a)

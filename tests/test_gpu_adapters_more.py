@@ -69,8 +69,9 @@ def test_tiles_of_64_tokens(real, slices, rank, cols_in):
 
 @pytest.mark.parametrize("real", ["bf16", "f16"])
 @pytest.mark.parametrize("tokens,batch,slices,rank", [
-    (8063, 3, [16], 32), (8064, 3, [16], 32), (7999, 3, [16], 32),  # 128 tiles, 129, and 127
-    (4095, 64, [16], 32), (4096, 64, [16], 32),                     # 63 and 64 tokens a sequence
+    (8191, 3, [16], 32), (8192, 3, [16], 32),      # 127 whole tiles of 64 tokens, and 128
+    (8256, 130, [16], 32), (8320, 130, [16], 32),  # 63 and 64 tokens a sequence
+    (4095, 64, [16], 32), (4096, 64, [16], 32),
     (8300, 3, [16, 16], 48), (8300, 3, [16], 104), (8300, 3, [16], 128), (8300, 3, [16, 16], 72),
     (500, 16, [16], 64), (512, 16, [16], 64), (300, 3, [16, 16], 64), (300, 3, [16, 16, 16], 48)])
 def test_either_side_of_the_tiles_thresholds(real, tokens, batch, slices, rank):

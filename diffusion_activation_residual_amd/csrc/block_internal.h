@@ -209,31 +209,8 @@ __device__ inline float lanes_sum(float x, int lanes)
     return x;
 }
 
-// The larger of x and another lane's x, by DPP.
-template <int CTRL> __device__ inline float max_lane(float x)
-{
-    const int o = __builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), CTRL, 0xf, 0xf, true);
-    return fmaxf(x, __uint_as_float((uint32_t)o));
-}
-
-// The largest over groups of lanes, as lanes_sum.
-__device__ inline float lanes_max(float x, int lanes)
-{
-    x = max_lane<0xb1>(x);
-    x = max_lane<0x4e>(x);
-    if (lanes >= 8)
-        x = max_lane<0x141>(x);
-    if (lanes >= 16)
-        x = max_lane<0x140>(x);
-    if (lanes >= 32)
-        x = fmaxf(x, __shfl_xor(x, 16));
-    if (lanes >= 64)
-        x = fmaxf(x, __shfl_xor(x, 32));
-    return x;
-}
-
 // Whether a mean of squares plus eps says what it should in fp32: squares below 2^-149 vanish, and those from
-// 2^128 on overflow.  Where it does not, the row is multiplied by norm_shrink and summed once more.
+// 2^128 on overflow.  Where it does not, the row is multiplied by norm_step and summed once more.
 // (From 2^-96 up to infinity: the bits of numbers that are not negative are in their order, a NaN's behind.)
 __device__ inline bool norm_in_range(float mean)
 {
@@ -241,13 +218,9 @@ __device__ inline bool norm_in_range(float mean)
     return __builtin_expect(__float_as_uint(mean) - low < high - low, 1);
 }
 
-// A power of two that brings the largest of a row's magnitudes and the root of eps to about 1 (0 and what
-// is not finite stay what they are).
-__device__ inline float norm_shrink(float top, float eps)
-{
-    int e = (int)(__float_as_uint(fmaxf(top, sqrtf(eps))) >> 23) - 127;
-    e = e > 126 ? 126 : (e < -126 ? -126 : e);
-    return __uint_as_float((uint32_t)(127 - e) << 23);
-}
+// A power of two.  Means below 2^-96: a row's values, 2^-149 to 2^-41, come to 2^-45 to 2^63.  Infinite ones: the
+// largest, 2^56 to 2^128, come to 2^-24 to 2^48, and 16,384 squares of them to 2^110 at most (what then falls
+// below fp32's range is 2^-102 of the largest).
+__device__ inline float norm_step(float mean) { return mean < 1.0f ? 0x1p104f : 0x1p-80f; }
 
 }  // namespace cfz

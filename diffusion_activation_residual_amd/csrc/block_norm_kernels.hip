@@ -21,20 +21,6 @@ template <int G> __device__ inline float row_sum(float x, float *red)
     return G == 128 ? red[0] + red[1] : (red[0] + red[1]) + (red[2] + red[3]);
 }
 
-// Largest over the threads that hold one row.
-template <int G> __device__ inline float row_max(float x, float *red)
-{
-    x = lanes_max(x, G < 64 ? G : 64);
-    if (G <= 64)
-        return x;
-    const int wave = threadIdx.x >> 6;
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0)
-        red[wave] = x;
-    __syncthreads();
-    return G == 128 ? fmaxf(red[0], red[1]) : fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-}
-
 // v becomes its norm, in two passes over registers: the mean first, so that nothing cancels in
 // the squares' sum.  Vectors past the row hold zeros and are left out of the second pass.
 template <class T, int V, int G>
@@ -66,22 +52,16 @@ __device__ inline void normalise(float (&v)[V][8], const BlockNormOf &n, int col
     }
     float square = row_sum<G>(q, red) * inv + n.eps;
     if (!norm_in_range(square)) {  // (the same for all threads of the row)
-        float top = 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                top = fmaxf(top, fabsf(v[i][j]));
-        const float shrink = norm_shrink(row_max<G>(top, red), n.eps);
+        const float step = norm_step(square);
         q = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                v[i][j] *= shrink;
+                v[i][j] *= step;
                 q = fmaf(v[i][j], v[i][j], q);
             }
-        square = row_sum<G>(q, red) * inv + n.eps * shrink * shrink;
+        square = row_sum<G>(q, red) * inv + n.eps * step * step;
     }
     const float f = rsqrtf(square);
 #pragma unroll

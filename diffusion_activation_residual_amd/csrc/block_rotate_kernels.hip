@@ -108,17 +108,14 @@ __global__ __launch_bounds__(kThreads) void rotate_kernel(RotateArgs a)
             for (int i = 0; i < kRotateUnits; ++i) {
                 if (norm_in_range(square[i]))
                     continue;
-                float top = 0.0f, q = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    top = fmaxf(top, fabsf(v[i][j]));
-                const float shrink = norm_shrink(lanes_max(top, lanes), a.eps);
+                const float step = norm_step(square[i]);
+                float q = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    v[i][j] *= shrink;
+                    v[i][j] *= step;
                     q = fmaf(v[i][j], v[i][j], q);
                 }
-                square[i] = lanes_sum(q, lanes) * inv + a.eps * shrink * shrink;
+                square[i] = lanes_sum(q, lanes) * inv + a.eps * step * step;
             }
         }
 #pragma unroll

@@ -93,7 +93,8 @@ __device__ inline void normalise(float (&v)[V][8], const BlockNormOf &n, int col
 // gate, scale and shift in 27.1 us (135 MB, 5.0 TB/s); 12,393 rows of 4096 between an fp32 stream and fp16 with a norm on
 // either side in 115 us (609 MB, 5.3 TB/s).  Few values a thread and short work-groups keep more rows under way
 // than a wave a row did (30.9 and 143 us with 4 and 8 vectors a lane), and narrow rows share a wave (131,072 rows of
-// 256: 41.5 us, 65 with half of the lanes idle).  32 rows of 1024: 3.7 us.
+// 256: 49.7 us, 5.4 TB/s, of 32 items 51.7 us and of 4096 items 59.5, as the rows of a wave look up their items one
+// after the other; 524,288 rows of 64: 49.5, 64.7 and 100 us).  32 rows of 1024: 3.7 us.
 template <class X, class Y, int V, int G>
 __global__ __launch_bounds__(group_threads(G)) void residual_norm_kernel(ResidualArgs a)
 {

@@ -49,7 +49,8 @@ __global__ __launch_bounds__(kThreads) void kv8_free_kernel(Kv8Pages p, const in
 }
 
 // A thread a place of a child.  Which pairs count is decided by all of them, so that the order in
-// which the work-groups run changes nothing: a child is written by one pair and is nobody's parent.
+// which the work-groups run changes nothing: a child is written by one pair and is nobody's parent.  Every
+// work-group looks through the whole list: 5 us for 1024 pairs, 15 for 4096, 0.53 ms for 32,000.
 __global__ __launch_bounds__(kThreads) void kv8_fork_kernel(Kv8Pages p, int count,
                                                             const int32_t *parents,
                                                             const int32_t *children, int chunks)
@@ -84,8 +85,9 @@ __global__ __launch_bounds__(kThreads) void kv8_fork_kernel(Kv8Pages p, int coun
 // One work-group: which places need a page is a matter of a few thousand integers and of steps that
 // wait for each other, which costs less in one launch than spread over the card and several.  The
 // free pages are looked for from the front, kScan pages at a time, until there are enough.  96 rows, one token
-// each, 32 of them forked: 8.7 us, most of it reads that wait for each other (length, table, count,
-// holders); a scan step of 64 KB more for every 16,384 pages in use before the free ones.
+// each, 32 of them forked: 9.3 us, most of it reads that wait for each other (length, table, count,
+// holders); a scan step of 64 KB more for every 16,384 pages in use before the free ones, and 4 us for every 1024
+// places (65,535 rows, a token each: 0.29 ms; 4096 rows of 4096 tokens: 1.05 ms).
 constexpr int kWide = 1024, kWaves = kWide / 64, kPieces = 16, kScan = kWide * kPieces;
 
 __global__ __launch_bounds__(kWide) void kv8_reserve_kernel(Kv8Pages p, Kv8Reserve r)

